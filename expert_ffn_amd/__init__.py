@@ -13,3 +13,7 @@ from .ops import (  # noqa: F401
     expert_perslot, fit_times, kernels_per_call, pack_tiled, pack_w_down, route_group, router_topk, step_time_model,
     tree_select,
 )
+from .grouped import (  # noqa: F401
+    Fp8Layer, Quantized, dequant_rows, expert_grouped, group_slots, group_workspace, grouped_down, grouped_gate_up,
+    quant_rows, quant_weights,
+)

@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SO_PATH = os.path.join(HERE, "libmoe_expert.so")
 
 MOE_OK, MOE_E_INVAL, MOE_E_DTYPE, MOE_E_WORKSPACE, MOE_E_HIP, MOE_E_IDS = 0, -1, -2, -3, -4, -5
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_FP8 = 0, 1, 2
 MOE_KIND_SLOT, MOE_KIND_DEDUP = 0, 1
 MOE_MAX_SLOTS, MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_SHARED = 256, 64, 1024, 16
 MOE_FLAG_ACCUMULATE = 1
@@ -20,6 +20,7 @@ MOE_FLAG_TILED = 4
 MOE_MAT_GATE_UP, MOE_MAT_DOWN = 0, 1
 MOE_STEP_NMAX, MOE_STEP_AMAX = 16, 64
 MOE_SCRATCH_BYTES = 16 << 20
+MOE_MAX_GROUP_SLOTS, MOE_MAX_GROUP_WIDTH = 1 << 22, 1 << 16
 
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_E_INVAL", -2: "MOE_E_DTYPE", -3: "MOE_E_WORKSPACE",
                 -4: "MOE_E_HIP", -5: "MOE_E_IDS"}
@@ -29,7 +30,11 @@ EXPORTS = ("moe_route_group", "moe_workspace_bytes", "moe_expert_perslot", "moe_
            "moe_kernels_per_call", "moe_expert_perslot_ev", "moe_expert_dedup_ev", "bytes_requested",
            "step_time_model", "moe_pack_w_down", "moe_fit_times", "moe_error_bounds",
            "moe_router_topk", "moe_router_workspace_bytes", "moe_tree_select",
-           "moe_expert_auto", "moe_pack_tiled", "moe_expert_auto_noalloc")
+           "moe_expert_auto", "moe_pack_tiled", "moe_expert_auto_noalloc",
+           "moe_group_workspace_bytes", "moe_group_slots", "moe_quant_rows", "moe_dequant_rows",
+           "moe_quant_weights", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
+           "moe_grouped_gate_up_fp8", "moe_grouped_down", "moe_grouped_down_fp8", "moe_expert_grouped",
+           "moe_expert_grouped_fp8")
 
 
 class MoeError(RuntimeError):
@@ -48,6 +53,11 @@ class LayerWeights(ctypes.Structure):
     _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("w_gate_shared", ctypes.c_void_p), ("w_up_shared", ctypes.c_void_p),
                 ("w_down_shared", ctypes.c_void_p)]
+
+
+class Fp8Weights(ctypes.Structure):
+    _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
 
 
 MOE_TREE_MAXV, MOE_TREE_MAXK, MOE_TREE_MAXW = 63, 16, 16
@@ -137,6 +147,25 @@ def lib():
             L.moe_expert_auto.restype = ctypes.c_int
             L.moe_expert_auto_noalloc.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, i32, vp, vp]
             L.moe_expert_auto_noalloc.restype = ctypes.c_int
+            pw8 = ctypes.POINTER(Fp8Weights)
+            L.moe_group_workspace_bytes.argtypes = [i32, i32, i32]
+            L.moe_group_workspace_bytes.restype = sz
+            L.moe_group_slots.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_quant_rows.argtypes = [vp, i64, i32, vp, vp, vp]
+            L.moe_dequant_rows.argtypes = [vp, vp, i64, i32, vp, vp]
+            L.moe_quant_weights.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+            L.moe_grouped_workspace_bytes.argtypes = [pdesc, i32]
+            L.moe_grouped_workspace_bytes.restype = sz
+            L.moe_grouped_gate_up.argtypes = [pdesc, pw, vp, i32, vp, vp, vp, vp]
+            L.moe_grouped_gate_up_fp8.argtypes = [pdesc, pw8, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_grouped_down.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+            L.moe_grouped_down_fp8.argtypes = [pdesc, pw8, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+            L.moe_expert_grouped.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+            L.moe_expert_grouped_fp8.argtypes = [pdesc, pw8, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+            for f in (L.moe_group_slots, L.moe_quant_rows, L.moe_dequant_rows, L.moe_quant_weights,
+                      L.moe_grouped_gate_up, L.moe_grouped_gate_up_fp8, L.moe_grouped_down, L.moe_grouped_down_fp8,
+                      L.moe_expert_grouped, L.moe_expert_grouped_fp8):
+                f.restype = ctypes.c_int
             _LIB = L
     return _LIB
 

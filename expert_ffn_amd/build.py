@@ -47,7 +47,8 @@ def build(verbose=False, jobs=None):
     """Compile every translation unit (in parallel, `jobs` at a time; default: the
     CPU count, at most 8) and link the shared library."""
     os.makedirs(BUILD, exist_ok=True)
-    hip = [(os.path.join(CSRC, "moe_expert.hip"), os.path.join(BUILD, "moe_expert.o"), [])] + _variant_objects()
+    hip = [(os.path.join(CSRC, n + ".hip"), os.path.join(BUILD, n + ".o"), []) for n in ("moe_expert", "grouped")]
+    hip += _variant_objects()
     cmds = [[HIPCC, "--offload-arch=" + ARCH, *COMMON, *DEVICE_FLAGS, *defs, "-c", src, "-o", obj]
             for src, obj, defs in hip]
     o2 = os.path.join(BUILD, "host_model.o")

@@ -1,0 +1,341 @@
+// C ABI of the expert operation on grouped rows (include/moe_expert.h): argument checks,
+// workspaces and launches of the kernels in grouped_kernel.h.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "grouped_kernel.h"
+#include "moe_expert.h"
+
+namespace {
+
+using namespace moe_g;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+hipStream_t stream_of(void* s) { return reinterpret_cast<hipStream_t>(s); }
+int launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP; }
+int64_t blocks_of(int64_t v) { return (v + kBlk - 1) / kBlk; }
+
+int check_slots(int32_t n, int32_t m, int32_t N) {
+    if (N < 1 || N > MOE_MAX_EXPERTS || m < 1 || m > N || m > MOE_MAX_SLOTS || n < 1 ||
+        (int64_t)n * m > MOE_MAX_GROUP_SLOTS)
+        return MOE_E_INVAL;
+    return MOE_OK;
+}
+
+// The descriptor of a grouped product of `dtype` weights.
+int check_desc(const moe_layer_desc* d, int32_t n, int32_t dtype) {
+    if (!d) return MOE_E_INVAL;
+    if (d->dtype != dtype) return MOE_E_DTYPE;
+    const int per = dtype == MOE_FP8 ? 16 : 8;  // whole 16-byte pieces of a row
+    if (d->d_model < per || d->d_ff < per || d->d_model % per || d->d_ff % per) return MOE_E_DTYPE;
+    const int rc = check_slots(n, d->m, d->N);
+    if (rc != MOE_OK) return rc;
+    if (d->flags & ~(MOE_FLAG_ACCUMULATE | MOE_FLAG_TILED)) return MOE_E_INVAL;
+    if (d->n_shared != 0) return MOE_E_INVAL;
+    const int64_t es = dtype == MOE_FP8 ? 1 : 2;
+    if ((d->flags & MOE_FLAG_TILED) && (d->d_model % (64 / es) || d->d_ff % (64 / es))) return MOE_E_INVAL;
+    if (d->d_model > MOE_MAX_GROUP_WIDTH || d->d_ff > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    return MOE_OK;
+}
+
+// Grouping workspace: [chunks][N + 1] counts
+int group_chunks(int64_t S) { return (int)((S + group_chunk(S) - 1) / group_chunk(S)); }
+size_t group_ws(int64_t S, int N) { return align_up((size_t)group_chunks(S) * (N + 1) * 4); }
+
+void run_group(const int32_t* ids, int64_t S, int m, int N, int32_t* count, int32_t* offset, int32_t* sbe,
+               int32_t* distinct, int32_t* u_err, void* ws, hipStream_t st) {
+    int32_t* hist = reinterpret_cast<int32_t*>(ws);
+    const int G = group_chunks(S);
+    hipLaunchKernelGGL(k_group_hist, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist);
+    hipLaunchKernelGGL(k_group_scatter, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist, count, offset, sbe,
+                       distinct, u_err);
+}
+
+int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
+    return (int)std::min<int64_t>((rows * blocks_of(K) + 15) / 16, 16384);
+}
+
+// Workspace of a whole pass, and of the products alone (which use hf and O).
+struct Space {
+    size_t hist, count, offset, sbe, distinct, u_err, xq, xs, h, hs, hf, o, total;
+};
+
+Space space_of(const moe_layer_desc* d, int32_t n) {
+    const size_t S = (size_t)n * d->m;
+    const bool fp8 = d->dtype == MOE_FP8;
+    Space p;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t a = at;
+        at += align_up(bytes);
+        return a;
+    };
+    p.o = take(S * d->d_model * 4);
+    p.hf = take(fp8 ? S * d->d_ff * 4 : 0);
+    p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
+    p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
+    p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
+    p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : 0);
+    p.hist = take(group_ws(S, d->N));
+    p.count = take((size_t)d->N * 4);
+    p.offset = take((size_t)(d->N + 1) * 4);
+    p.sbe = take(S * 4);
+    p.distinct = take((size_t)d->N * 4);
+    p.u_err = take(8);
+    p.total = at;
+    return p;
+}
+
+template <bool FP8, bool GU>
+void launch_product(const Args& a, bool tiled, hipStream_t st) {
+    const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
+    const int grid = (int)(tiles * ((a.R + 15) / 16));
+    if (tiled)
+        hipLaunchKernelGGL((k_thin<FP8, true, GU>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_thin<FP8, false, GU>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+}
+
+struct Weights {
+    const void *w0, *w1;
+    const uint8_t *s0, *s1;
+};
+
+template <bool FP8>
+void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const uint8_t* xs, int32_t n,
+                 const int32_t* offset, const int32_t* sbe, void* h, uint8_t* hs, void* hf, hipStream_t st) {
+    Args a{};
+    a.x = reinterpret_cast<const char*>(x);
+    a.xs = xs;
+    a.w0 = reinterpret_cast<const char*>(w.w0);
+    a.w1 = reinterpret_cast<const char*>(w.w1);
+    a.s0 = w.s0;
+    a.s1 = w.s1;
+    a.offset = offset;
+    a.slot = sbe;
+    a.out = reinterpret_cast<char*>(FP8 ? hf : h);
+    a.outs = hs;
+    a.N = d->N;
+    a.m = d->m;
+    a.S = n * d->m;
+    a.R = d->d_ff;
+    a.K = d->d_model;
+    launch_product<FP8, true>(a, d->flags & MOE_FLAG_TILED, st);
+    if (FP8)
+        hipLaunchKernelGGL(k_quant_rows<true>, dim3(rows_grid(a.S, a.R)), dim3(256), 0, st,
+                           reinterpret_cast<const char*>(hf), (int64_t)a.S, a.R, offset + d->N,
+                           reinterpret_cast<uint8_t*>(h), hs);
+}
+
+template <bool FP8>
+void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
+              const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, void* y, void* o,
+              const int32_t* u_err, int32_t* info, hipStream_t st) {
+    Args a{};
+    a.x = reinterpret_cast<const char*>(h);
+    a.xs = hs;
+    a.w0 = reinterpret_cast<const char*>(w.w0);
+    a.s0 = w.s0;
+    a.offset = offset;
+    a.slot = sbe;
+    a.out = reinterpret_cast<char*>(o);
+    a.N = d->N;
+    a.m = d->m;
+    a.S = n * d->m;
+    a.R = d->d_model;
+    a.K = d->d_ff;
+    launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
+    const int64_t work = (int64_t)n * (d->d_model / 4);
+    hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 255) / 256, 16384)), dim3(256), 0, st,
+                       reinterpret_cast<const float*>(o), ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
+}
+
+template <bool FP8>
+int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, const void* x, const int32_t* ids,
+             const float* w, int32_t n, void* y, int32_t* info, void* ws, hipStream_t st) {
+    const Space p = space_of(d, n);
+    char* b = reinterpret_cast<char*>(ws);
+    auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(b + at); };
+    auto u8 = [&](size_t at) { return reinterpret_cast<uint8_t*>(b + at); };
+    (void)hipGetLastError();
+    run_group(ids, (int64_t)n * d->m, d->m, d->N, i32(p.count), i32(p.offset), i32(p.sbe), i32(p.distinct),
+              i32(p.u_err), b + p.hist, st);
+    if (FP8)
+        hipLaunchKernelGGL(k_quant_rows<false>, dim3(rows_grid(n, d->d_model)), dim3(256), 0, st,
+                           reinterpret_cast<const char*>(x), (int64_t)n, d->d_model,
+                           static_cast<const int32_t*>(nullptr), u8(p.xq), u8(p.xs));
+    run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
+                     b + p.h, u8(p.hs), b + p.hf, st);
+    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), y, b + p.o, i32(p.u_err), info, st);
+    return launched();
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+    if (!ws || !aligned(ws, kAlign)) return MOE_E_INVAL;
+    return have < need ? MOE_E_WORKSPACE : MOE_OK;
+}
+
+bool fp8_ok(const void* w, const uint8_t* s) { return w && aligned(w, 16) && s; }
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_group_workspace_bytes(int32_t n, int32_t m, int32_t N) {
+    if (check_slots(n, m, N) != MOE_OK) return 0;
+    return align_up((size_t)kGMaxChunks * (N + 1) * 4);
+}
+
+int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t* count, int32_t* offset,
+                    int32_t* slot_by_expert, int32_t* distinct, int32_t* u_and_err, void* ws, size_t ws_bytes,
+                    void* hip_stream) {
+    if (!ids || !count || !offset || !slot_by_expert || !distinct || !u_and_err) return MOE_E_INVAL;
+    int rc = check_slots(n, m, N);
+    if (rc != MOE_OK) return rc;
+    rc = check_ws(ws, ws_bytes, group_ws((int64_t)n * m, N));
+    if (rc != MOE_OK) return rc;
+    (void)hipGetLastError();
+    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, ws, stream_of(hip_stream));
+    return launched();
+}
+
+size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
+    if (!desc || (desc->dtype != MOE_BF16 && desc->dtype != MOE_FP8)) return 0;
+    if (check_desc(desc, n, desc->dtype) != MOE_OK) return 0;
+    return space_of(desc, n).total;
+}
+
+int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, int32_t n,
+                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* hip_stream) {
+    const int rc = check_desc(desc, n, MOE_BF16);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !weights->w_gate || !weights->w_up || !x || !offset || !slot_by_expert || !h) return MOE_E_INVAL;
+    if (!aligned(weights->w_gate, 16) || !aligned(weights->w_up, 16) || !aligned(x, 16) || !aligned(h, 16))
+        return MOE_E_INVAL;
+    (void)hipGetLastError();
+    run_gate_up<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr}, x, nullptr, n, offset,
+                       slot_by_expert, h, nullptr, nullptr, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* xq,
+                            const uint8_t* x_scale, int32_t n, const int32_t* offset, const int32_t* slot_by_expert,
+                            void* hq, uint8_t* h_scale, void* ws, size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_FP8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !fp8_ok(weights->w_gate, weights->s_gate) || !fp8_ok(weights->w_up, weights->s_up) ||
+        !fp8_ok(xq, x_scale) || !fp8_ok(hq, h_scale) || !offset || !slot_by_expert)
+        return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    (void)hipGetLastError();
+    run_gate_up<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up}, xq, x_scale, n,
+                      offset, slot_by_expert, hq, h_scale, reinterpret_cast<char*>(ws) + p.hf, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* h, const int32_t* ids,
+                     const float* w, int32_t n, const int32_t* offset, const int32_t* slot_by_expert, void* y, void* ws,
+                     size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_BF16);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !weights->w_down || !h || !ids || !w || !offset || !slot_by_expert || !y) return MOE_E_INVAL;
+    if (!aligned(weights->w_down, 16) || !aligned(h, 16) || !aligned(y, 16)) return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    (void)hipGetLastError();
+    run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
+                    slot_by_expert, y, reinterpret_cast<char*>(ws) + p.o, nullptr, nullptr, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* hq,
+                         const uint8_t* h_scale, const int32_t* ids, const float* w, int32_t n, const int32_t* offset,
+                         const int32_t* slot_by_expert, void* y, void* ws, size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_FP8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !fp8_ok(weights->w_down, weights->s_down) || !fp8_ok(hq, h_scale) || !ids || !w || !offset ||
+        !slot_by_expert || !y || !aligned(y, 16))
+        return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    (void)hipGetLastError();
+    run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
+                   slot_by_expert, y, reinterpret_cast<char*>(ws) + p.o, nullptr, nullptr, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_expert_grouped(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, const int32_t* ids,
+                       const float* w, int32_t n, void* y, int32_t* info, void* ws, size_t ws_bytes,
+                       void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_BF16);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !weights->w_gate || !weights->w_up || !weights->w_down || !x || !ids || !w || !y)
+        return MOE_E_INVAL;
+    if (!aligned(weights->w_gate, 16) || !aligned(weights->w_up, 16) || !aligned(weights->w_down, 16) ||
+        !aligned(x, 16) || !aligned(y, 16))
+        return MOE_E_INVAL;
+    rc = check_ws(ws, ws_bytes, space_of(desc, n).total);
+    if (rc != MOE_OK) return rc;
+    return run_pass<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr},
+                           Weights{weights->w_down, nullptr, nullptr, nullptr}, x, ids, w, n, y, info, ws,
+                           stream_of(hip_stream));
+}
+
+int moe_expert_grouped_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* x,
+                           const int32_t* ids, const float* w, int32_t n, void* y, int32_t* info, void* ws,
+                           size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_FP8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !fp8_ok(weights->w_gate, weights->s_gate) || !fp8_ok(weights->w_up, weights->s_up) ||
+        !fp8_ok(weights->w_down, weights->s_down) || !x || !aligned(x, 16) || !ids || !w || !y || !aligned(y, 16))
+        return MOE_E_INVAL;
+    rc = check_ws(ws, ws_bytes, space_of(desc, n).total);
+    if (rc != MOE_OK) return rc;
+    return run_pass<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up},
+                          Weights{weights->w_down, nullptr, weights->s_down, nullptr}, x, ids, w, n, y, info, ws,
+                          stream_of(hip_stream));
+}
+
+int moe_quant_rows(const void* x, int64_t rows, int32_t K, void* q, uint8_t* scale, void* hip_stream) {
+    if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16)) return MOE_E_INVAL;
+    if (K < 16 || K % 16) return MOE_E_DTYPE;
+    if (rows < 1 || rows > MOE_MAX_GROUP_SLOTS || K > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(k_quant_rows<false>, dim3(rows_grid(rows, K)), dim3(256), 0, stream_of(hip_stream),
+                       reinterpret_cast<const char*>(x), rows, K, static_cast<const int32_t*>(nullptr),
+                       reinterpret_cast<uint8_t*>(q), scale);
+    return launched();
+}
+
+int moe_dequant_rows(const void* q, const uint8_t* scale, int64_t rows, int32_t K, void* x, void* hip_stream) {
+    if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16)) return MOE_E_INVAL;
+    if (K < 16 || K % 16) return MOE_E_DTYPE;
+    if (rows < 1 || rows > MOE_MAX_GROUP_SLOTS || K > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(k_dequant_rows, dim3(rows_grid(rows, K)), dim3(256), 0, stream_of(hip_stream),
+                       reinterpret_cast<const uint8_t*>(q), scale, rows, K, reinterpret_cast<char*>(x));
+    return launched();
+}
+
+int moe_quant_weights(const void* w, int32_t N, int32_t R, int32_t K, void* q, uint8_t* scale, void* hip_stream) {
+    if (!w || !q || !scale || !aligned(w, 16) || !aligned(q, 16)) return MOE_E_INVAL;
+    if (R < 16 || K < 16 || R % 16 || K % 16) return MOE_E_DTYPE;
+    if (N < 1 || N > MOE_MAX_EXPERTS || R > MOE_MAX_GROUP_WIDTH || K > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    const int64_t grid = (int64_t)N * blocks_of(R) * blocks_of(K);
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(k_quant_weights, dim3((unsigned)grid), dim3(256), 0, stream_of(hip_stream),
+                       reinterpret_cast<const char*>(w), R, K, reinterpret_cast<uint8_t*>(q), scale);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,342 @@
+"""The expert operation on grouped rows: passes of any length, in bf16 or with 8-bit
+weights (argument marshalling of the grouped calls of ``include/moe_expert.h``).
+
+Every call runs on ``stream`` (default: the current stream of its tensors' device), with
+that device current.  Outputs and workspaces that are not given are allocated for that
+stream.
+"""
+import contextlib
+import ctypes
+from collections import namedtuple
+
+import torch
+
+from . import _abi
+from ._abi import check, lib
+from .ops import Grouping, Layer, _check_dev
+
+# e4m3 codes [rows][K] and their scale bytes [rows][ceil(K/128)]: code * 2^(byte - 127)
+Quantized = namedtuple("Quantized", ["q", "scale"])
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _blocks(v):
+    return -(-v // 128)
+
+
+def _guard(dev):
+    return _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _on(dev, stream):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):  # memory of the stream that the call runs on
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _same(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+
+
+def _ws(ws, nbytes, where, dev, stream):
+    if nbytes == 0:
+        raise _abi.MoeError(where, _abi.MOE_E_INVAL)
+    if ws is None:
+        return _empty(nbytes, torch.uint8, dev, stream)
+    _check_dev("ws", ws, torch.uint8)
+    _same(dev, ws=ws)
+    return ws
+
+
+def _check_quantized(name, v, rows, K):
+    if not isinstance(v, Quantized):
+        raise TypeError("%s must be Quantized (codes and scale bytes), got %s" % (name, type(v).__name__))
+    _check_dev(name + ".q", v.q, torch.float8_e4m3fn, (rows, K))
+    _check_dev(name + ".scale", v.scale, torch.uint8, (rows, _blocks(K)))
+
+
+class Fp8Layer:
+    """8-bit weights of one MoE layer: each matrix a pair (codes float8_e4m3fn, scale
+    bytes uint8), W_gate and W_up [N][d_ff][d] with [N][d_ff/128][d/128] scales, W_down
+    [N][d][d_ff] with [N][d/128][d_ff/128] (sizes rounded up), as ``Layer.fp8_copy``
+    makes them; with ``tiled`` the codes are in the layout of ``moe_pack_tiled``."""
+
+    def __init__(self, gate, up, down, m, tiled=False):
+        for name, pair in (("gate", gate), ("up", up), ("down", down)):
+            if len(pair) != 2:
+                raise ValueError("%s must be (codes, scale bytes)" % name)
+        N, d_ff, d = gate[0].shape
+        self.N, self.m, self.d, self.d_ff = N, int(m), d, d_ff
+        self.tiled = bool(tiled)
+        for name, (q, s), (R, K) in (("gate", gate, (d_ff, d)), ("up", up, (d_ff, d)), ("down", down, (d, d_ff))):
+            _check_dev("w_" + name, q, torch.float8_e4m3fn, (N, R, K))
+            _check_dev("s_" + name, s, torch.uint8, (N, _blocks(R), _blocks(K)))
+            _same(gate[0].device, **{"w_" + name: q, "s_" + name: s})
+        self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
+        self._weights = _abi.Fp8Weights(*(m_[i].data_ptr() for i in (0, 1) for m_ in (self.gate, self.up, self.down)))
+
+    @property
+    def device(self):
+        return self.gate[0].device
+
+    @property
+    def expert_bytes(self):
+        return 3 * self.d * self.d_ff + sum(p[1][0].numel() for p in (self.gate, self.up, self.down))
+
+    def desc(self, accumulate=False):
+        flags = (_abi.MOE_FLAG_ACCUMULATE if accumulate else 0) | (_abi.MOE_FLAG_TILED if self.tiled else 0)
+        return _abi.LayerDesc(self.N, self.m, self.d, self.d_ff, _abi.MOE_FP8, flags, 0)
+
+    def tiled_copy(self, stream=None):
+        """The same layer with the codes copied into the tiled layout by
+        ``moe_pack_tiled`` (scales shared)."""
+        if self.tiled:
+            return self
+        desc, dev = self.desc(), self.device
+
+        def tl(pair, mat):
+            out = _empty(pair[0].shape, torch.float8_e4m3fn, dev, stream)
+            with _guard(dev):
+                check("moe_pack_tiled", lib().moe_pack_tiled(ctypes.byref(desc), pair[0].data_ptr(), out.data_ptr(),
+                                                             mat, _on(dev, stream)))
+            return out, pair[1]
+        G, D = _abi.MOE_MAT_GATE_UP, _abi.MOE_MAT_DOWN
+        return Fp8Layer(tl(self.gate, G), tl(self.up, G), tl(self.down, D), self.m, tiled=True)
+
+    def grouped_workspace(self, n):
+        """Workspace of the grouped calls on this layer for passes of up to n tokens."""
+        return grouped_workspace(self, n)
+
+
+def quant_weights(w, stream=None):
+    """bf16 matrices [N][R][K] to (codes, scale bytes [N][R/128][K/128]), one power of
+    two for each block of 128 x 128 (``moe_quant_weights``)."""
+    _check_dev("w", w, torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError("w must be [N][R][K], got %s" % (tuple(w.shape),))
+    N, R, K = w.shape
+    dev = w.device
+    q = _empty((N, R, K), torch.float8_e4m3fn, dev, stream)
+    s = _empty((N, _blocks(R), _blocks(K)), torch.uint8, dev, stream)
+    with _guard(dev):
+        check("moe_quant_weights", lib().moe_quant_weights(w.data_ptr(), N, R, K, q.data_ptr(), s.data_ptr(),
+                                                           _on(dev, stream)))
+    return q, s
+
+
+def fp8_copy(layer, stream=None):
+    """``layer`` (plain bf16 weights) with 8-bit weights in plain layout."""
+    if layer.dtype != torch.bfloat16 or layer.packed or layer.tiled:
+        raise ValueError("fp8_copy takes plain bf16 weights (tile the copy)")
+    if layer.shared is not None:
+        raise ValueError("copy the routed and the shared experts as layers of their own (without_shared)")
+    return Fp8Layer(*(quant_weights(w, stream) for w in (layer.w_gate, layer.w_up, layer.w_down)), m=layer.m)
+
+
+def quant_rows(x, out=None, stream=None):
+    """Rows of bf16 values [rows][K] to ``Quantized``, one power of two for each block of
+    128 along a row (``moe_quant_rows``)."""
+    _check_dev("x", x, torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][K], got %s" % (tuple(x.shape),))
+    rows, K = x.shape
+    dev = x.device
+    if out is None:
+        out = Quantized(_empty((rows, K), torch.float8_e4m3fn, dev, stream),
+                        _empty((rows, _blocks(K)), torch.uint8, dev, stream))
+    else:
+        _check_quantized("out", out, rows, K)
+        _same(dev, q=out.q, scale=out.scale)
+    with _guard(dev):
+        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, K, out.q.data_ptr(), out.scale.data_ptr(),
+                                                     _on(dev, stream)))
+    return out
+
+
+def dequant_rows(v, out=None, stream=None):
+    """The bf16 values that ``Quantized`` rows stand for (``moe_dequant_rows``)."""
+    if not isinstance(v, Quantized) or v.q.dim() != 2:
+        raise TypeError("dequant_rows takes Quantized rows")
+    rows, K = v.q.shape
+    _check_quantized("v", v, rows, K)
+    dev = v.q.device
+    _same(dev, scale=v.scale)
+    if out is None:
+        out = _empty((rows, K), torch.bfloat16, dev, stream)
+    else:
+        _check_dev("out", out, torch.bfloat16, (rows, K))
+        _same(dev, out=out)
+    with _guard(dev):
+        check("moe_dequant_rows", lib().moe_dequant_rows(v.q.data_ptr(), v.scale.data_ptr(), rows, K, out.data_ptr(),
+                                                         _on(dev, stream)))
+    return out
+
+
+def group_workspace(n, m, N, device="cuda"):
+    """Workspace of ``group_slots`` for n tokens of m slots and N experts."""
+    nb = lib().moe_group_workspace_bytes(int(n), int(m), int(N))
+    if nb == 0:
+        raise _abi.MoeError("moe_group_workspace_bytes", _abi.MOE_E_INVAL)
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def group_slots(ids, N, out=None, ws=None, stream=None):
+    """``route_group`` for any number of slots (``moe_group_slots``): ids int32 [n][m];
+    ids outside [0, N) take no part."""
+    _check_dev("ids", ids, torch.int32)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [n][m], got %s" % (tuple(ids.shape),))
+    n, m = ids.shape
+    dev = ids.device
+    ws = _ws(ws, lib().moe_group_workspace_bytes(n, m, int(N)), "moe_group_workspace_bytes", dev, stream)
+    sizes = (N, N + 1, n * m, N, 2)
+    if out is None:
+        out = Grouping(*(_empty(k, torch.int32, dev, stream) for k in sizes))
+    else:
+        _check_grouping(out, n, m, N, dev)
+    with _guard(dev):
+        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), n, m, int(N), *(t.data_ptr() for t in out),
+                                                       ws.data_ptr(), ws.numel(), _on(dev, stream)))
+    return out
+
+
+def _check_grouping(g, n, m, N, dev):
+    for name, t, k in zip(Grouping._fields, g, (N, N + 1, n * m, N, 2)):
+        _check_dev(name, t, torch.int32, (k,))
+        _same(dev, **{name: t})
+
+
+def _kind(layer):
+    """(layer has 8-bit weights, its device); refuses what the grouped calls do not take."""
+    if isinstance(layer, Fp8Layer):
+        return True, layer.device
+    if not isinstance(layer, Layer):
+        raise TypeError("layer must be Layer or Fp8Layer, got %s" % type(layer).__name__)
+    if layer.dtype != torch.bfloat16:
+        raise TypeError("grouped calls take bf16 or 8-bit weights, got %s" % layer.dtype)
+    if layer.packed:
+        raise ValueError("grouped calls take plain or tiled weights, not a packed W_down")
+    if layer.n_shared:
+        raise ValueError("run the shared experts as a layer of their own with m = N and accumulate=True "
+                         "(and the routed ones from without_shared())")
+    return False, layer.w_gate.device
+
+
+def grouped_workspace(layer, n):
+    """Workspace of the grouped calls for passes of up to n tokens."""
+    _, dev = _kind(layer)
+    nb = lib().moe_grouped_workspace_bytes(ctypes.byref(layer.desc()), int(n))
+    if nb == 0:
+        raise _abi.MoeError("moe_grouped_workspace_bytes", _abi.MOE_E_INVAL)
+    return torch.empty(nb, dtype=torch.uint8, device=dev)
+
+
+def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
+    """h [n*m][d_ff] in row order (``moe_grouped_gate_up``): bf16 from bf16 x [n][d], or
+    with 8-bit weights ``Quantized`` from ``Quantized`` x (``quant_rows``).  Rows from
+    offset[N] on are left as they were."""
+    fp8, dev = _kind(layer)
+    n = (x.q if isinstance(x, Quantized) else x).shape[0]
+    S, f = n * layer.m, layer.d_ff
+    _check_grouping(grouping, n, layer.m, layer.N, dev)
+    desc, L = layer.desc(), lib()
+    if not fp8:
+        _check_dev("x", x, torch.bfloat16, (n, layer.d))
+        if out is None:
+            out = _empty((S, f), torch.bfloat16, dev, stream)
+        _check_dev("out", out, torch.bfloat16, (S, f))
+        _same(dev, x=x, out=out)
+        with _guard(dev):
+            check("moe_grouped_gate_up", L.moe_grouped_gate_up(
+                ctypes.byref(desc), ctypes.byref(layer._weights), x.data_ptr(), n, grouping.offset.data_ptr(),
+                grouping.slot_by_expert.data_ptr(), out.data_ptr(), _on(dev, stream)))
+        return out
+    _check_quantized("x", x, n, layer.d)
+    if out is None:
+        out = Quantized(_empty((S, f), torch.float8_e4m3fn, dev, stream),
+                        _empty((S, _blocks(f)), torch.uint8, dev, stream))
+    _check_quantized("out", out, S, f)
+    _same(dev, x=x.q, x_scale=x.scale, out=out.q, out_scale=out.scale)
+    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
+    with _guard(dev):
+        check("moe_grouped_gate_up_fp8", L.moe_grouped_gate_up_fp8(
+            ctypes.byref(desc), ctypes.byref(layer._weights), x.q.data_ptr(), x.scale.data_ptr(), n,
+            grouping.offset.data_ptr(), grouping.slot_by_expert.data_ptr(), out.q.data_ptr(), out.scale.data_ptr(),
+            ws.data_ptr(), ws.numel(), _on(dev, stream)))
+    return out
+
+
+def _check_routing(layer, ids, w, n, dev):
+    _check_dev("ids", ids, torch.int32, (n, layer.m))
+    _check_dev("w", w, torch.float32, (n, layer.m))
+    _same(dev, ids=ids, w=w)
+
+
+def _check_y(layer, y, n, dev, accumulate, stream):
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs y")
+        return _empty((n, layer.d), torch.bfloat16, dev, stream)
+    _check_dev("y", y, torch.bfloat16, (n, layer.d))
+    _same(dev, y=y)
+    return y
+
+
+def grouped_down(layer, h, ids, w, grouping, y=None, ws=None, accumulate=False, stream=None):
+    """y [n][d] bf16: the down products of h's rows, summed over each token's slots with
+    the routing weights w (``moe_grouped_down``); ``accumulate`` adds to y."""
+    fp8, dev = _kind(layer)
+    n, m, f = ids.shape[0], layer.m, layer.d_ff
+    _check_routing(layer, ids, w, n, dev)
+    _check_grouping(grouping, n, m, layer.N, dev)
+    y = _check_y(layer, y, n, dev, accumulate, stream)
+    desc, L = layer.desc(accumulate), lib()
+    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
+    tail = (ids.data_ptr(), w.data_ptr(), n, grouping.offset.data_ptr(), grouping.slot_by_expert.data_ptr(),
+            y.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream))
+    with _guard(dev):
+        if fp8:
+            _check_quantized("h", h, n * m, f)
+            _same(dev, h=h.q, h_scale=h.scale)
+            check("moe_grouped_down_fp8", L.moe_grouped_down_fp8(
+                ctypes.byref(desc), ctypes.byref(layer._weights), h.q.data_ptr(), h.scale.data_ptr(), *tail))
+        else:
+            _check_dev("h", h, torch.bfloat16, (n * m, f))
+            _same(dev, h=h)
+            check("moe_grouped_down", L.moe_grouped_down(ctypes.byref(desc), ctypes.byref(layer._weights), h.data_ptr(),
+                                                         *tail))
+    return y
+
+
+def expert_grouped(layer, x, ids, w, y=None, ws=None, info=None, accumulate=False, stream=None):
+    """A whole pass of any length: grouping, gate/up and down (``moe_expert_grouped``, or
+    ``moe_expert_grouped_fp8`` for an ``Fp8Layer``, which quantises x first).  x and y
+    bf16 [n][d]; ids outside [0, N) add nothing; ``info`` int32 [3]: U, ids status, 0."""
+    fp8, dev = _kind(layer)
+    n = x.shape[0]
+    _check_dev("x", x, torch.bfloat16, (n, layer.d))
+    _check_routing(layer, ids, w, n, dev)
+    y = _check_y(layer, y, n, dev, accumulate, stream)
+    if info is not None:
+        _check_dev("info", info, torch.int32, (3,))
+    _same(dev, x=x, info=info)
+    desc, L = layer.desc(accumulate), lib()
+    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
+    name = "moe_expert_grouped_fp8" if fp8 else "moe_expert_grouped"
+    with _guard(dev):
+        check(name, getattr(L, name)(
+            ctypes.byref(desc), ctypes.byref(layer._weights), x.data_ptr(), ids.data_ptr(), w.data_ptr(), n,
+            y.data_ptr(), None if info is None else info.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream)))
+    return y

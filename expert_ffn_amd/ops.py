@@ -135,6 +135,17 @@ class Layer:
             raise _abi.MoeError("moe_workspace_bytes", _abi.MOE_E_INVAL)
         return torch.zeros(nb, dtype=torch.uint8, device=self.w_gate.device)
 
+    def grouped_workspace(self, n):
+        """Workspace of the grouped calls (``expert_grouped`` and its parts) for passes of
+        up to n tokens."""
+        from .grouped import grouped_workspace
+        return grouped_workspace(self, n)
+
+    def fp8_copy(self, stream=None):
+        """The same layer with 8-bit weights (``Fp8Layer``), from plain bf16 weights."""
+        from .grouped import fp8_copy
+        return fp8_copy(self, stream)
+
 
 def pack_w_down(layer, w_down, out, stream=None):
     """Copy W_down [E][d][d_ff] (E experts: the layer's N, or its shared experts) into

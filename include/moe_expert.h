@@ -55,7 +55,9 @@ typedef enum {
     MOE_E_IDS = -5        /* an expert id out of [0, N), or repeated within a token */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+/* MOE_FP8 (e4m3 codes with a power of two for each block of 128): the grouped products
+ * and moe_pack_tiled only; the calls on verification passes return MOE_E_DTYPE */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8 = 2 } moe_dtype;
 
 enum { MOE_KIND_SLOT = 0, MOE_KIND_DEDUP = 1 };
 
@@ -294,6 +296,116 @@ int moe_router_topk(const moe_layer_desc* desc, const void* w_router, const void
 /* Workspace bytes of moe_router_topk for passes of up to n tokens (the largest over
  * 1..n), or 0 for invalid arguments. */
 size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
+
+/* ---------------------------------------------------------------------------
+ * The expert operation on grouped rows: the same layers on passes of any length (a
+ * prompt, a padded batch, one token), in bf16 or with 8-bit weights and activations.
+ * The calls above stop at MOE_MAX_TOKENS tokens and MOE_MAX_SLOTS slots and read the
+ * weights once per slot or expert; these form, for every expert, matrix products over
+ * all of its tokens.
+ *
+ * Rows: the n*m slots s = t*m + j sorted stably by expert; row r holds slot
+ * slot_by_expert[r], and expert e owns rows offset[e] .. offset[e+1].  The slots whose
+ * id is outside [0, N) (padding: -1) hold no row; their routing weights are not read,
+ * and rows from offset[N] on are neither read nor written.
+ *   gate/up   h_r = round( silu(W_gate[e] x_t) * (W_up[e] x_t) )
+ *   down      y_t = round( sum_j w_tj W_down[e_tj] h_row(t,j) ), j increasing; a token
+ *             without a valid id gets zeros
+ * y is bf16 (these passes feed the next layer), every sum is fp32; round is to bf16, or,
+ * for h with 8-bit weights, the quantisation below.  Results are deterministic.
+ *
+ * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=
+ * MOE_MAX_GROUP_SLOTS, d_model and d_ff <= MOE_MAX_GROUP_WIDTH, multiples of 8 (bf16)
+ * or 16 (MOE_FP8).  Descriptor flags: MOE_FLAG_TILED (whole 64-byte steps) and
+ * MOE_FLAG_ACCUMULATE (y = round(y + sum)); n_shared must be 0: always-on experts run
+ * as a layer of their own with m = N, every weight 1 and MOE_FLAG_ACCUMULATE.  fp32
+ * layers get MOE_E_DTYPE.  Matrices, x, h, q and y are 16-byte aligned, other arrays aligned to their
+ * elements; outputs overlap no input.  The current device is the stream's and the
+ * arrays' device.
+ * ------------------------------------------------------------------------- */
+#define MOE_MAX_GROUP_SLOTS (1 << 22)
+#define MOE_MAX_GROUP_WIDTH (1 << 16)
+
+/*
+ * moe_group_slots -- the grouping of moe_route_group for any number of slots: the same
+ * outputs, bit for bit (count [N], offset [N+1], slot_by_expert [n*m], distinct [N],
+ * u_and_err [2]), from the same ids.  Two launches, deterministic.
+ *   ws   device workspace, ws_bytes >= moe_group_workspace_bytes(n, m, N), 256-byte
+ *        aligned; no zero-fill needed, nothing kept between calls
+ * Returns MOE_OK, MOE_E_INVAL, MOE_E_WORKSPACE (nothing enqueued) or MOE_E_HIP.
+ */
+size_t moe_group_workspace_bytes(int32_t n, int32_t m, int32_t N);
+int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t* count, int32_t* offset,
+                    int32_t* slot_by_expert, int32_t* distinct, int32_t* u_and_err, void* ws, size_t ws_bytes,
+                    void* hip_stream);
+
+/*
+ * 8-bit values.  A block of 128 values shares a power of two: k is the smallest integer
+ * >= -127 with max|v| <= 448 * 2^k (448 is the largest e4m3 value), the code is
+ * e4m3(v * 2^-k) rounded to nearest even, and stands for code * 2^k.  Codes are OCP e4m3
+ * (no infinities); the scale is stored as the byte k + 127.  A value that is not finite
+ * takes no part in the maximum and gets the NaN code; a block of zeros has byte 0.  The last
+ * block of a row may be short.
+ *   moe_quant_rows     x bf16 [rows][K] -> q [rows][K], scale [rows][ceil(K/128)]
+ *   moe_dequant_rows   back to bf16 [rows][K] (exact where bf16 holds the value)
+ *   moe_quant_weights  w bf16 [N][R][K] -> q [N][R][K], scale [N][ceil(R/128)][ceil(K/128)],
+ *                      blocks of 128 x 128 (a weight-load-time step)
+ * K (and R) are multiples of 16, at most MOE_MAX_GROUP_WIDTH, else MOE_E_DTYPE /
+ * MOE_E_INVAL; 1 <= rows <= MOE_MAX_GROUP_SLOTS.  One launch each.  moe_pack_tiled tiles
+ * codes with desc->dtype MOE_FP8 (steps of 64 elements); scales keep their layout.
+ */
+int moe_quant_rows(const void* x, int64_t rows, int32_t K, void* q, uint8_t* scale, void* hip_stream);
+int moe_dequant_rows(const void* q, const uint8_t* scale, int64_t rows, int32_t K, void* x, void* hip_stream);
+int moe_quant_weights(const void* w, int32_t N, int32_t R, int32_t K, void* q, uint8_t* scale, void* hip_stream);
+
+/* Codes (plain or tiled) and scale bytes of a layer's matrices, as moe_quant_weights
+ * gives them; device, caller-owned. */
+typedef struct {
+    const void* w_gate; /* [N][d_ff][d_model] */
+    const void* w_up;
+    const void* w_down; /* [N][d_model][d_ff] */
+    const uint8_t* s_gate; /* [N][ceil(d_ff/128)][ceil(d_model/128)] */
+    const uint8_t* s_up;
+    const uint8_t* s_down; /* [N][ceil(d_model/128)][ceil(d_ff/128)] */
+} moe_fp8_weights;
+
+/* Workspace bytes of the calls below for n tokens (0 for invalid arguments); it grows
+ * with n, so a workspace for n serves fewer tokens too.  256-byte aligned; no zero-fill
+ * needed, nothing kept between calls; calls that share one must not overlap in time. */
+size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n);
+
+/*
+ * The two products by themselves.  offset and slot_by_expert come from moe_group_slots
+ * (or moe_route_group) for the same n, m and N.  The other product's weights may be NULL.
+ *   x    device [n][d_model] bf16, or codes with x_scale [n][ceil(d_model/128)]
+ *   h    device [n*m][d_ff] bf16, or codes with h_scale [n*m][ceil(d_ff/128)], in row order
+ *   y    device [n][d_model] bf16
+ * Return MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE (nothing enqueued) or
+ * MOE_E_HIP.
+ */
+int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, int32_t n,
+                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* hip_stream);
+int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* xq,
+                            const uint8_t* x_scale, int32_t n, const int32_t* offset, const int32_t* slot_by_expert,
+                            void* hq, uint8_t* h_scale, void* ws, size_t ws_bytes, void* hip_stream);
+int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* h, const int32_t* ids,
+                     const float* w, int32_t n, const int32_t* offset, const int32_t* slot_by_expert, void* y, void* ws,
+                     size_t ws_bytes, void* hip_stream);
+int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* hq,
+                         const uint8_t* h_scale, const int32_t* ids, const float* w, int32_t n, const int32_t* offset,
+                         const int32_t* slot_by_expert, void* y, void* ws, size_t ws_bytes, void* hip_stream);
+
+/*
+ * moe_expert_grouped / moe_expert_grouped_fp8 -- a whole pass: grouping, (x quantised in
+ * blocks of 128,) gate/up, down.  Arguments as for moe_expert_dedup, with x and y bf16
+ * (also with 8-bit weights).  info device [3] int32 or NULL: U, ids status, MOE_OK.
+ */
+int moe_expert_grouped(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, const int32_t* ids,
+                       const float* w, int32_t n, void* y, int32_t* info, void* ws, size_t ws_bytes,
+                       void* hip_stream);
+int moe_expert_grouped_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* x,
+                           const int32_t* ids, const float* w, int32_t n, void* y, int32_t* info, void* ws,
+                           size_t ws_bytes, void* hip_stream);
 
 /* Number of kernel launches moe_expert_perslot / moe_expert_dedup enqueue per
  * call (moe_route_group is a separate, optional launch), or a negative status for
