@@ -75,7 +75,7 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
         at += align_up(bytes);
         return a;
     };
-    p.o = take(S * d->d_model * 4);
+    p.o = take(S * d->d_model * 2);
     p.hf = take(fp8 ? S * d->d_ff * 4 : 0);
     p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
     p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
@@ -91,8 +91,23 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     return p;
 }
 
+// Square tiles from 16 rows an expert on average; their buffer offsets are 31 bits.
+bool square(const Args& a, bool fp8, bool gu) {
+    const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
+    return a.S >= 16 * (int64_t)a.N && a.R * kby <= most && (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
+}
+
 template <bool FP8, bool GU>
 void launch_product(const Args& a, bool tiled, hipStream_t st) {
+    if (square(a, FP8, GU)) {
+        const int64_t tiles = (int64_t)a.S / kTM + std::min(a.N, a.S), tc = GU ? kTN / 2 : kTN;
+        const int grid = (int)((tiles * ((a.R + tc - 1) / tc) + 7) / 8 * 8);
+        if (tiled)
+            hipLaunchKernelGGL((k_tile<FP8, true, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
+        else
+            hipLaunchKernelGGL((k_tile<FP8, false, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
+        return;
+    }
     const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
     const int grid = (int)(tiles * ((a.R + 15) / 16));
     if (tiled)
@@ -118,15 +133,17 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
     a.s1 = w.s1;
     a.offset = offset;
     a.slot = sbe;
-    a.out = reinterpret_cast<char*>(FP8 ? hf : h);
+    a.out = reinterpret_cast<char*>(h);
     a.outs = hs;
     a.N = d->N;
     a.m = d->m;
     a.S = n * d->m;
     a.R = d->d_ff;
     a.K = d->d_model;
+    const bool by16 = FP8 && !square(a, FP8, true);  // thin tiles leave h in fp32
+    if (by16) a.out = reinterpret_cast<char*>(hf);
     launch_product<FP8, true>(a, d->flags & MOE_FLAG_TILED, st);
-    if (FP8)
+    if (by16)
         hipLaunchKernelGGL(k_quant_rows<true>, dim3(rows_grid(a.S, a.R)), dim3(256), 0, st,
                            reinterpret_cast<const char*>(hf), (int64_t)a.S, a.R, offset + d->N,
                            reinterpret_cast<uint8_t*>(h), hs);
@@ -150,9 +167,9 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.R = d->d_model;
     a.K = d->d_ff;
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
-    const int64_t work = (int64_t)n * (d->d_model / 4);
+    const int64_t work = (int64_t)n * (d->d_model / 8);
     hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 255) / 256, 16384)), dim3(256), 0, st,
-                       reinterpret_cast<const float*>(o), ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       reinterpret_cast<const char*>(o), ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 

@@ -23,6 +23,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_expert.h"
 
 namespace moe_g {
@@ -486,36 +488,310 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
             *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
                 u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
     } else {
-        *reinterpret_cast<f32x4*>(a.out + ((int64_t)slot * a.R + c) * 4) = v[0];
+        *reinterpret_cast<u32x2*>(a.out + ((int64_t)slot * a.R + c) * 2) =
+            u32x2{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3])};
     }
 }
 
-// y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, rounded to bf16
-// once; four columns a thread.  info (may be null): U, ids status, MOE_OK.
-__global__ __launch_bounds__(256) void k_combine(const float* __restrict__ O, const int32_t* __restrict__ ids,
+// Square tiles: up to 256 rows by 256 weight rows (gate/up: 128 of each matrix, so 128
+// columns of h), eight waves as 2 x 4, each up to 128 rows by 64 weight rows in registers.
+// Units of both operands go to shared memory two deep; a wave takes the 16-row blocks
+// 2 i + wm, so a tile of few rows is shared by both wave rows.
+constexpr int kTM = 256, kTN = 256, kTileThreads = 512;
+constexpr int kStage = (kTM + kTN) * kUnit;
+constexpr uint32_t kOOB = 0x80000000u;  // beyond every buffer: reads give zero
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+// 1 KB of memory, 16 bytes a lane, to shared memory in lane order
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t vo, uint32_t so) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, (int)vo, (int)so, 0, 0);
+}
+// place of 16-byte chunk c of row r in shared memory's 128-byte rows
+__device__ __forceinline__ int swz(int r, int c) { return r * kUnit + ((c ^ (r & 7)) << 4); }
+
+struct Place {
+    int e, r0, rows, ct;
+};
+
+// Work group b's tile: expert, rows and column tile.  Work groups b, b + 8, ... share an
+// XCD and its L2: each XCD takes a run of tiles, in which the column tiles of up to 8 row
+// tiles are neighbours.
+__device__ __forceinline__ Place find_place(const Args& a, int CT, int b) {
+    const int lane = threadIdx.x & 63, C = (a.N + 63) / 64;
+    int sum = 0;
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        if (e < a.N) {
+            const int lo = min(max(a.offset[e], 0), a.S), hi = min(max(a.offset[e + 1], lo), a.S);
+            sum += (hi - lo + kTM - 1) / kTM;
+        }
+    }
+    int s = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(s, o, 64);
+        if (lane >= o) s += u;
+    }
+    const int total = __shfl(s, 63, 64) * CT;
+    const int per = (total + 7) / 8;
+    const int t = (b & 7) * per + (b >> 3);
+    if ((b >> 3) >= per || t >= total) return Place{-1, 0, 0, 0};
+    const uint64_t past = __ballot(s * CT > t);
+    const int from = __ffsll((unsigned long long)past) - 1;
+    int k = t - (__shfl(s, from, 64) - __shfl(sum, from, 64)) * CT;
+    for (int i = 0; i < C; ++i) {
+        const int e = from * C + i;
+        if (e >= a.N) break;
+        const int lo = min(max(uni(a.offset[e]), 0), a.S), hi = min(max(uni(a.offset[e + 1]), lo), a.S);
+        const int rt = (hi - lo + kTM - 1) / kTM;
+        if (k < rt * CT) {
+            const int sg = k / (8 * CT), in = min(8, rt - 8 * sg);
+            k -= sg * 8 * CT;
+            const int r0 = lo + (8 * sg + k % in) * kTM;
+            return Place{e, r0, min(hi - r0, kTM), k / in};
+        }
+        k -= rt * CT;
+    }
+    return Place{-1, 0, 0, 0};
+}
+
+struct TileLds {
+    char stage[2][kStage];
+    uint8_t xs[2][kTM];     // e4m3: scale bytes of a unit's rows, [wm][row % 16][i]
+    float red[4][kTM];      // e4m3 gate/up: |h| maxima of a row's four column groups
+};
+
+template <bool FP8, bool TILED, bool GU>
+__global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
+    constexpr int ES = FP8 ? 1 : 2;
+    __shared__ TileLds lds;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int lr = lane & 15, q = lane >> 4, wm = wave >> 2, wn = wave & 3;
+    const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
+    constexpr int TC = GU ? kTN / 2 : kTN;  // weight rows of each matrix in a tile
+    const int CT = (a.R + TC - 1) / TC;
+    const Place p = find_place(a, CT, blockIdx.x);
+    if (p.e < 0) return;
+    const int R16 = (p.rows + 15) / 16;
+    // operands: rows of x through the slots (gate/up) or consecutive rows of h
+    const auto rx = GU ? rsrc(a.x, (uint32_t)((int64_t)(a.S / a.m) * KBy))
+                       : rsrc(a.x + (int64_t)p.r0 * KBy, (uint32_t)p.rows * KBy);
+    const uint32_t wbytes = (uint32_t)((int64_t)a.R * KBy);
+    const auto rw0 = rsrc(a.w0 + (int64_t)p.e * wbytes, wbytes);
+    const auto rw1 = GU ? rsrc(a.w1 + (int64_t)p.e * wbytes, wbytes) : rw0;
+    const int ca = ((lane & 7) ^ (lane >> 3)) * 16;  // byte of this lane's chunk in a row's unit
+    uint32_t va[4], vb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int in = i * 8 + wave;
+        int r = min(in * 8 + (lane >> 3), p.rows - 1);
+        if (GU) r = min(max(a.slot[p.r0 + r], 0), a.S - 1) / a.m;
+        va[i] = (uint32_t)r * KBy + ca;
+        // staged weight row -> matrix row: wave columns wn of 64: gate/up 32 of each
+        if (TILED) {
+            const int blk = in >> 1;  // 16 rows
+            const int row = p.ct * TC + (GU ? (blk >> 2) * 32 + (blk & 1) * 16 : blk * 16);
+            vb[i] = row < a.R ? (uint32_t)row * KBy + (in & 1) * 1024 + lane * 16 : kOOB;
+        } else {
+            const int st = in * 8 + (lane >> 3);
+            const int row = p.ct * TC + (GU ? (st >> 6) * 32 + (st & 31) : st);
+            vb[i] = row < a.R ? (uint32_t)row * KBy + ca : kOOB;
+        }
+    }
+    const uint8_t *sx = nullptr, *s0 = nullptr, *s1 = nullptr;
+    if (FP8) {
+        int64_t r = min(tid & (kTM - 1), p.rows - 1) + p.r0;
+        if (GU) r = min(max(a.slot[r], 0), a.S - 1) / a.m;
+        sx = a.xs + r * KB;
+        const int RB = (a.R + kBlk - 1) / kBlk;
+        const int64_t at = ((int64_t)p.e * RB + min(p.ct * TC + (GU ? 0 : wn * 64), a.R - 1) / kBlk) * KB;
+        s0 = a.s0 + at;
+        if (GU) s1 = a.s1 + at;
+    }
+    const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
+    auto stage = [&](int u) {
+        char* A = lds.stage[u & 1];
+        char* B = A + kTM * kUnit;
+        const int left = KBy - u * kUnit;
+        const bool tail = left < kUnit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int in = i * 8 + wave;
+            if (in < R16 * 2) to_lds(rx, A + in * 1024, tail && ca >= left ? kOOB : va[i], u * kUnit);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int in = i * 8 + wave;
+            const bool up = GU && (TILED ? (in >> 2) & 1 : (in >> 2) & 1);
+            const bool off = tail && (TILED ? (in & 1) * 64 >= left : ca >= left);
+            to_lds(up ? rw1 : rw0, B + in * 1024, off ? kOOB : vb[i], u * (TILED ? 2048 : kUnit));
+        }
+    };
+
+    auto run = [&](auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        f32x4 acc[NB][4];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int nx = 0, n0 = 0, n1 = 0;  // the next unit's scale bytes
+        if (FP8) {
+            nx = sx[0];
+            n0 = s0[0];
+            if (GU) n1 = s1[0];
+        }
+        stage(0);
+        for (int u = 0; u < U; ++u) {
+            int e0 = 0, e1 = 0;
+            if (FP8) {
+                if (tid < kTM) lds.xs[u & 1][sxat] = (uint8_t)nx;
+                e0 = n0;
+                e1 = n1;
+            }
+            __syncthreads();
+            if (u + 1 < U) {
+                stage(u + 1);
+                if (FP8) {
+                    nx = sx[u + 1];
+                    n0 = s0[u + 1];
+                    if (GU) n1 = s1[u + 1];
+                }
+            }
+            const char* A = lds.stage[u & 1];
+            const char* B = A + kTM * kUnit;
+            u32x4 b[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    b[j][kk] = *reinterpret_cast<const u32x4*>(
+                        B + (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
+            uint32_t ex[2] = {0u, 0u};
+            if (FP8) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[u & 1][wm * 128 + lr * 8]);
+                ex[0] = v[0];
+                ex[1] = v[1];
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                u32x4 x[2];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    x[kk] = *reinterpret_cast<const u32x4*>(A + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
+                const int e = (int)(ex[i >> 2] >> (8 * (i & 3)));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[0], x[1], acc[i][j], GU && j >= 2 ? e1 : e0, e);
+            }
+        }
+        // a lane holds columns 4 q .. + 4 of 16, of row lr of each block
+        if (GU) {
+            float m[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                m[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float h = silu(acc[i][j][k]) * acc[i][j + 2][k];
+                        acc[i][j][k] = h;
+                        if (FP8) m[i] = fmaxf(m[i], p.ct * TC + wn * 32 + j * 16 + 4 * q + k < a.R ? mag(h) : 0.f);
+                    }
+            }
+            if (FP8) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    m[i] = fmaxf(m[i], __shfl_xor(m[i], 16, 64));
+                    m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, 64));
+                    if (q == 0) lds.red[wn][(i * 2 + wm) * 16 + lr] = m[i];
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int rr = (i * 2 + wm) * 16 + lr;
+                if (rr >= p.rows) continue;
+                const int64_t row = p.r0 + rr;
+                float inv = 1.f;
+                if (FP8) {
+                    const int k = block_exp(fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
+                    inv = pow2(-k);
+                    if (wn == 0 && q == 0) a.outs[row * CT + p.ct] = (uint8_t)(k + 127);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = p.ct * TC + wn * 32 + j * 16 + 4 * q;
+                    const f32x4 h = acc[i][j];
+                    if (c >= a.R) continue;
+                    if (FP8)
+                        *reinterpret_cast<uint32_t*>(a.out + row * a.R + c) = codes4(h[0], h[1], h[2], h[3], inv);
+                    else
+                        *reinterpret_cast<u32x2*>(a.out + (row * a.R + c) * 2) =
+                            u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int rr = (i * 2 + wm) * 16 + lr;
+                if (rr >= p.rows) continue;
+                const int64_t slot = min(max(a.slot[p.r0 + rr], 0), a.S - 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = p.ct * TC + wn * 64 + j * 16 + 4 * q;
+                    if (c < a.R)
+                        *reinterpret_cast<u32x2*>(a.out + (slot * a.R + c) * 2) =
+                            u32x2{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3])};
+                }
+            }
+        }
+    };
+    const int nb = (R16 + 1) / 2;
+    if (nb <= 1) run(std::integral_constant<int, 1>());
+    else if (nb <= 2) run(std::integral_constant<int, 2>());
+    else if (nb <= 4) run(std::integral_constant<int, 4>());
+    else run(std::integral_constant<int, 8>());
+}
+
+// y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
+// to bf16 once; eight columns a thread.  info (may be null): U, ids status, MOE_OK.
+__global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ ids,
                                                 const float* __restrict__ w, int64_t n, int m, int N, int d,
                                                 int accumulate, char* __restrict__ y, const int32_t* __restrict__ u_err,
                                                 int32_t* __restrict__ info) {
-    const int D4 = d / 4;
+    const int D8 = d / 8;
     if (info && blockIdx.x == 0 && threadIdx.x < 3) info[threadIdx.x] = threadIdx.x < 2 ? u_err[threadIdx.x] : MOE_OK;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * D4; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / D4;
-        const int c = (int)(i - t * D4) * 4;
-        f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * D8; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / D8;
+        const int c = (int)(i - t * D8) * 8;
+        float s[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] = 0.f;
         for (int j = 0; j < m; ++j) {
             const int id = ids[t * m + j];
             if (id < 0 || id >= N) continue;
             const float wj = w[t * m + j];
-            const f32x4 o = *reinterpret_cast<const f32x4*>(O + (t * m + j) * d + c);
+            const u32x4 o = *reinterpret_cast<const u32x4*>(O + ((t * m + j) * d + c) * 2);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] += wj * o[k];
+            for (int k = 0; k < 4; ++k) {
+                s[2 * k] += wj * bf16_lo(o[k]);
+                s[2 * k + 1] += wj * bf16_hi(o[k]);
+            }
         }
-        u32x2* p = reinterpret_cast<u32x2*>(y + (t * d + c) * 2);
+        u32x4* p = reinterpret_cast<u32x4*>(y + (t * d + c) * 2);
         if (accumulate) {
-            const u32x2 v = *p;
-            s += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+            const u32x4 v = *p;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[2 * k] += bf16_lo(v[k]);
+                s[2 * k + 1] += bf16_hi(v[k]);
+            }
         }
-        *p = u32x2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
+        *p = u32x4{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]), bf16_pair(s[4], s[5]), bf16_pair(s[6], s[7])};
     }
 }
 
