@@ -14,6 +14,7 @@ namespace {
 using namespace moe_g;
 
 constexpr size_t kAlign = 256;
+constexpr int kCUs = 256;  // a work group of square tiles each
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 hipStream_t stream_of(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -91,17 +92,18 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     return p;
 }
 
-// Square tiles from 16 rows an expert on average; their buffer offsets are 31 bits.
+// Square tiles from 16 rows an expert on average; their loads run up to two units ahead
+// into the next tile, which takes four units a tile, with buffer offsets of 31 bits.
 bool square(const Args& a, bool fp8, bool gu) {
     const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
-    return a.S >= 16 * (int64_t)a.N && a.R * kby <= most && (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
+    return kby > 3 * kUnit && a.S >= 16 * (int64_t)a.N && a.R * kby <= most && (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
 }
 
 template <bool FP8, bool GU>
 void launch_product(const Args& a, bool tiled, hipStream_t st) {
     if (square(a, FP8, GU)) {
         const int64_t tiles = (int64_t)a.S / kTM + std::min(a.N, a.S), tc = GU ? kTN / 2 : kTN;
-        const int grid = (int)((tiles * ((a.R + tc - 1) / tc) + 7) / 8 * 8);
+        const int grid = (int)std::min<int64_t>(kCUs, (tiles * ((a.R + tc - 1) / tc) + 7) / 8 * 8);
         if (tiled)
             hipLaunchKernelGGL((k_tile<FP8, true, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
         else

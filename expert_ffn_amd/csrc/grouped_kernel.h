@@ -30,6 +30,8 @@
 namespace moe_g {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
 typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
@@ -55,30 +57,35 @@ struct Args {
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// One unit's product; sa, sb: the operands' scale bytes (e4m3).
+// One unit's product.  e4m3: the operands' scale bytes, sa's lowest and byte `sel` of sb
+// (a constant once its loop is unrolled).
 template <bool FP8>
-__device__ __forceinline__ f32x4 mma_unit(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c, int sa, int sb) {
-    if (FP8) {
+__device__ __forceinline__ f32x4 mma_unit(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c, int sa, int sb, int sel = 0) {
+    if constexpr (FP8) {
         struct Pair {
             u32x4 lo, hi;
         };
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, Pair{a0, a1}),
-                                                                __builtin_bit_cast(i32x8, Pair{b0, b1}), c, 0, 0, 0, sa,
-                                                                0, sb);
+        const i32x8 a = __builtin_bit_cast(i32x8, Pair{a0, a1}), b = __builtin_bit_cast(i32x8, Pair{b0, b1});
+        switch (sel & 3) {
+            case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+            case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 1, sb);
+            case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 2, sb);
+            default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 3, sb);
+        }
+    } else {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a0), __builtin_bit_cast(bf16x8_t, b0),
+                                                    c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a1),
+                                                       __builtin_bit_cast(bf16x8_t, b1), c, 0, 0, 0);
     }
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a0), __builtin_bit_cast(bf16x8_t, b0), c,
-                                                0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a1), __builtin_bit_cast(bf16x8_t, b1),
-                                                   c, 0, 0, 0);
 }
 
 // silu(z) = z / (1 + exp(-z)); exp(-z) overflows to infinity below z = -88: -0.
-__device__ __forceinline__ float silu(float z) { return z / (1.f + __expf(-z)); }
+__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2_t));
 }
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return bf16_bits(a) | (bf16_bits(b) << 16); }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -494,11 +501,26 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 }
 
 // Square tiles: up to 256 rows by 256 weight rows (gate/up: 128 of each matrix, so 128
-// columns of h), eight waves as 2 x 4, each up to 128 rows by 64 weight rows in registers.
-// Units of both operands go to shared memory two deep; a wave takes the 16-row blocks
-// 2 i + wm, so a tile of few rows is shared by both wave rows.
+// columns of h), eight waves as 2 x 4, each up to 128 rows by 64 weight rows in registers;
+// a wave takes the 16-row blocks 2 i + wm, so a tile of few rows is shared by both wave
+// rows.  One work group a compute unit runs its tiles as one stream of contraction units,
+// so that a tile's first loads are on their way while the one before is finished.
+//
+// The two waves of a SIMD (wm = 0, 1) take turns: while one reads its operands of half a
+// unit from shared memory, the other runs the products of its own.  A unit has four
+// phases, a barrier after each: Ra (all weight rows and the first half of the row blocks),
+// Ma (their products), Rb (the other half), Mb; wm = 1 is one phase behind.  Two units of
+// each operand fit in shared memory.  Every phase issues two of a wave's eight loads of a
+// unit, as early as what they overwrite has been read:
+//     phase of unit v     loads                                 overwrites, last read
+//     Ra                  first-half rows of v + 1              of v - 1, in Ra (v - 1)
+//     Ma                  second-half rows of v + 1             of v - 1, in Rb (v - 1)
+//     Rb, Mb              weight rows of v + 2                  of v, in Ra (v)
+// (each read ends before the barrier of its phase, and wm = 1 reads one phase later, before
+// these).  They are waited for at the end of Ra (the second half of v) and of Rb (the rest
+// of v + 1), one phase before wm = 0 reads them: the counts are of the loads issued since.
 constexpr int kTM = 256, kTN = 256, kTileThreads = 512;
-constexpr int kStage = (kTM + kTN) * kUnit;
+constexpr int kStageA = kTM * kUnit, kStage = (kTM + kTN) * kUnit;
 constexpr uint32_t kOOB = 0x80000000u;  // beyond every buffer: reads give zero
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
@@ -508,57 +530,82 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t vo, uint32_t so) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, (int)vo, (int)so, 0, 0);
 }
-// place of 16-byte chunk c of row r in shared memory's 128-byte rows
+// place of 16-byte chunk c of row r in shared memory's 128-byte rows: the 16 rows that a
+// read instruction touches then fall on different banks
 __device__ __forceinline__ int swz(int r, int c) { return r * kUnit + ((c ^ (r & 7)) << 4); }
 
-struct Place {
-    int e, r0, rows, ct;
-};
-
-// Work group b's tile: expert, rows and column tile.  Work groups b, b + 8, ... share an
-// XCD and its L2: each XCD takes a run of tiles, in which the column tiles of up to 8 row
-// tiles are neighbours.
-__device__ __forceinline__ Place find_place(const Args& a, int CT, int b) {
-    const int lane = threadIdx.x & 63, C = (a.N + 63) / 64;
-    int sum = 0;
-    for (int i = 0; i < C; ++i) {
-        const int e = lane * C + i;
-        if (e < a.N) {
-            const int lo = min(max(a.offset[e], 0), a.S), hi = min(max(a.offset[e + 1], lo), a.S);
-            sum += (hi - lo + kTM - 1) / kTM;
-        }
-    }
-    int s = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(s, o, 64);
-        if (lane >= o) s += u;
-    }
-    const int total = __shfl(s, 63, 64) * CT;
-    const int per = (total + 7) / 8;
-    const int t = (b & 7) * per + (b >> 3);
-    if ((b >> 3) >= per || t >= total) return Place{-1, 0, 0, 0};
-    const uint64_t past = __ballot(s * CT > t);
-    const int from = __ffsll((unsigned long long)past) - 1;
-    int k = t - (__shfl(s, from, 64) - __shfl(sum, from, 64)) * CT;
-    for (int i = 0; i < C; ++i) {
-        const int e = from * C + i;
-        if (e >= a.N) break;
-        const int lo = min(max(uni(a.offset[e]), 0), a.S), hi = min(max(uni(a.offset[e + 1]), lo), a.S);
-        const int rt = (hi - lo + kTM - 1) / kTM;
-        if (k < rt * CT) {
-            const int sg = k / (8 * CT), in = min(8, rt - 8 * sg);
-            k -= sg * 8 * CT;
-            const int r0 = lo + (8 * sg + k % in) * kTM;
-            return Place{e, r0, min(hi - r0, kTM), k / in};
-        }
-        k -= rt * CT;
-    }
-    return Place{-1, 0, 0, 0};
+template <int N>
+__device__ __forceinline__ void wait_vm() {  // all but the last N loads of this wave are done
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_lds() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void block_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
+struct Place {
+    int e, r0, rows, ct;  // rows 0: no tile
+};
+
+// The row tiles of every expert, one scan kept by the wave: lane l holds N / 64 experts.
+struct Tiles {
+    int sum, upto, total, C;
+
+    __device__ __forceinline__ void count(const Args& a) {
+        const int lane = threadIdx.x & 63;
+        C = (a.N + 63) / 64;
+        sum = 0;
+        for (int i = 0; i < C; ++i) {
+            const int e = lane * C + i;
+            if (e < a.N) {
+                const int lo = min(max(a.offset[e], 0), a.S), hi = min(max(a.offset[e + 1], lo), a.S);
+                sum += (hi - lo + kTM - 1) / kTM;
+            }
+        }
+        upto = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += u;
+        }
+        total = __builtin_amdgcn_readlane(upto, 63);
+    }
+
+    // Tile t of CT column tiles each: the column tiles of up to 8 row tiles are neighbours.
+    __device__ __forceinline__ Place place(const Args& a, int CT, int t) const {
+        const uint64_t past = __ballot(upto * CT > t);
+        if (t >= total * CT || !past) return Place{0, 0, 0, 0};
+        const int from = __ffsll((unsigned long long)past) - 1;
+        int k = t - (__builtin_amdgcn_readlane(upto, from) - __builtin_amdgcn_readlane(sum, from)) * CT;
+        for (int i = 0; i < C; ++i) {
+            const int e = from * C + i;
+            if (e >= a.N) break;
+            const int lo = min(max(uni(a.offset[e]), 0), a.S), hi = min(max(uni(a.offset[e + 1]), lo), a.S);
+            const int rt = (hi - lo + kTM - 1) / kTM;
+            if (k < rt * CT) {
+                const int sg = k / (8 * CT), in = min(8, rt - 8 * sg);
+                k -= sg * 8 * CT;
+                const int r0 = lo + (8 * sg + k % in) * kTM;
+                return Place{e, uni(r0), uni(min(hi - r0, kTM)), uni(k / in)};
+            }
+            k -= rt * CT;
+        }
+        return Place{0, 0, 0, 0};
+    }
+};
+
 struct TileLds {
-    char stage[2][kStage];
+    char stage[2][kStage];  // rows, then weight rows
     uint8_t xs[2][kTM];     // e4m3: scale bytes of a unit's rows, [wm][row % 16][i]
     float red[4][kTM];      // e4m3 gate/up: |h| maxima of a row's four column groups
 };
@@ -566,126 +613,235 @@ struct TileLds {
 template <bool FP8, bool TILED, bool GU>
 __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     constexpr int ES = FP8 ? 1 : 2;
+    constexpr int TC = GU ? kTN / 2 : kTN;  // weight rows of each matrix in a tile
     __shared__ TileLds lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int lr = lane & 15, q = lane >> 4, wm = wave >> 2, wn = wave & 3;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
-    constexpr int TC = GU ? kTN / 2 : kTN;  // weight rows of each matrix in a tile
-    const int CT = (a.R + TC - 1) / TC;
-    const Place p = find_place(a, CT, blockIdx.x);
-    if (p.e < 0) return;
-    const int R16 = (p.rows + 15) / 16;
-    // operands: rows of x through the slots (gate/up) or consecutive rows of h
-    const auto rx = GU ? rsrc(a.x, (uint32_t)((int64_t)(a.S / a.m) * KBy))
-                       : rsrc(a.x + (int64_t)p.r0 * KBy, (uint32_t)p.rows * KBy);
-    const uint32_t wbytes = (uint32_t)((int64_t)a.R * KBy);
-    const auto rw0 = rsrc(a.w0 + (int64_t)p.e * wbytes, wbytes);
-    const auto rw1 = GU ? rsrc(a.w1 + (int64_t)p.e * wbytes, wbytes) : rw0;
-    const int ca = ((lane & 7) ^ (lane >> 3)) * 16;  // byte of this lane's chunk in a row's unit
-    uint32_t va[4], vb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    const int CT = (a.R + TC - 1) / TC, RB = (a.R + kBlk - 1) / kBlk;
+    // Work groups b, b + 8, ... share an XCD and its L2: each XCD takes a run of tiles.
+    Tiles tiles;
+    tiles.count(a);
+    const int per = (tiles.total * CT + 7) / 8, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    int next_t = blockIdx.x >> 3;  // within the XCD's run
+    auto take = [&]() {  // in scalar registers: buffer descriptors and loops go by it
+        Place t{0, 0, 0, 0};
+        if (next_t < per) t = tiles.place(a, CT, xcd * per + next_t);
+        next_t += step;
+        return Place{uni(t.e), uni(t.r0), uni(t.rows), uni(t.ct)};
+    };
+
+    // What a tile's loads go by: offsets are one value a lane (chunk of a row's unit, rows of
+    // 8 or a whole 1 KB block) plus one the wave holds.  Rows and weight rows come in eights.
+    // Beyond a tile's rows, and for no tile, loads give zeros.
+    const uint32_t wbytes = (uint32_t)a.R * (uint32_t)KBy;
+    const uint32_t ca = ((lane & 7) ^ (lane >> 3)) * 16;     // this lane's chunk of a row's unit
+    const uint32_t v8 = (uint32_t)(lane >> 3) * KBy + ca;    // in eight consecutive rows
+    const int rem = KBy - (U - 1) * kUnit;                   // bytes of the last unit
+    const uint32_t cut = (int)ca >= rem ? kOOB : 0u;
+    struct Weights {
+        __amdgpu_buffer_rsrc_t r;
+        int row, rows;  // first matrix row of the tile; rows of the matrix, 0 for no tile
+        int at;         // the first scale byte (e4m3)
+    };
+    struct Rows {
+        __amdgpu_buffer_rsrc_t r;
+        int rows;
+    };
+    auto token = [&](int slot) { return min(max(slot, 0), a.S - 1) / a.m; };
+    auto rows_of = [&](const Place& t) {
+        return Rows{GU ? rsrc(a.x, (uint32_t)(a.S / a.m) * (uint32_t)KBy)
+                       : rsrc(a.x + (int64_t)t.r0 * KBy, (uint32_t)t.rows * (uint32_t)KBy),
+                    t.rows};
+    };
+    auto weights_of = [&](const Place& t) {
+        Weights o;
+        o.r = rsrc((GU && wm ? a.w1 : a.w0) + (int64_t)t.e * wbytes, wbytes);
+        o.row = t.ct * TC;
+        o.rows = t.rows ? a.R : 0;
+        o.at = (t.e * RB + min(t.ct * TC + (GU ? 0 : wn * 64), a.R - 1) / kBlk) * KB;
+        return o;
+    };
+    // load i of a wave's four row and four weight loads of unit u
+    auto load_rows = [&](const Rows& w, const uint32_t (&gather)[4], int u, char* stage, int i) {
         const int in = i * 8 + wave;
-        int r = min(in * 8 + (lane >> 3), p.rows - 1);
-        if (GU) r = min(max(a.slot[p.r0 + r], 0), a.S - 1) / a.m;
-        va[i] = (uint32_t)r * KBy + ca;
-        // staged weight row -> matrix row: wave columns wn of 64: gate/up 32 of each
-        if (TILED) {
-            const int blk = in >> 1;  // 16 rows
-            const int row = p.ct * TC + (GU ? (blk >> 2) * 32 + (blk & 1) * 16 : blk * 16);
-            vb[i] = row < a.R ? (uint32_t)row * KBy + (in & 1) * 1024 + lane * 16 : kOOB;
+        uint32_t vo = GU ? gather[i] : v8;
+        if (u == U - 1) vo |= cut;
+        to_lds(w.r, stage + in * 1024, in * 8 < w.rows ? vo : kOOB, u * kUnit + (GU ? 0 : in * 8 * KBy));
+    };
+    auto load_weights = [&](const Weights& w, int u, char* stage, int i) {
+        const int in = i * 8 + wave;
+        // staged weight row -> matrix row: wave columns of 64, gate/up 32 of each matrix
+        // (rows 8 in with wm = 1 are W_up's)
+        const int st = in * 8, row = w.row + (GU ? (st >> 6) * 32 + (st & 31) : st);
+        if (TILED) {  // blocks of 16 rows by 64 bytes
+            const bool in_range = row < w.rows && u * kUnit + (in & 1) * 64 < KBy;
+            to_lds(w.r, stage + kStageA + in * 1024, in_range ? (uint32_t)lane * 16 : kOOB,
+                   (row & ~15) * KBy + (u * 2 + (in & 1)) * 1024);
         } else {
-            const int st = in * 8 + (lane >> 3);
-            const int row = p.ct * TC + (GU ? (st >> 6) * 32 + (st & 31) : st);
-            vb[i] = row < a.R ? (uint32_t)row * KBy + ca : kOOB;
-        }
-    }
-    const uint8_t *sx = nullptr, *s0 = nullptr, *s1 = nullptr;
-    if (FP8) {
-        int64_t r = min(tid & (kTM - 1), p.rows - 1) + p.r0;
-        if (GU) r = min(max(a.slot[r], 0), a.S - 1) / a.m;
-        sx = a.xs + r * KB;
-        const int RB = (a.R + kBlk - 1) / kBlk;
-        const int64_t at = ((int64_t)p.e * RB + min(p.ct * TC + (GU ? 0 : wn * 64), a.R - 1) / kBlk) * KB;
-        s0 = a.s0 + at;
-        if (GU) s1 = a.s1 + at;
-    }
-    const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
-    auto stage = [&](int u) {
-        char* A = lds.stage[u & 1];
-        char* B = A + kTM * kUnit;
-        const int left = KBy - u * kUnit;
-        const bool tail = left < kUnit;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int in = i * 8 + wave;
-            if (in < R16 * 2) to_lds(rx, A + in * 1024, tail && ca >= left ? kOOB : va[i], u * kUnit);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int in = i * 8 + wave;
-            const bool up = GU && (TILED ? (in >> 2) & 1 : (in >> 2) & 1);
-            const bool off = tail && (TILED ? (in & 1) * 64 >= left : ca >= left);
-            to_lds(up ? rw1 : rw0, B + in * 1024, off ? kOOB : vb[i], u * (TILED ? 2048 : kUnit));
+            const uint32_t vo = u == U - 1 ? v8 | cut : v8;
+            to_lds(w.r, stage + kStageA + in * 1024, row < w.rows ? vo : kOOB, row * KBy + u * kUnit);
         }
     };
 
-    auto run = [&](auto nb) {
-        constexpr int NB = decltype(nb)::value;
+    Place p = take();
+    if (!p.rows) return;
+    uint32_t gather[4] = {0, 0, 0, 0}, gather_n[4] = {0, 0, 0, 0};  // gate/up: offsets of the rows' tokens
+    uint32_t xrow = 0, xrow_n = 0;                                  // e4m3: of this thread's row's scale bytes
+    auto ask = [&](const Place& t, uint32_t (&g)[4], uint32_t& x) {  // the slots of a tile's rows
+        const int last = max(t.rows - 1, 0);
+        if (GU) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = a.slot[t.r0 + min((i * 8 + wave) * 8 + (lane >> 3), last)];
+        }
+        if (FP8) {
+            const int r = t.r0 + min(tid & (kTM - 1), last);
+            x = GU ? a.slot[r] : r;
+        }
+    };
+    auto address = [&](uint32_t (&g)[4], uint32_t& x) {
+        if (GU) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = (uint32_t)token(g[i]) * KBy + ca;
+        }
+        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, a.S - 1)) * KB;
+    };
+    ask(p, gather, xrow);
+    address(gather, xrow);
+    const auto rs0 = rsrc(a.s0, (uint32_t)a.N * RB * KB), rs1 = rsrc(a.s1, (uint32_t)a.N * RB * KB);
+    const auto rxs = rsrc(a.xs, (uint32_t)(GU ? a.S / a.m : a.S) * KB);
+    auto byte_of = [](__amdgpu_buffer_rsrc_t r, uint32_t vo, int so) {
+        return (int)__builtin_amdgcn_raw_buffer_load_b8(r, (int)vo, so, 0);
+    };
+    const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
+    int nx = 0, n0 = 0, n1 = 0;  // scale bytes on their way: rows of v + 2, weights of v + 1
+    {
+    const Rows xr = rows_of(p);
+    const Weights wr = weights_of(p);
+    if (FP8) {
+        n0 = byte_of(rs0, 0, wr.at);
+        if (GU) n1 = byte_of(rs1, 0, wr.at);
+        if (!wm) {
+            lds.xs[0][sxat] = (uint8_t)byte_of(rxs, xrow, 0);
+            nx = byte_of(rxs, xrow, 1);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_weights(wr, 0, lds.stage[0], i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_rows(xr, gather, 0, lds.stage[0], i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_weights(wr, 1, lds.stage[1], i);
+    }
+    wait_vm<4>();
+    wait_lds();
+    block_barrier();
+    if (wm) block_barrier();
+
+    int par = 0;  // the stage of the unit at hand
+    auto tile = [&](auto nb) {
+        constexpr int NB = decltype(nb)::value, H = NB / 2;
+        Place pn{0, 0, 0, 0};  // the next tile
+        Rows xr = rows_of(p);
+        Weights wr = weights_of(p);
+        int at = wr.at;  // of the weights' scale bytes that come next
         f32x4 acc[NB][4];
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        int nx = 0, n0 = 0, n1 = 0;  // the next unit's scale bytes
-        if (FP8) {
-            nx = sx[0];
-            n0 = s0[0];
-            if (GU) n1 = s1[0];
-        }
-        stage(0);
         for (int u = 0; u < U; ++u) {
-            int e0 = 0, e1 = 0;
-            if (FP8) {
-                if (tid < kTM) lds.xs[u & 1][sxat] = (uint8_t)nx;
-                e0 = n0;
-                e1 = n1;
+            char* here = lds.stage[par];
+            char* there = lds.stage[par ^ 1];
+            u32x4 b[4][2], x[H][2];
+            uint32_t ex[2] = {0u, 0u};
+            auto read_rows = [&](int first) {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+                        x[i][kk] = *reinterpret_cast<const u32x4*>(
+                            here + swz(((first + i) * 2 + wm) * 16 + lr, kk * 4 + q));
+            };
+            int e0 = n0, e1 = n1;
+            auto products = [&](auto first) {
+                constexpr int F = decltype(first)::value;
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[F + i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i][0], x[i][1], acc[F + i][j],
+                                                      GU && j >= 2 ? e1 : e0, (int)ex[(F + i) / 4], F + i);
+                __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[F + i][j]));  // they stay in this phase
+            };
+            // Ra.  The loads below are of unit u + 1's rows; past the last, of the next tile's first.
+            int ua = u + 1, ub = u + 2;
+            if (ua >= U) {
+                xr = rows_of(pn);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gather[i] = gather_n[i];
+                if (FP8) at = wr.at;
+                ua = 0;
             }
-            __syncthreads();
-            if (u + 1 < U) {
-                stage(u + 1);
-                if (FP8) {
-                    nx = sx[u + 1];
-                    n0 = s0[u + 1];
-                    if (GU) n1 = s1[u + 1];
-                }
-            }
-            const char* A = lds.stage[u & 1];
-            const char* B = A + kTM * kUnit;
-            u32x4 b[4][2];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
                     b[j][kk] = *reinterpret_cast<const u32x4*>(
-                        B + (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
-            uint32_t ex[2] = {0u, 0u};
+                        here + kStageA +
+                        (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
+            read_rows(0);
             if (FP8) {
-                const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[u & 1][wm * 128 + lr * 8]);
+                const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[par][wm * 128 + lr * 8]);
                 ex[0] = v[0];
                 ex[1] = v[1];
+                n0 = byte_of(rs0, 0, at + ua);
+                if (GU) n1 = byte_of(rs1, 0, at + ua);
             }
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                u32x4 x[2];
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    x[kk] = *reinterpret_cast<const u32x4*>(A + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
-                const int e = (int)(ex[i >> 2] >> (8 * (i & 3)));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[0], x[1], acc[i][j], GU && j >= 2 ? e1 : e0, e);
+            load_rows(xr, gather, ua, there, 0);
+            load_rows(xr, gather, ua, there, 1);
+            wait_lds();
+            wait_vm<6>();
+            block_barrier();
+            // Ma
+            load_rows(xr, gather, ua, there, 2);
+            load_rows(xr, gather, ua, there, 3);
+            products(std::integral_constant<int, 0>());
+            block_barrier();
+            // Rb
+            if (u == 0) {
+                pn = take();
+                ask(pn, gather_n, xrow_n);
             }
+            if (u == 1) address(gather_n, xrow_n);
+            if (ub >= U) {
+                if (ub == U) {
+                    wr = weights_of(pn);
+                    if (FP8) xrow = xrow_n;
+                }
+                ub -= U;
+            }
+            read_rows(H);
+            if (FP8 && !wm) {
+                lds.xs[par ^ 1][sxat] = (uint8_t)nx;
+                nx = byte_of(rxs, xrow, ub);
+            }
+            load_weights(wr, ub, here, 0);
+            load_weights(wr, ub, here, 1);
+            wait_lds();
+            wait_vm<4>();
+            block_barrier();
+            // Mb
+            load_weights(wr, ub, here, 2);
+            load_weights(wr, ub, here, 3);
+            products(std::integral_constant<int, H>());
+            block_barrier();
+            par ^= 1;
         }
         // a lane holds columns 4 q .. + 4 of 16, of row lr of each block
         if (GU) {
@@ -699,7 +855,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     for (int k = 0; k < 4; ++k) {
                         const float h = silu(acc[i][j][k]) * acc[i][j + 2][k];
                         acc[i][j][k] = h;
-                        if (FP8) m[i] = fmaxf(m[i], p.ct * TC + wn * 32 + j * 16 + 4 * q + k < a.R ? mag(h) : 0.f);
+                        if (FP8) m[i] = fmaxf(m[i], mag(h));  // columns past R: zero weights, h = 0
                     }
             }
             if (FP8) {
@@ -709,7 +865,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, 64));
                     if (q == 0) lds.red[wn][(i * 2 + wm) * 16 + lr] = m[i];
                 }
-                __syncthreads();
+                wait_lds();
+                block_barrier();
             }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -718,7 +875,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 const int64_t row = p.r0 + rr;
                 float inv = 1.f;
                 if (FP8) {
-                    const int k = block_exp(fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
+                    const int k = block_exp(
+                        fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
                     inv = pow2(-k);
                     if (wn == 0 && q == 0) a.outs[row * CT + p.ct] = (uint8_t)(k + 127);
                 }
@@ -749,12 +907,20 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 }
             }
         }
+        return pn;
     };
-    const int nb = (R16 + 1) / 2;
-    if (nb <= 1) run(std::integral_constant<int, 1>());
-    else if (nb <= 2) run(std::integral_constant<int, 2>());
-    else if (nb <= 4) run(std::integral_constant<int, 4>());
-    else run(std::integral_constant<int, 8>());
+    while (p.rows) {
+        Place pn;
+        if (p.rows <= 64) pn = tile(std::integral_constant<int, 2>());
+        else if (p.rows <= 128) pn = tile(std::integral_constant<int, 4>());
+        else if (p.rows <= 192) pn = tile(std::integral_constant<int, 6>());
+        else pn = tile(std::integral_constant<int, 8>());
+        // values of the wave, which the compiler no longer knows them to be where tiles of several heights meet
+        p = Place{uni(pn.e), uni(pn.r0), uni(pn.rows), uni(pn.ct)};
+        next_t = uni(next_t);
+        par = uni(par);
+    }
+    if (!wm) block_barrier();
 }
 
 // y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
