@@ -49,12 +49,16 @@ int group_chunks(int64_t S) { return (int)((S + group_chunk(S) - 1) / group_chun
 size_t group_ws(int64_t S, int N) { return align_up((size_t)group_chunks(S) * (N + 1) * 4); }
 
 void run_group(const int32_t* ids, int64_t S, int m, int N, int32_t* count, int32_t* offset, int32_t* sbe,
-               int32_t* distinct, int32_t* u_err, void* ws, hipStream_t st) {
+               int32_t* distinct, int32_t* u_err, int32_t* row_of, void* ws, hipStream_t st) {
     int32_t* hist = reinterpret_cast<int32_t*>(ws);
     const int G = group_chunks(S);
     hipLaunchKernelGGL(k_group_hist, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist);
     hipLaunchKernelGGL(k_group_scatter, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist, count, offset, sbe,
-                       distinct, u_err);
+                       distinct, u_err, row_of);
+}
+
+void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of, hipStream_t st) {
+    hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of);
 }
 
 int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
@@ -63,7 +67,7 @@ int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
 
 // Workspace of a whole pass, and of the products alone (which use hf and O).
 struct Space {
-    size_t hist, count, offset, sbe, distinct, u_err, xq, xs, h, hs, hf, o, total;
+    size_t hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
 };
 
 Space space_of(const moe_layer_desc* d, int32_t n) {
@@ -86,6 +90,7 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     p.count = take((size_t)d->N * 4);
     p.offset = take((size_t)(d->N + 1) * 4);
     p.sbe = take(S * 4);
+    p.row_of = take(S * 4);
     p.distinct = take((size_t)d->N * 4);
     p.u_err = take(8);
     p.total = at;
@@ -153,8 +158,8 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
 
 template <bool FP8>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
-              const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, void* y, void* o,
-              const int32_t* u_err, int32_t* info, hipStream_t st) {
+              const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, const int32_t* row_of, void* y,
+              void* o, const int32_t* u_err, int32_t* info, hipStream_t st) {
     Args a{};
     a.x = reinterpret_cast<const char*>(h);
     a.xs = hs;
@@ -171,7 +176,7 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * (d->d_model / 8);
     hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 255) / 256, 16384)), dim3(256), 0, st,
-                       reinterpret_cast<const char*>(o), ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       reinterpret_cast<const char*>(o), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 
@@ -184,14 +189,15 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     auto u8 = [&](size_t at) { return reinterpret_cast<uint8_t*>(b + at); };
     (void)hipGetLastError();
     run_group(ids, (int64_t)n * d->m, d->m, d->N, i32(p.count), i32(p.offset), i32(p.sbe), i32(p.distinct),
-              i32(p.u_err), b + p.hist, st);
+              i32(p.u_err), i32(p.row_of), b + p.hist, st);
     if (FP8)
         hipLaunchKernelGGL(k_quant_rows<false>, dim3(rows_grid(n, d->d_model)), dim3(256), 0, st,
                            reinterpret_cast<const char*>(x), (int64_t)n, d->d_model,
                            static_cast<const int32_t*>(nullptr), u8(p.xq), u8(p.xs));
     run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
                      b + p.h, u8(p.hs), b + p.hf, st);
-    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), y, b + p.o, i32(p.u_err), info, st);
+    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y,
+                  b + p.o, i32(p.u_err), info, st);
     return launched();
 }
 
@@ -220,7 +226,8 @@ int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t
     rc = check_ws(ws, ws_bytes, group_ws((int64_t)n * m, N));
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
-    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, ws, stream_of(hip_stream));
+    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, nullptr, ws,
+              stream_of(hip_stream));
     return launched();
 }
 
@@ -271,8 +278,11 @@ int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weight
     rc = check_ws(ws, ws_bytes, p.total);
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
+    char* b = reinterpret_cast<char*>(ws);
+    int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
+    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, stream_of(hip_stream));
     run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
-                    slot_by_expert, y, reinterpret_cast<char*>(ws) + p.o, nullptr, nullptr, stream_of(hip_stream));
+                    slot_by_expert, row_of, y, b + p.o, nullptr, nullptr, stream_of(hip_stream));
     return launched();
 }
 
@@ -288,8 +298,11 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
     rc = check_ws(ws, ws_bytes, p.total);
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
+    char* b = reinterpret_cast<char*>(ws);
+    int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
+    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, stream_of(hip_stream));
     run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
-                   slot_by_expert, y, reinterpret_cast<char*>(ws) + p.o, nullptr, nullptr, stream_of(hip_stream));
+                   slot_by_expert, row_of, y, b + p.o, nullptr, nullptr, stream_of(hip_stream));
     return launched();
 }
 

@@ -50,7 +50,7 @@ struct Args {
     const uint8_t* s1;
     const int32_t* offset;
     const int32_t* slot;
-    char* out;            // gate/up: h [S][R]; down: O [S][R]
+    char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order
     uint8_t* outs;        // e4m3 gate/up: scale bytes of h
     int N, m, S, R, K;
 };
@@ -293,7 +293,8 @@ __device__ __forceinline__ int group_scan(int v, int* part, int& total) {
 __global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __restrict__ ids, int64_t S, int m, int N,
                                                             const int32_t* __restrict__ hist, int32_t* __restrict__ count,
                                                             int32_t* __restrict__ offset, int32_t* __restrict__ sbe,
-                                                            int32_t* __restrict__ distinct, int32_t* __restrict__ u_err) {
+                                                            int32_t* __restrict__ distinct, int32_t* __restrict__ u_err,
+                                                            int32_t* __restrict__ row_of) {
     __shared__ int base[kGWaves * MOE_MAX_EXPERTS];  // [wave][N]: next place of the wave's slots
     __shared__ int part[kGWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -357,6 +358,7 @@ __global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __re
             const uint64_t under = same & ((1ull << lane) - 1);
             const int at = base[wave * N + id];
             sbe[at + __popcll(under)] = (int)s;
+            if (row_of) row_of[s] = at + __popcll(under);
             __builtin_amdgcn_wave_barrier();
             if (under == 0) base[wave * N + id] = at + __popcll(same);
         }
@@ -495,7 +497,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
             *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
                 u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
     } else {
-        *reinterpret_cast<u32x2*>(a.out + ((int64_t)slot * a.R + c) * 2) =
+        *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
             u32x2{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3])};
     }
 }
@@ -508,17 +510,17 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 //
 // The two waves of a SIMD (wm = 0, 1) take turns: while one reads its operands of half a
 // unit from shared memory, the other runs the products of its own.  A unit has four
-// phases, a barrier after each: Ra (all weight rows and the first half of the row blocks),
-// Ma (their products), Rb (the other half), Mb; wm = 1 is one phase behind.  Two units of
-// each operand fit in shared memory.  Every phase issues two of a wave's eight loads of a
-// unit, as early as what they overwrite has been read:
-//     phase of unit v     loads                                 overwrites, last read
-//     Ra                  first-half rows of v + 1              of v - 1, in Ra (v - 1)
-//     Ma                  second-half rows of v + 1             of v - 1, in Rb (v - 1)
-//     Rb, Mb              weight rows of v + 2                  of v, in Ra (v)
+// phases, a barrier after each: Ra (all weight rows and the first 128 rows), Ma (their
+// products), Rb (the other 128), Mb; wm = 1 is one phase behind.  Two units of
+// each operand fit in shared memory.  A wave's eight loads of a unit go out as soon as what
+// they overwrite has been read, and none in Ra, which reads the most:
+//     phase of unit v     loads                                       overwrites, last read
+//     Ma                  last 128 rows of v + 1 (two)                of v - 1, in Rb (v - 1)
+//     Rb, Mb              weight rows, first 128 rows of v + 2        of v, in Ra (v)
+//                         (three each)
 // (each read ends before the barrier of its phase, and wm = 1 reads one phase later, before
-// these).  They are waited for at the end of Ra (the second half of v) and of Rb (the rest
-// of v + 1), one phase before wm = 0 reads them: the counts are of the loads issued since.
+// these).  They are waited for at the end of Ra (the last 128 rows of v) and of Rb (the rest
+// of v + 1), one phase before wm = 0 reads them: the counts are of what was issued since.
 constexpr int kTM = 256, kTN = 256, kTileThreads = 512;
 constexpr int kStageA = kTM * kUnit, kStage = (kTM + kTN) * kUnit;
 constexpr uint32_t kOOB = 0x80000000u;  // beyond every buffer: reads give zero
@@ -608,6 +610,7 @@ struct TileLds {
     char stage[2][kStage];  // rows, then weight rows
     uint8_t xs[2][kTM];     // e4m3: scale bytes of a unit's rows, [wm][row % 16][i]
     float red[4][kTM];      // e4m3 gate/up: |h| maxima of a row's four column groups
+    char turn[8][16 * 144]; // a wave's results on their way from columns to rows
 };
 
 template <bool FP8, bool TILED, bool GU>
@@ -732,17 +735,23 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     for (int i = 0; i < 4; ++i) load_rows(xr, gather, 0, lds.stage[0], i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_weights(wr, 1, lds.stage[1], i);
+    load_rows(xr, gather, 1, lds.stage[1], 0);
+    load_rows(xr, gather, 1, lds.stage[1], 1);
     }
-    wait_vm<4>();
+    wait_vm<6>();
     wait_lds();
     block_barrier();
     if (wm) block_barrier();
 
-    int par = 0;  // the stage of the unit at hand
+    int par = 0;      // the stage of the unit at hand
+    int stores = 0;   // of the tile before, which may still be on their way
+    constexpr int kScale = FP8 ? (GU ? 2 : 1) : 0;  // loads of weight scale bytes, in Ra
     auto tile = [&](auto nb) {
-        constexpr int NB = decltype(nb)::value, H = NB / 2;
+        constexpr int NB = decltype(nb)::value, H = NB < 4 ? NB : 4;  // row blocks of a wave; of Ra and Ma
+        // its own stores, the same number whatever the rows: those of no row are dropped by their bounds
+        constexpr int kStores = GU ? (FP8 ? NB / 2 + 1 : NB) : 2 * NB;
         Place pn{0, 0, 0, 0};  // the next tile
-        Rows xr = rows_of(p);
+        Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
         Weights wr = weights_of(p);
         int at = wr.at;  // of the weights' scale bytes that come next
         f32x4 acc[NB][4];
@@ -755,36 +764,44 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             char* there = lds.stage[par ^ 1];
             u32x4 b[4][2], x[H][2];
             uint32_t ex[2] = {0u, 0u};
-            auto read_rows = [&](int first) {
+            auto read_rows = [&](int first, int end) {
 #pragma unroll
-                for (int i = 0; i < H; ++i)
+                for (int i = first; i < end; ++i)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk)
-                        x[i][kk] = *reinterpret_cast<const u32x4*>(
-                            here + swz(((first + i) * 2 + wm) * 16 + lr, kk * 4 + q));
+                        x[i - first][kk] =
+                            *reinterpret_cast<const u32x4*>(here + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
             };
             int e0 = n0, e1 = n1;
-            auto products = [&](auto first) {
-                constexpr int F = decltype(first)::value;
+            // the products of row blocks first .. end, `loads` after the first half of them
+            auto products = [&](auto first, auto end, auto loads) {
+                constexpr int F = decltype(first)::value, E = decltype(end)::value;
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                for (int i = 0; i < H; ++i)
+                for (int i = F; i < E; ++i) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[F + i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i][0], x[i][1], acc[F + i][j],
-                                                      GU && j >= 2 ? e1 : e0, (int)ex[(F + i) / 4], F + i);
+                        acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i - F][0], x[i - F][1], acc[i][j],
+                                                  GU && j >= 2 ? e1 : e0, (int)ex[i / 4], i);
+                    if (i == (F + E - 1) / 2) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        loads();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                if (E <= F) loads();
                 __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-                for (int i = 0; i < H; ++i)
+                for (int i = F; i < E; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[F + i][j]));  // they stay in this phase
+                    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));  // they stay in this phase
             };
-            // Ra.  The loads below are of unit u + 1's rows; past the last, of the next tile's first.
-            int ua = u + 1, ub = u + 2;
+            // Ra
+            int ua = u + 1, ub = u + 2;  // past the last unit: the next tile's first
             if (ua >= U) {
-                xr = rows_of(pn);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) gather[i] = gather_n[i];
+                xb = rows_of(pn);
+                gather[2] = gather_n[2];
+                gather[3] = gather_n[3];
                 if (FP8) at = wr.at;
                 ua = 0;
             }
@@ -795,7 +812,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     b[j][kk] = *reinterpret_cast<const u32x4*>(
                         here + kStageA +
                         (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
-            read_rows(0);
+            read_rows(0, H);
             if (FP8) {
                 const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[par][wm * 128 + lr * 8]);
                 ex[0] = v[0];
@@ -803,15 +820,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 n0 = byte_of(rs0, 0, at + ua);
                 if (GU) n1 = byte_of(rs1, 0, at + ua);
             }
-            load_rows(xr, gather, ua, there, 0);
-            load_rows(xr, gather, ua, there, 1);
             wait_lds();
-            wait_vm<6>();
+            if (u == 0 && stores == 16) wait_vm<6 + kScale + 16>();
+            else if (u == 0 && stores >= 5) wait_vm<6 + kScale + 5>();
+            else wait_vm<6 + kScale>();
             block_barrier();
             // Ma
-            load_rows(xr, gather, ua, there, 2);
-            load_rows(xr, gather, ua, there, 3);
-            products(std::integral_constant<int, 0>());
+            products(std::integral_constant<int, 0>(), std::integral_constant<int, H>(), [&] {
+                load_rows(xb, gather, ua, there, 2);
+                load_rows(xb, gather, ua, there, 3);
+            });
             block_barrier();
             // Rb
             if (u == 0) {
@@ -822,29 +840,44 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             if (ub >= U) {
                 if (ub == U) {
                     wr = weights_of(pn);
+                    xa = rows_of(pn);
+                    gather[0] = gather_n[0];
+                    gather[1] = gather_n[1];
                     if (FP8) xrow = xrow_n;
                 }
                 ub -= U;
             }
-            read_rows(H);
+            read_rows(H, NB);
             if (FP8 && !wm) {
                 lds.xs[par ^ 1][sxat] = (uint8_t)nx;
                 nx = byte_of(rxs, xrow, ub);
             }
             load_weights(wr, ub, here, 0);
             load_weights(wr, ub, here, 1);
+            load_rows(xa, gather, ub, here, 0);
             wait_lds();
-            wait_vm<4>();
+            if (u == 0 && stores == 16) wait_vm<5 + kScale + 16>();
+            else if (u == 0 && stores >= 5) wait_vm<5 + kScale + 5>();
+            else wait_vm<5 + kScale>();
             block_barrier();
             // Mb
-            load_weights(wr, ub, here, 2);
-            load_weights(wr, ub, here, 3);
-            products(std::integral_constant<int, H>());
+            products(std::integral_constant<int, H>(), nb, [&] {
+                load_weights(wr, ub, here, 2);
+                load_weights(wr, ub, here, 3);
+                load_rows(xa, gather, ub, here, 1);
+            });
             block_barrier();
             par ^= 1;
         }
-        // a lane holds columns 4 q .. + 4 of 16, of row lr of each block
-        if (GU) {
+        // A lane holds columns 4 q .. + 4 of 16, of row lr of each block; turned in shared memory,
+        // four or eight lanes store 64 or 128 bytes of a row.
+        char* turn = lds.turn[wave];
+        int el = lane;
+        asm volatile("" : "+v"(el));  // addresses below are formed here, not kept through the products
+        const int er = el & 15, eq = el >> 4;
+        if constexpr (GU) {
+            const auto ro = rsrc(a.out + (int64_t)p.r0 * a.R * ES, (uint32_t)p.rows * a.R * ES);
+            const int c0 = p.ct * TC + wn * 32;  // this wave's 32 columns of h
             float m[NB];
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -858,55 +891,75 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         if (FP8) m[i] = fmaxf(m[i], mag(h));  // columns past R: zero weights, h = 0
                     }
             }
-            if (FP8) {
+            if constexpr (FP8) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     m[i] = fmaxf(m[i], __shfl_xor(m[i], 16, 64));
                     m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, 64));
-                    if (q == 0) lds.red[wn][(i * 2 + wm) * 16 + lr] = m[i];
+                    if (eq == 0) lds.red[wn][(i * 2 + wm) * 16 + er] = m[i];
                 }
                 wait_lds();
                 block_barrier();
-            }
+                auto exp_of = [&](int rr) {
+                    return block_exp(fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
+                };
+                // codes, two blocks of rows at a time: 32 rows of 32 bytes
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int rr = (i * 2 + wm) * 16 + lr;
-                if (rr >= p.rows) continue;
-                const int64_t row = p.r0 + rr;
-                float inv = 1.f;
-                if (FP8) {
-                    const int k = block_exp(
-                        fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
-                    inv = pow2(-k);
-                    if (wn == 0 && q == 0) a.outs[row * CT + p.ct] = (uint8_t)(k + 127);
+                for (int i = 0; i < NB; i += 2) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float inv = pow2(-exp_of(((i + k) * 2 + wm) * 16 + er));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const f32x4 h = acc[i + k][j];
+                            *reinterpret_cast<uint32_t*>(turn + (k * 16 + er) * 48 + j * 16 + 4 * eq) =
+                                codes4(h[0], h[1], h[2], h[3], inv);
+                        }
+                    }
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 1) * 48 + (el & 1) * 16);
+                    const int rr = ((i + (el >> 5)) * 2 + wm) * 16 + ((el >> 1) & 15), c = c0 + (el & 1) * 16;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? (uint32_t)rr * a.R + c : kOOB, 0, 0);
                 }
+                // scale bytes: wave column wn those of two blocks
+                const int i = wn * 2 + (el >> 4), rr = (i * 2 + wm) * 16 + er;
+                const auto rso = rsrc(a.outs + (int64_t)p.r0 * CT, (uint32_t)p.rows * CT);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(exp_of(rr & (kTM - 1)) + 127), rso,
+                                                     el < 32 && i < NB ? rr * CT + p.ct : kOOB, 0, 0);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = p.ct * TC + wn * 32 + j * 16 + 4 * q;
-                    const f32x4 h = acc[i][j];
-                    if (c >= a.R) continue;
-                    if (FP8)
-                        *reinterpret_cast<uint32_t*>(a.out + row * a.R + c) = codes4(h[0], h[1], h[2], h[3], inv);
-                    else
-                        *reinterpret_cast<u32x2*>(a.out + (row * a.R + c) * 2) =
+                for (int i = 0; i < NB; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4 h = acc[i][j];
+                        *reinterpret_cast<u32x2*>(turn + er * 80 + j * 32 + 8 * eq) =
                             u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+                    }
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 2) * 80 + (el & 3) * 16);
+                    const int rr = (i * 2 + wm) * 16 + (el >> 2), c = c0 + (el & 3) * 8;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
                 }
             }
         } else {
+            const auto ro = rsrc(a.out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
+            const int c0 = p.ct * TC + wn * 64;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                const int rr = (i * 2 + wm) * 16 + lr;
-                if (rr >= p.rows) continue;
-                const int64_t slot = min(max(a.slot[p.r0 + rr], 0), a.S - 1);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = p.ct * TC + wn * 64 + j * 16 + 4 * q;
-                    if (c < a.R)
-                        *reinterpret_cast<u32x2*>(a.out + (slot * a.R + c) * 2) =
-                            u32x2{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3])};
+                    const f32x4 o = acc[i][j];
+                    *reinterpret_cast<u32x2*>(turn + er * 144 + j * 32 + 8 * eq) =
+                        u32x2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = k * 8 + (el >> 3);
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(turn + r * 144 + (el & 7) * 16);
+                    const int rr = (i * 2 + wm) * 16 + r, c = c0 + (el & 7) * 8;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
                 }
             }
         }
+        stores = kStores;
         return pn;
     };
     while (p.rows) {
@@ -919,14 +972,23 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         p = Place{uni(pn.e), uni(pn.r0), uni(pn.rows), uni(pn.ct)};
         next_t = uni(next_t);
         par = uni(par);
+        stores = uni(stores);
     }
     if (!wm) block_barrier();
 }
 
+// The row of each slot that has one.
+__global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot, const int32_t* __restrict__ rows,
+                                               int S, int32_t* __restrict__ row_of) {
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    if (r < min(*rows, S)) row_of[min(max(slot[r], 0), S - 1)] = r;
+}
+
 // y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
 // to bf16 once; eight columns a thread.  info (may be null): U, ids status, MOE_OK.
-__global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ ids,
-                                                const float* __restrict__ w, int64_t n, int m, int N, int d,
+__global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ row_of,
+                                                const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
+                                                int m, int N, int d,
                                                 int accumulate, char* __restrict__ y, const int32_t* __restrict__ u_err,
                                                 int32_t* __restrict__ info) {
     const int D8 = d / 8;
@@ -941,7 +1003,8 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
             const int id = ids[t * m + j];
             if (id < 0 || id >= N) continue;
             const float wj = w[t * m + j];
-            const u32x4 o = *reinterpret_cast<const u32x4*>(O + ((t * m + j) * d + c) * 2);
+            const int64_t r = min(max(row_of[t * m + j], 0), (int)(n * m) - 1);
+            const u32x4 o = *reinterpret_cast<const u32x4*>(O + (r * d + c) * 2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 s[2 * k] += wj * bf16_lo(o[k]);
