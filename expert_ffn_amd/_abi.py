@@ -156,7 +156,7 @@ def lib():
             L.moe_quant_weights.argtypes = [vp, i32, i32, i32, vp, vp, vp]
             L.moe_grouped_workspace_bytes.argtypes = [pdesc, i32]
             L.moe_grouped_workspace_bytes.restype = sz
-            L.moe_grouped_gate_up.argtypes = [pdesc, pw, vp, i32, vp, vp, vp, vp]
+            L.moe_grouped_gate_up.argtypes = [pdesc, pw, vp, i32, vp, vp, vp, vp, sz, vp]
             L.moe_grouped_gate_up_fp8.argtypes = [pdesc, pw8, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
             L.moe_grouped_down.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
             L.moe_grouped_down_fp8.argtypes = [pdesc, pw8, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]

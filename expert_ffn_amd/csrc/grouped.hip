@@ -49,16 +49,17 @@ int group_chunks(int64_t S) { return (int)((S + group_chunk(S) - 1) / group_chun
 size_t group_ws(int64_t S, int N) { return align_up((size_t)group_chunks(S) * (N + 1) * 4); }
 
 void run_group(const int32_t* ids, int64_t S, int m, int N, int32_t* count, int32_t* offset, int32_t* sbe,
-               int32_t* distinct, int32_t* u_err, int32_t* row_of, void* ws, hipStream_t st) {
+               int32_t* distinct, int32_t* u_err, int32_t* row_of, int32_t* queues, int nq, void* ws, hipStream_t st) {
     int32_t* hist = reinterpret_cast<int32_t*>(ws);
     const int G = group_chunks(S);
     hipLaunchKernelGGL(k_group_hist, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist);
     hipLaunchKernelGGL(k_group_scatter, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist, count, offset, sbe,
-                       distinct, u_err, row_of);
+                       distinct, u_err, row_of, queues, nq);
 }
 
-void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of, hipStream_t st) {
-    hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of);
+void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of, int32_t* queue, hipStream_t st) {
+    static_assert(kQueue == 256, "");
+    hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of, queue);
 }
 
 int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
@@ -67,7 +68,7 @@ int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
 
 // Workspace of a whole pass, and of the products alone (which use hf and O).
 struct Space {
-    size_t hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
+    size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
 };
 
 Space space_of(const moe_layer_desc* d, int32_t n) {
@@ -80,6 +81,7 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
         at += align_up(bytes);
         return a;
     };
+    p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
     p.o = take(S * d->d_model * 2);
     p.hf = take(fp8 ? S * d->d_ff * 4 : 0);
     p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
@@ -130,7 +132,8 @@ struct Weights {
 
 template <bool FP8>
 void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const uint8_t* xs, int32_t n,
-                 const int32_t* offset, const int32_t* sbe, void* h, uint8_t* hs, void* hf, hipStream_t st) {
+                 const int32_t* offset, const int32_t* sbe, void* h, uint8_t* hs, void* hf, int32_t* queue,
+                 hipStream_t st) {
     Args a{};
     a.x = reinterpret_cast<const char*>(x);
     a.xs = xs;
@@ -142,6 +145,7 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
     a.slot = sbe;
     a.out = reinterpret_cast<char*>(h);
     a.outs = hs;
+    a.queue = queue;
     a.N = d->N;
     a.m = d->m;
     a.S = n * d->m;
@@ -159,7 +163,7 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
 template <bool FP8>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
               const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, const int32_t* row_of, void* y,
-              void* o, const int32_t* u_err, int32_t* info, hipStream_t st) {
+              void* o, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
     Args a{};
     a.x = reinterpret_cast<const char*>(h);
     a.xs = hs;
@@ -168,6 +172,7 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.offset = offset;
     a.slot = sbe;
     a.out = reinterpret_cast<char*>(o);
+    a.queue = queue;
     a.N = d->N;
     a.m = d->m;
     a.S = n * d->m;
@@ -189,15 +194,15 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     auto u8 = [&](size_t at) { return reinterpret_cast<uint8_t*>(b + at); };
     (void)hipGetLastError();
     run_group(ids, (int64_t)n * d->m, d->m, d->N, i32(p.count), i32(p.offset), i32(p.sbe), i32(p.distinct),
-              i32(p.u_err), i32(p.row_of), b + p.hist, st);
+              i32(p.u_err), i32(p.row_of), i32(p.queue), 2 * kQueue, b + p.hist, st);
     if (FP8)
         hipLaunchKernelGGL(k_quant_rows<false>, dim3(rows_grid(n, d->d_model)), dim3(256), 0, st,
                            reinterpret_cast<const char*>(x), (int64_t)n, d->d_model,
                            static_cast<const int32_t*>(nullptr), u8(p.xq), u8(p.xs));
     run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
-                     b + p.h, u8(p.hs), b + p.hf, st);
+                     b + p.h, u8(p.hs), b + p.hf, i32(p.queue), st);
     run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y,
-                  b + p.o, i32(p.u_err), info, st);
+                  b + p.o, i32(p.queue) + kQueue, i32(p.u_err), info, st);
     return launched();
 }
 
@@ -226,8 +231,8 @@ int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t
     rc = check_ws(ws, ws_bytes, group_ws((int64_t)n * m, N));
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
-    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, nullptr, ws,
-              stream_of(hip_stream));
+    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, nullptr, nullptr,
+              0, ws, stream_of(hip_stream));
     return launched();
 }
 
@@ -238,15 +243,21 @@ size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
 }
 
 int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, int32_t n,
-                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* hip_stream) {
-    const int rc = check_desc(desc, n, MOE_BF16);
+                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* ws, size_t ws_bytes,
+                        void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_BF16);
     if (rc != MOE_OK) return rc;
     if (!weights || !weights->w_gate || !weights->w_up || !x || !offset || !slot_by_expert || !h) return MOE_E_INVAL;
     if (!aligned(weights->w_gate, 16) || !aligned(weights->w_up, 16) || !aligned(x, 16) || !aligned(h, 16))
         return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
+    hipLaunchKernelGGL(k_zero_queue, dim3(1), dim3(kQueue), 0, stream_of(hip_stream), queue);
     run_gate_up<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr}, x, nullptr, n, offset,
-                       slot_by_expert, h, nullptr, nullptr, stream_of(hip_stream));
+                       slot_by_expert, h, nullptr, nullptr, queue, stream_of(hip_stream));
     return launched();
 }
 
@@ -261,9 +272,12 @@ int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* w
     const Space p = space_of(desc, n);
     rc = check_ws(ws, ws_bytes, p.total);
     if (rc != MOE_OK) return rc;
+    int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
+    hipLaunchKernelGGL(k_zero_queue, dim3(1), dim3(kQueue), 0, stream_of(hip_stream), queue);
     run_gate_up<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up}, xq, x_scale, n,
-                      offset, slot_by_expert, hq, h_scale, reinterpret_cast<char*>(ws) + p.hf, stream_of(hip_stream));
+                      offset, slot_by_expert, hq, h_scale, reinterpret_cast<char*>(ws) + p.hf, queue,
+                      stream_of(hip_stream));
     return launched();
 }
 
@@ -280,9 +294,10 @@ int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weight
     (void)hipGetLastError();
     char* b = reinterpret_cast<char*>(ws);
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
-    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, stream_of(hip_stream));
+    int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
+    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, queue, stream_of(hip_stream));
     run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
-                    slot_by_expert, row_of, y, b + p.o, nullptr, nullptr, stream_of(hip_stream));
+                    slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
     return launched();
 }
 
@@ -300,9 +315,10 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
     (void)hipGetLastError();
     char* b = reinterpret_cast<char*>(ws);
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
-    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, stream_of(hip_stream));
+    int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
+    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, queue, stream_of(hip_stream));
     run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
-                   slot_by_expert, row_of, y, b + p.o, nullptr, nullptr, stream_of(hip_stream));
+                   slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
     return launched();
 }
 

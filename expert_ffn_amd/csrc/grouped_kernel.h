@@ -51,6 +51,7 @@ struct Args {
     const int32_t* offset;
     const int32_t* slot;
     char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order
+    int32_t* queue;       // square tiles: [8][kLine], tiles taken from each XCD's run, zero at the start
     uint8_t* outs;        // e4m3 gate/up: scale bytes of h
     int N, m, S, R, K;
 };
@@ -294,13 +295,15 @@ __global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __re
                                                             const int32_t* __restrict__ hist, int32_t* __restrict__ count,
                                                             int32_t* __restrict__ offset, int32_t* __restrict__ sbe,
                                                             int32_t* __restrict__ distinct, int32_t* __restrict__ u_err,
-                                                            int32_t* __restrict__ row_of) {
+                                                            int32_t* __restrict__ row_of, int32_t* __restrict__ queues,
+                                                            int nq) {
     __shared__ int base[kGWaves * MOE_MAX_EXPERTS];  // [wave][N]: next place of the wave's slots
     __shared__ int part[kGWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int G = gridDim.x, g = blockIdx.x;
     const int64_t chunk = group_chunk(S), s0 = g * chunk;
     const int64_t per = chunk / kGWaves;  // a multiple of 64
+    if (g == 0 && tid < nq) queues[tid] = 0;  // the queues of the products that follow
     for (int i = tid; i < kGWaves * N; i += kGThreads) base[i] = 0;
     __syncthreads();
     // this wave's own histogram
@@ -524,6 +527,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 constexpr int kTM = 256, kTN = 256, kTileThreads = 512;
 constexpr int kStageA = kTM * kUnit, kStage = (kTM + kTN) * kUnit;
 constexpr uint32_t kOOB = 0x80000000u;  // beyond every buffer: reads give zero
+constexpr int kLine = 32;               // words a counter of its own cache line takes
+constexpr int kQueue = 8 * kLine;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
@@ -559,28 +564,68 @@ struct Place {
     int e, r0, rows, ct;  // rows 0: no tile
 };
 
-// The row tiles of every expert, one scan kept by the wave: lane l holds N / 64 experts.
-struct Tiles {
-    int sum, upto, total, C;
+// Every expert's row tiles and what they cost, one scan kept by the wave: lane l holds
+// N / 64 experts.  A unit of a tile takes about the same time up to 64 rows (the weights'
+// way), then more with every 64 (clocks / 100, measured).
+__device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 14 : rows <= 128 ? 17 : rows <= 192 ? 23 : 29; }
 
+struct Tiles {
+    int sum, upto, cost, cost_upto;  // of this lane's experts; up to and with them
+    int total, cost_total, C;
+
+    struct Span {
+        int lo, hi, tiles, cost;
+    };
+    __device__ __forceinline__ static Span span(const Args& a, int lo, int hi) {
+        lo = min(max(lo, 0), a.S);
+        hi = min(max(hi, lo), a.S);
+        const int n = hi - lo, rest = n & (kTM - 1);
+        return Span{lo, hi, (n + kTM - 1) / kTM, n / kTM * tile_cost(kTM) + (rest ? tile_cost(rest) : 0)};
+    }
+    __device__ __forceinline__ static int scan(int v) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(v, o, 64);
+            if (lane >= o) v += u;
+        }
+        return v;
+    }
     __device__ __forceinline__ void count(const Args& a) {
         const int lane = threadIdx.x & 63;
         C = (a.N + 63) / 64;
-        sum = 0;
+        sum = cost = 0;
         for (int i = 0; i < C; ++i) {
             const int e = lane * C + i;
             if (e < a.N) {
-                const int lo = min(max(a.offset[e], 0), a.S), hi = min(max(a.offset[e + 1], lo), a.S);
-                sum += (hi - lo + kTM - 1) / kTM;
+                const Span s = span(a, a.offset[e], a.offset[e + 1]);
+                sum += s.tiles;
+                cost += s.cost;
             }
         }
-        upto = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(upto, o, 64);
-            if (lane >= o) upto += u;
-        }
+        upto = scan(sum);
+        cost_upto = scan(cost);
         total = __builtin_amdgcn_readlane(upto, 63);
+        cost_total = __builtin_amdgcn_readlane(cost_upto, 63);
+    }
+
+    // The tile (row tiles times CT) at cost x / 8 of all.
+    __device__ __forceinline__ int bound(const Args& a, int CT, int x) const {
+        if (x >= 8) return total * CT;
+        const int64_t target = (int64_t)cost_total * CT * x / 8;
+        const uint64_t past = __ballot((int64_t)cost_upto * CT > target);
+        if (!past) return total * CT;
+        const int from = __ffsll((unsigned long long)past) - 1;
+        int t = __builtin_amdgcn_readlane(upto, from) - __builtin_amdgcn_readlane(sum, from);
+        int64_t left = target - (int64_t)(__builtin_amdgcn_readlane(cost_upto, from) - __builtin_amdgcn_readlane(cost, from)) * CT;
+        for (int i = 0; i < C && from * C + i < a.N; ++i) {
+            const int e = from * C + i;
+            const Span s = span(a, uni(a.offset[e]), uni(a.offset[e + 1]));
+            if (left < (int64_t)s.cost * CT) return t * CT + (int)(left * s.tiles / s.cost);
+            left -= (int64_t)s.cost * CT;
+            t += s.tiles;
+        }
+        return t * CT;
     }
 
     // Tile t of CT column tiles each: the column tiles of up to 8 row tiles are neighbours.
@@ -589,18 +634,16 @@ struct Tiles {
         if (t >= total * CT || !past) return Place{0, 0, 0, 0};
         const int from = __ffsll((unsigned long long)past) - 1;
         int k = t - (__builtin_amdgcn_readlane(upto, from) - __builtin_amdgcn_readlane(sum, from)) * CT;
-        for (int i = 0; i < C; ++i) {
+        for (int i = 0; i < C && from * C + i < a.N; ++i) {
             const int e = from * C + i;
-            if (e >= a.N) break;
-            const int lo = min(max(uni(a.offset[e]), 0), a.S), hi = min(max(uni(a.offset[e + 1]), lo), a.S);
-            const int rt = (hi - lo + kTM - 1) / kTM;
-            if (k < rt * CT) {
-                const int sg = k / (8 * CT), in = min(8, rt - 8 * sg);
+            const Span s = span(a, uni(a.offset[e]), uni(a.offset[e + 1]));
+            if (k < s.tiles * CT) {
+                const int sg = k / (8 * CT), in = min(8, s.tiles - 8 * sg);
                 k -= sg * 8 * CT;
-                const int r0 = lo + (8 * sg + k % in) * kTM;
-                return Place{e, uni(r0), uni(min(hi - r0, kTM)), uni(k / in)};
+                const int r0 = s.lo + (8 * sg + k % in) * kTM;
+                return Place{e, r0, min(s.hi - r0, kTM), k / in};
             }
-            k -= rt * CT;
+            k -= s.tiles * CT;
         }
         return Place{0, 0, 0, 0};
     }
@@ -611,6 +654,7 @@ struct TileLds {
     uint8_t xs[2][kTM];     // e4m3: scale bytes of a unit's rows, [wm][row % 16][i]
     float red[4][kTM];      // e4m3 gate/up: |h| maxima of a row's four column groups
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
+    int after;              // the tile after the next
 };
 
 template <bool FP8, bool TILED, bool GU>
@@ -622,17 +666,19 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     const int lr = lane & 15, q = lane >> 4, wm = wave >> 2, wn = wave & 3;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
     const int CT = (a.R + TC - 1) / TC, RB = (a.R + kBlk - 1) / kBlk;
-    // Work groups b, b + 8, ... share an XCD and its L2: each XCD takes a run of tiles.
+    // Work groups b, b + 8, ... share an XCD and its L2: each XCD has a run of tiles of an
+    // eighth of the cost, of which its work groups take two each and then whoever is free
+    // the next (which tile runs where does not change its result).
     Tiles tiles;
     tiles.count(a);
-    const int per = (tiles.total * CT + 7) / 8, xcd = blockIdx.x & 7, step = gridDim.x >> 3;
-    int next_t = blockIdx.x >> 3;  // within the XCD's run
-    auto take = [&]() {  // in scalar registers: buffer descriptors and loops go by it
+    const int xcd = blockIdx.x & 7, mine = blockIdx.x >> 3, step = gridDim.x >> 3;
+    const int run = uni(tiles.bound(a, CT, xcd)), run_end = uni(tiles.bound(a, CT, xcd + 1));
+    auto take = [&](int k) {  // in scalar registers: buffer descriptors and loops go by it
         Place t{0, 0, 0, 0};
-        if (next_t < per) t = tiles.place(a, CT, xcd * per + next_t);
-        next_t += step;
+        if (k < run_end - run) t = tiles.place(a, CT, run + k);
         return Place{uni(t.e), uni(t.r0), uni(t.rows), uni(t.ct)};
     };
+    int after = mine + step;  // the tile after this one
 
     // What a tile's loads go by: offsets are one value a lane (chunk of a row's unit, rows of
     // 8 or a whole 1 KB block) plus one the wave holds.  Rows and weight rows come in eights.
@@ -687,7 +733,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         }
     };
 
-    Place p = take();
+    Place p = take(mine);
     if (!p.rows) return;
     uint32_t gather[4] = {0, 0, 0, 0}, gather_n[4] = {0, 0, 0, 0};  // gate/up: offsets of the rows' tokens
     uint32_t xrow = 0, xrow_n = 0;                                  // e4m3: of this thread's row's scale bytes
@@ -751,6 +797,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         // its own stores, the same number whatever the rows: those of no row are dropped by their bounds
         constexpr int kStores = GU ? (FP8 ? NB / 2 + 1 : NB) : 2 * NB;
         Place pn{0, 0, 0, 0};  // the next tile
+        int got = 0;
         Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
         Weights wr = weights_of(p);
         int at = wr.at;  // of the weights' scale bytes that come next
@@ -833,20 +880,21 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             block_barrier();
             // Rb
             if (u == 0) {
-                pn = take();
+                pn = take(after);
                 ask(pn, gather_n, xrow_n);
+                if (tid == 0) got = atomicAdd(&a.queue[xcd * kLine], 1);
+            } else if (u == 1) {
+                address(gather_n, xrow_n);
+                if (tid == 0) lds.after = got + 2 * step;
+            } else if (ub == U) {
+                wr = weights_of(pn);
+                xa = rows_of(pn);
+                gather[0] = gather_n[0];
+                gather[1] = gather_n[1];
+                if (FP8) xrow = xrow_n;
+                after = uni(lds.after);
             }
-            if (u == 1) address(gather_n, xrow_n);
-            if (ub >= U) {
-                if (ub == U) {
-                    wr = weights_of(pn);
-                    xa = rows_of(pn);
-                    gather[0] = gather_n[0];
-                    gather[1] = gather_n[1];
-                    if (FP8) xrow = xrow_n;
-                }
-                ub -= U;
-            }
+            if (ub >= U) ub -= U;
             read_rows(H, NB);
             if (FP8 && !wm) {
                 lds.xs[par ^ 1][sxat] = (uint8_t)nx;
@@ -970,16 +1018,19 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         else pn = tile(std::integral_constant<int, 8>());
         // values of the wave, which the compiler no longer knows them to be where tiles of several heights meet
         p = Place{uni(pn.e), uni(pn.r0), uni(pn.rows), uni(pn.ct)};
-        next_t = uni(next_t);
+        after = uni(after);
         par = uni(par);
         stores = uni(stores);
     }
     if (!wm) block_barrier();
 }
 
-// The row of each slot that has one.
+__global__ __launch_bounds__(kQueue) void k_zero_queue(int32_t* __restrict__ queue) { queue[threadIdx.x] = 0; }
+
+// The row of each slot that has one; an empty queue.
 __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot, const int32_t* __restrict__ rows,
-                                               int S, int32_t* __restrict__ row_of) {
+                                               int S, int32_t* __restrict__ row_of, int32_t* __restrict__ queue) {
+    if (blockIdx.x == 0) queue[threadIdx.x] = 0;
     const int r = blockIdx.x * 256 + threadIdx.x;
     if (r < min(*rows, S)) row_of[min(max(slot[r], 0), S - 1)] = r;
 }

@@ -252,6 +252,7 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
     S, f = n * layer.m, layer.d_ff
     _check_grouping(grouping, n, layer.m, layer.N, dev)
     desc, L = layer.desc(), lib()
+    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
     if not fp8:
         _check_dev("x", x, torch.bfloat16, (n, layer.d))
         if out is None:
@@ -261,7 +262,7 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
         with _guard(dev):
             check("moe_grouped_gate_up", L.moe_grouped_gate_up(
                 ctypes.byref(desc), ctypes.byref(layer._weights), x.data_ptr(), n, grouping.offset.data_ptr(),
-                grouping.slot_by_expert.data_ptr(), out.data_ptr(), _on(dev, stream)))
+                grouping.slot_by_expert.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream)))
         return out
     _check_quantized("x", x, n, layer.d)
     if out is None:
@@ -269,7 +270,6 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
                         _empty((S, _blocks(f)), torch.uint8, dev, stream))
     _check_quantized("out", out, S, f)
     _same(dev, x=x.q, x_scale=x.scale, out=out.q, out_scale=out.scale)
-    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
     with _guard(dev):
         check("moe_grouped_gate_up_fp8", L.moe_grouped_gate_up_fp8(
             ctypes.byref(desc), ctypes.byref(layer._weights), x.q.data_ptr(), x.scale.data_ptr(), n,

@@ -384,7 +384,8 @@ size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  * MOE_E_HIP.
  */
 int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, int32_t n,
-                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* hip_stream);
+                        const int32_t* offset, const int32_t* slot_by_expert, void* h, void* ws, size_t ws_bytes,
+                        void* hip_stream);
 int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* xq,
                             const uint8_t* x_scale, int32_t n, const int32_t* offset, const int32_t* slot_by_expert,
                             void* hq, uint8_t* h_scale, void* ws, size_t ws_bytes, void* hip_stream);

@@ -37,7 +37,8 @@ def _calls(desc, n, only=("gate_up", "down", "pass"), **kw):
     else:
         W = _abi.LayerWeights(a["w"], a["w"], a["w"])
         f = {
-            "gate_up": lambda: L.moe_grouped_gate_up(dp, ctypes.byref(W), a["x"], n, a["off"], a["sbe"], a["h"], None),
+            "gate_up": lambda: L.moe_grouped_gate_up(dp, ctypes.byref(W), a["x"], n, a["off"], a["sbe"], a["h"],
+                                                     a["ws"], a["size"], None),
             "down": lambda: L.moe_grouped_down(dp, ctypes.byref(W), a["h"], a["ids"], a["rw"], n, a["off"], a["sbe"],
                                                a["y"], a["ws"], a["size"], None),
             "pass": lambda: L.moe_expert_grouped(dp, ctypes.byref(W), a["x"], a["ids"], a["rw"], n, a["y"], None,
@@ -86,9 +87,9 @@ def test_pointers_and_workspace(dtype):
     need = _abi.lib().moe_grouped_workspace_bytes(ctypes.byref(d), 4)
     assert need > 0 and need % 256 == 0
     used = {"w": "gate_up down pass", "x": "gate_up pass", "h": "gate_up down", "ids": "down pass", "rw": "down pass",
-            "y": "down pass", "off": "gate_up down", "sbe": "gate_up down", "ws": "down pass"}
+            "y": "down pass", "off": "gate_up down", "sbe": "gate_up down", "ws": "gate_up down pass"}
     if dtype == _abi.MOE_FP8:
-        used.update(s="gate_up down pass", xs="gate_up", hs="gate_up down", ws="gate_up down pass")
+        used.update(s="gate_up down pass", xs="gate_up", hs="gate_up down")
     used = {k: v.split() for k, v in used.items()}
     for name, where in used.items():
         assert set(_calls(d, 4, where, **{name: None}).values()) == {INVAL}, name
