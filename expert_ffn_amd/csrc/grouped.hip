@@ -48,22 +48,21 @@ int check_desc(const moe_layer_desc* d, int32_t n, int32_t dtype) {
 int group_chunks(int64_t S) { return (int)((S + group_chunk(S) - 1) / group_chunk(S)); }
 size_t group_ws(int64_t S, int N) { return align_up((size_t)group_chunks(S) * (N + 1) * 4); }
 
-void run_group(const int32_t* ids, int64_t S, int m, int N, int32_t* count, int32_t* offset, int32_t* sbe,
-               int32_t* distinct, int32_t* u_err, int32_t* row_of, int32_t* queues, int nq, void* ws, hipStream_t st) {
-    int32_t* hist = reinterpret_cast<int32_t*>(ws);
-    const int G = group_chunks(S);
-    hipLaunchKernelGGL(k_group_hist, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist);
-    hipLaunchKernelGGL(k_group_scatter, dim3(G), dim3(kGThreads), 0, st, ids, S, m, N, hist, count, offset, sbe,
-                       distinct, u_err, row_of, queues, nq);
+int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
+    return (int)std::min<int64_t>((rows * blocks_of(K) + 15) / 16, 16384);
+}
+
+void run_group(Group g, hipStream_t st) {
+    g.G = group_chunks(g.S);
+    // work groups of 1024 threads for the rows to quantise: 64 blocks of 128 at a time
+    const int quant = g.x ? (int)std::min<int64_t>((g.n * blocks_of(g.d) + 63) / 64, 1024) : 0;
+    if (g.G > 1) hipLaunchKernelGGL(k_group_hist, dim3(g.G + quant), dim3(kGThreads), 0, st, g);
+    hipLaunchKernelGGL(k_group_scatter, dim3(g.G > 1 ? g.G : 1 + quant), dim3(kGThreads), 0, st, g);
 }
 
 void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of, int32_t* queue, hipStream_t st) {
     static_assert(kQueue == 256, "");
     hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of, queue);
-}
-
-int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
-    return (int)std::min<int64_t>((rows * blocks_of(K) + 15) / 16, 16384);
 }
 
 // Workspace of a whole pass, and of the products alone (which use hf and O).
@@ -193,12 +192,28 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(b + at); };
     auto u8 = [&](size_t at) { return reinterpret_cast<uint8_t*>(b + at); };
     (void)hipGetLastError();
-    run_group(ids, (int64_t)n * d->m, d->m, d->N, i32(p.count), i32(p.offset), i32(p.sbe), i32(p.distinct),
-              i32(p.u_err), i32(p.row_of), i32(p.queue), 2 * kQueue, b + p.hist, st);
-    if (FP8)
-        hipLaunchKernelGGL(k_quant_rows<false>, dim3(rows_grid(n, d->d_model)), dim3(256), 0, st,
-                           reinterpret_cast<const char*>(x), (int64_t)n, d->d_model,
-                           static_cast<const int32_t*>(nullptr), u8(p.xq), u8(p.xs));
+    Group g{};
+    g.ids = ids;
+    g.S = (int64_t)n * d->m;
+    g.m = d->m;
+    g.N = d->N;
+    g.hist = i32(p.hist);
+    g.count = i32(p.count);
+    g.offset = i32(p.offset);
+    g.sbe = i32(p.sbe);
+    g.distinct = i32(p.distinct);
+    g.u_err = i32(p.u_err);
+    g.row_of = i32(p.row_of);
+    g.queues = i32(p.queue);
+    g.nq = 2 * kQueue;
+    if (FP8) {
+        g.x = reinterpret_cast<const char*>(x);
+        g.xq = u8(p.xq);
+        g.xs = u8(p.xs);
+        g.n = n;
+        g.d = d->d_model;
+    }
+    run_group(g, st);
     run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
                      b + p.h, u8(p.hs), b + p.hf, i32(p.queue), st);
     run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y,
@@ -231,8 +246,18 @@ int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t
     rc = check_ws(ws, ws_bytes, group_ws((int64_t)n * m, N));
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
-    run_group(ids, (int64_t)n * m, m, N, count, offset, slot_by_expert, distinct, u_and_err, nullptr, nullptr,
-              0, ws, stream_of(hip_stream));
+    Group g{};
+    g.ids = ids;
+    g.S = (int64_t)n * m;
+    g.m = m;
+    g.N = N;
+    g.hist = reinterpret_cast<int32_t*>(ws);
+    g.count = count;
+    g.offset = offset;
+    g.sbe = slot_by_expert;
+    g.distinct = distinct;
+    g.u_err = u_and_err;
+    run_group(g, stream_of(hip_stream));
     return launched();
 }
 

@@ -117,16 +117,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 }
 
 // Rows of bf16 (or float32) values to codes and scale bytes, in blocks of 128 along the row:
-// sixteen lanes a block, eight values a lane.
+// sixteen lanes a block, eight values a lane; work group g of G.
 template <bool F32>
-__global__ __launch_bounds__(256) void k_quant_rows(const char* __restrict__ x, int64_t rows, int K,
-                                                   const int32_t* __restrict__ limit, uint8_t* __restrict__ q,
-                                                   uint8_t* __restrict__ s) {
-    const int KB = (K + kBlk - 1) / kBlk;
-    if (limit) rows = min(rows, (int64_t)max(*limit, 0));
+__device__ __forceinline__ void quant_rows(const char* __restrict__ x, int64_t rows, int K, uint8_t* __restrict__ q,
+                                           uint8_t* __restrict__ s, int64_t g, int64_t G) {
+    const int KB = (K + kBlk - 1) / kBlk, per = blockDim.x / 16;
     const int64_t blocks = rows * KB;
     const int l = threadIdx.x & 15;
-    for (int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; b < blocks; b += (int64_t)gridDim.x * 16) {
+    for (int64_t b = g * per + threadIdx.x / 16; b < blocks; b += G * per) {
         const int64_t row = b / KB;
         const int kb = (int)(b - row * KB), c = kb * kBlk + l * 8;
         float v[8];
@@ -156,6 +154,15 @@ __global__ __launch_bounds__(256) void k_quant_rows(const char* __restrict__ x, 
                 u32x2{codes4(v[0], v[1], v[2], v[3], inv), codes4(v[4], v[5], v[6], v[7], inv)};
         if (l == 0) s[b] = (uint8_t)(k + 127);
     }
+}
+
+// `limit`: rows in use, where only the device knows (null: all)
+template <bool F32>
+__global__ __launch_bounds__(256) void k_quant_rows(const char* __restrict__ x, int64_t rows, int K,
+                                                   const int32_t* __restrict__ limit, uint8_t* __restrict__ q,
+                                                   uint8_t* __restrict__ s) {
+    if (limit) rows = min(rows, (int64_t)max(*limit, 0));
+    quant_rows<F32>(x, rows, K, q, s, blockIdx.x, gridDim.x);
 }
 
 // Codes and scale bytes of rows back to bf16: four bits of significand fit bf16's eight,
@@ -223,51 +230,77 @@ __global__ __launch_bounds__(256) void k_quant_weights(const char* __restrict__ 
 // --- grouping of any number of slots -------------------------------------------------
 // A stable counting sort over G chunks of slots, one work group of 16 waves each, the
 // waves on consecutive pieces of the chunk: first every chunk's histogram, then every
-// chunk adds up the chunks before it and writes its slots behind them.  The rank of a
-// slot among equal ids of its wave's 64 comes from one ballot for each bit of the id, so
-// the order is that of the slots, whatever the timing.
+// chunk adds up the chunks before it and writes its slots behind them; one chunk needs
+// one launch.  The rank of a slot among equal ids of its wave's 64 comes from one ballot
+// for each bit of the id, so the order is that of the slots, whatever the timing.
+//
+// Latency is the time (a few loads, scans and barriers), so a pass's other preparation
+// rides along: work groups from G on quantise x, and the first clears the queues.
 constexpr int kGThreads = 1024, kGWaves = kGThreads / 64;
-constexpr int kGMaxChunks = 64;
+constexpr int kGMaxChunks = 64, kGOne = 8192;  // slots of one chunk
 
 __host__ __device__ __forceinline__ int64_t group_chunk(int64_t S) {
-    const int64_t c = (S + kGMaxChunks - 1) / kGMaxChunks;
+    const int64_t c = S <= kGOne ? S : (S + kGMaxChunks - 1) / kGMaxChunks;
     return (c + kGThreads - 1) / kGThreads * kGThreads;
 }
 
-// ids of this lane's slot, -1 outside [0, N) or past the end; sets bad for an invalid or
-// repeated id
-__device__ __forceinline__ int group_id(const int32_t* ids, int64_t s, int64_t S, int m, int N, bool& bad) {
-    if (s >= S) return -1;
-    const int id = ids[s];
-    if (id < 0 || id >= N) {
-        bad = true;
-        return -1;
-    }
-    const int j = (int)(s % m);
-    for (int i = 1; i <= j; ++i)
-        if (ids[s - i] == id) bad = true;
-    return id;
+struct Group {
+    const int32_t* ids;
+    int64_t S;
+    int m, N, G;            // G chunks
+    int32_t* hist;          // [G][N + 1], with more than one chunk
+    int32_t *count, *offset, *sbe, *distinct, *u_err;
+    int32_t* row_of;        // null, or the row of each slot
+    int32_t* queues;        // null, or nq words to clear
+    int nq;
+    const char* x;          // null, or rows to quantise (n rows of d)
+    uint8_t *xq, *xs;
+    int n, d;
+};
+
+__device__ __forceinline__ bool group_quant(const Group& g) {
+    if ((int)blockIdx.x < g.G) return false;
+    quant_rows<false>(g.x, g.n, g.d, g.xq, g.xs, blockIdx.x - g.G, gridDim.x - g.G);
+    return true;
 }
 
-__global__ __launch_bounds__(kGThreads) void k_group_hist(const int32_t* __restrict__ ids, int64_t S, int m, int N,
-                                                         int32_t* __restrict__ hist) {
-    __shared__ int cnt[MOE_MAX_EXPERTS];
-    __shared__ int flag;
-    const int tid = threadIdx.x;
-    const int64_t chunk = group_chunk(S), s0 = blockIdx.x * chunk;
-    for (int e = tid; e < N; e += kGThreads) cnt[e] = 0;
-    if (tid == 0) flag = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int64_t i = tid; i < chunk; i += kGThreads) {
-        const int id = group_id(ids, s0 + i, S, m, N, bad);
-        if (id >= 0) atomicAdd(&cnt[id], 1);
+// Whether slot s (its id valid) repeats an id of its token; eight loads at a time.
+__device__ __forceinline__ bool group_repeat(const int32_t* __restrict__ ids, int64_t s, int m, int id) {
+    const int j = (int)(s % m);
+    bool again = false;
+    for (int i0 = 1; i0 <= j; i0 += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ids[s - min(i0 + i, j)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) again |= v[i] == id;
     }
-    if (bad) atomicOr(&flag, 1);
+    return again;
+}
+
+__global__ __launch_bounds__(kGThreads) void k_group_hist(Group g) {
+    __shared__ int cnt[MOE_MAX_EXPERTS];
+    if (group_quant(g)) return;
+    const int tid = threadIdx.x;
+    const int64_t chunk = group_chunk(g.S), s0 = blockIdx.x * chunk;
+    for (int e = tid; e < g.N; e += kGThreads) cnt[e] = 0;
     __syncthreads();
-    int32_t* h = hist + (int64_t)blockIdx.x * (N + 1);
-    for (int e = tid; e < N; e += kGThreads) h[e] = cnt[e];
-    if (tid == 0) h[N] = flag;
+    int bad = 0;
+    for (int64_t i = tid; i < chunk; i += kGThreads) {
+        const int64_t s = s0 + i;
+        if (s >= g.S) break;
+        const int id = g.ids[s];
+        if (id >= 0 && id < g.N) {
+            atomicAdd(&cnt[id], 1);
+            bad |= group_repeat(g.ids, s, g.m, id);
+        } else {
+            bad = 1;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    int32_t* h = g.hist + (int64_t)blockIdx.x * (g.N + 1);
+    for (int e = tid; e < g.N; e += kGThreads) h[e] = cnt[e];
+    if (tid == 0) h[g.N] = bad;
 }
 
 // Exclusive sums over the work group of one value a thread; total to all.
@@ -282,6 +315,7 @@ __device__ __forceinline__ int group_scan(int v, int* part, int& total) {
     if (lane == 63) part[wave] = s;
     __syncthreads();
     int before = 0, all = 0;
+#pragma unroll
     for (int i = 0; i < kGWaves; ++i) {
         before += i < wave ? part[i] : 0;
         all += part[i];
@@ -291,66 +325,95 @@ __device__ __forceinline__ int group_scan(int v, int* part, int& total) {
     return before + s - v;
 }
 
-__global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __restrict__ ids, int64_t S, int m, int N,
-                                                            const int32_t* __restrict__ hist, int32_t* __restrict__ count,
-                                                            int32_t* __restrict__ offset, int32_t* __restrict__ sbe,
-                                                            int32_t* __restrict__ distinct, int32_t* __restrict__ u_err,
-                                                            int32_t* __restrict__ row_of, int32_t* __restrict__ queues,
-                                                            int nq) {
+__global__ __launch_bounds__(kGThreads) void k_group_scatter(Group g) {
     __shared__ int base[kGWaves * MOE_MAX_EXPERTS];  // [wave][N]: next place of the wave's slots
+    __shared__ int sums[2][kGThreads];
     __shared__ int part[kGWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int G = gridDim.x, g = blockIdx.x;
-    const int64_t chunk = group_chunk(S), s0 = g * chunk;
-    const int64_t per = chunk / kGWaves;  // a multiple of 64
-    if (g == 0 && tid < nq) queues[tid] = 0;  // the queues of the products that follow
+    if (g.G == 1 && group_quant(g)) return;  // with more chunks the first launch has quantised
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, N = g.N;
+    const int64_t chunk = group_chunk(g.S), s0 = blockIdx.x * chunk;
+    const int64_t per = chunk / kGWaves, w0 = s0 + wave * per;  // per: a multiple of 64
+    const bool first = blockIdx.x == 0;
+    if (first)
+        for (int i = tid; i < g.nq; i += kGThreads) g.queues[i] = 0;
     for (int i = tid; i < kGWaves * N; i += kGThreads) base[i] = 0;
+    // Every chunk's counts of expert e: P threads an expert, each a part of the chunks,
+    // with its loads in flight together.
+    int bad = 0, lo = 0, hi = 0;
+    const int P = kGThreads / N;  // >= 1
+    const int pe = tid % N, pp = tid / N;
+    if (g.G > 1 && pp < P) {
+        for (int c0 = pp; c0 < g.G; c0 += 8 * P) {
+            int v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = g.hist[(int64_t)min(c0 + i * P, g.G - 1) * (N + 1) + pe];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = c0 + i * P;
+                if (c < g.G) {
+                    hi += v[i];
+                    lo += c < (int)blockIdx.x ? v[i] : 0;
+                }
+            }
+        }
+    }
+    if (g.G > 1 && first && tid < g.G) bad = g.hist[(int64_t)tid * (N + 1) + N];
+    sums[0][tid] = lo;
+    sums[1][tid] = hi;
     __syncthreads();
     // this wave's own histogram
     for (int64_t i = lane; i < per; i += 64) {
-        const int64_t s = s0 + wave * per + i;
-        const int id = s < S ? ids[s] : -1;
-        if (id >= 0 && id < N) atomicAdd(&base[wave * N + id], 1);
+        const int64_t s = w0 + i;
+        if (s >= g.S) break;
+        const int id = g.ids[s];
+        const bool ok = id >= 0 && id < N;
+        if (ok) atomicAdd(&base[wave * N + id], 1);
+        if (g.G == 1) bad |= ok ? group_repeat(g.ids, s, g.m, id) : 1;
     }
+    bad = __syncthreads_or(bad);
     // thread e: expert e's slots in the chunks before this one, and in all
-    int before = 0, all = 0, bad = 0;
-    if (tid < N)
-        for (int c = 0; c < G; ++c) {
-            const int v = hist[(int64_t)c * (N + 1) + tid];
-            before += c < g ? v : 0;
-            all += v;
+    int before = 0, all = 0;
+    if (tid < N) {
+        if (g.G > 1) {
+            for (int i = 0; i < P; ++i) {
+                before += sums[0][i * N + tid];
+                all += sums[1][i * N + tid];
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < kGWaves; ++w) all += base[w * N + tid];
         }
-    int valid;
+    }
+    int valid, U;
     const int start = group_scan(all, part, valid);
-    int U;
     const int dpos = group_scan(tid < N && all > 0, part, U);
     if (tid < N) {
+        int c[kGWaves];
+#pragma unroll
+        for (int w = 0; w < kGWaves; ++w) c[w] = base[w * N + tid];
         int at = start + before;
+#pragma unroll
         for (int w = 0; w < kGWaves; ++w) {
-            const int c = base[w * N + tid];
             base[w * N + tid] = at;
-            at += c;
+            at += c[w];
         }
-        if (g == 0) {
-            count[tid] = all;
-            offset[tid] = start;
-            if (all > 0) distinct[dpos] = tid;
-            if (tid >= U) distinct[tid] = -1;
+        if (first) {
+            g.count[tid] = all;
+            g.offset[tid] = start;
+            if (all > 0) g.distinct[dpos] = tid;
+            if (tid >= U) g.distinct[tid] = -1;
         }
     }
-    if (g == 0) {
-        if (tid < G) bad = hist[(int64_t)tid * (N + 1) + N];
-        bad = __syncthreads_or(bad);
-        if (tid == 0) {
-            offset[N] = valid;
-            u_err[0] = U;
-            u_err[1] = bad ? MOE_E_IDS : MOE_OK;
-        }
+    if (first && tid == 0) {
+        g.offset[N] = valid;
+        g.u_err[0] = U;
+        g.u_err[1] = bad ? MOE_E_IDS : MOE_OK;
     }
     __syncthreads();
     for (int64_t i = lane; i < per; i += 64) {
-        const int64_t s = s0 + wave * per + i;
-        int id = s < S ? ids[s] : -1;
+        const int64_t s = w0 + i;
+        const int id = s < g.S ? g.ids[s] : -1;
         const bool ok = id >= 0 && id < N;
         uint64_t same = __ballot(ok);
         for (int b = 0; (1 << b) < N; ++b) {
@@ -360,8 +423,8 @@ __global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __re
         if (ok) {
             const uint64_t under = same & ((1ull << lane) - 1);
             const int at = base[wave * N + id];
-            sbe[at + __popcll(under)] = (int)s;
-            if (row_of) row_of[s] = at + __popcll(under);
+            g.sbe[at + __popcll(under)] = (int)s;
+            if (g.row_of) g.row_of[s] = at + __popcll(under);
             __builtin_amdgcn_wave_barrier();
             if (under == 0) base[wave * N + id] = at + __popcll(same);
         }
@@ -369,7 +432,7 @@ __global__ __launch_bounds__(kGThreads) void k_group_scatter(const int32_t* __re
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     // the places that no slot takes
-    for (int64_t r = valid + (int64_t)g * kGThreads + tid; r < S; r += (int64_t)G * kGThreads) sbe[r] = -1;
+    for (int64_t r = valid + (int64_t)blockIdx.x * kGThreads + tid; r < g.S; r += (int64_t)g.G * kGThreads) g.sbe[r] = -1;
 }
 
 // --- products ------------------------------------------------------------------------

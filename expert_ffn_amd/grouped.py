@@ -19,6 +19,7 @@ from .ops import Grouping, Layer, _check_dev
 Quantized = namedtuple("Quantized", ["q", "scale"])
 
 _NO_GUARD = contextlib.nullcontext()
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
 def _blocks(v):
@@ -44,27 +45,41 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _same(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+def _check(name, t, dtype, shape, dev):
+    """One tensor of a call: contiguous, of this type, shape and device.  Small calls are
+    bound by the host, so what is right is found right in one expression."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _check_dev(name, t, dtype, shape)
+    raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
 
 
-def _ws(ws, nbytes, where, dev, stream):
-    if nbytes == 0:
-        raise _abi.MoeError(where, _abi.MOE_E_INVAL)
+def _ws(ws, desc, n, dev, stream):
+    """Workspace of a grouped call (its size is checked by the call itself)."""
     if ws is None:
-        return _empty(nbytes, torch.uint8, dev, stream)
-    _check_dev("ws", ws, torch.uint8)
-    _same(dev, ws=ws)
+        nb = lib().moe_grouped_workspace_bytes(ctypes.byref(desc), n)
+        if nb == 0:
+            raise _abi.MoeError("moe_grouped_workspace_bytes", _abi.MOE_E_INVAL)
+        return _empty(nb, _U8, dev, stream)
+    if not (ws.dtype is _U8 and ws.device == dev and ws.is_contiguous()):
+        _check_dev("ws", ws, _U8)
+        raise ValueError("ws is on %s, expected %s" % (ws.device, dev))
     return ws
 
 
-def _check_quantized(name, v, rows, K):
+def _check_quantized(name, v, rows, K, dev):
     if not isinstance(v, Quantized):
         raise TypeError("%s must be Quantized (codes and scale bytes), got %s" % (name, type(v).__name__))
-    _check_dev(name + ".q", v.q, torch.float8_e4m3fn, (rows, K))
-    _check_dev(name + ".scale", v.scale, torch.uint8, (rows, _blocks(K)))
+    return (_check(name + ".q", v.q, _E4M3, (rows, K), dev),
+            _check(name + ".scale", v.scale, _U8, (rows, _blocks(K)), dev))
+
+
+def _check_grouping(g, n, m, N, dev):
+    if not isinstance(g, Grouping):
+        raise TypeError("grouping must be Grouping, got %s" % type(g).__name__)
+    return (_check("count", g.count, _I32, (N,), dev), _check("offset", g.offset, _I32, (N + 1,), dev),
+            _check("slot_by_expert", g.slot_by_expert, _I32, (n * m,), dev),
+            _check("distinct", g.distinct, _I32, (N,), dev), _check("u_and_err", g.u_and_err, _I32, (2,), dev))
 
 
 class Fp8Layer:
@@ -81,9 +96,9 @@ class Fp8Layer:
         self.N, self.m, self.d, self.d_ff = N, int(m), d, d_ff
         self.tiled = bool(tiled)
         for name, (q, s), (R, K) in (("gate", gate, (d_ff, d)), ("up", up, (d_ff, d)), ("down", down, (d, d_ff))):
-            _check_dev("w_" + name, q, torch.float8_e4m3fn, (N, R, K))
-            _check_dev("s_" + name, s, torch.uint8, (N, _blocks(R), _blocks(K)))
-            _same(gate[0].device, **{"w_" + name: q, "s_" + name: s})
+            _check_dev("w_" + name, q, _E4M3)
+            _check("w_" + name, q, _E4M3, (N, R, K), gate[0].device)
+            _check("s_" + name, s, _U8, (N, _blocks(R), _blocks(K)), gate[0].device)
         self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
         self._weights = _abi.Fp8Weights(*(m_[i].data_ptr() for i in (0, 1) for m_ in (self.gate, self.up, self.down)))
 
@@ -96,6 +111,7 @@ class Fp8Layer:
         return 3 * self.d * self.d_ff + sum(p[1][0].numel() for p in (self.gate, self.up, self.down))
 
     def desc(self, accumulate=False):
+        """The layer's descriptor (``moe_layer_desc``)."""
         flags = (_abi.MOE_FLAG_ACCUMULATE if accumulate else 0) | (_abi.MOE_FLAG_TILED if self.tiled else 0)
         return _abi.LayerDesc(self.N, self.m, self.d, self.d_ff, _abi.MOE_FP8, flags, 0)
 
@@ -107,7 +123,7 @@ class Fp8Layer:
         desc, dev = self.desc(), self.device
 
         def tl(pair, mat):
-            out = _empty(pair[0].shape, torch.float8_e4m3fn, dev, stream)
+            out = _empty(pair[0].shape, _E4M3, dev, stream)
             with _guard(dev):
                 check("moe_pack_tiled", lib().moe_pack_tiled(ctypes.byref(desc), pair[0].data_ptr(), out.data_ptr(),
                                                              mat, _on(dev, stream)))
@@ -123,13 +139,13 @@ class Fp8Layer:
 def quant_weights(w, stream=None):
     """bf16 matrices [N][R][K] to (codes, scale bytes [N][R/128][K/128]), one power of
     two for each block of 128 x 128 (``moe_quant_weights``)."""
-    _check_dev("w", w, torch.bfloat16)
+    _check_dev("w", w, _BF16)
     if w.dim() != 3:
         raise ValueError("w must be [N][R][K], got %s" % (tuple(w.shape),))
     N, R, K = w.shape
     dev = w.device
-    q = _empty((N, R, K), torch.float8_e4m3fn, dev, stream)
-    s = _empty((N, _blocks(R), _blocks(K)), torch.uint8, dev, stream)
+    q = _empty((N, R, K), _E4M3, dev, stream)
+    s = _empty((N, _blocks(R), _blocks(K)), _U8, dev, stream)
     with _guard(dev):
         check("moe_quant_weights", lib().moe_quant_weights(w.data_ptr(), N, R, K, q.data_ptr(), s.data_ptr(),
                                                            _on(dev, stream)))
@@ -148,20 +164,16 @@ def fp8_copy(layer, stream=None):
 def quant_rows(x, out=None, stream=None):
     """Rows of bf16 values [rows][K] to ``Quantized``, one power of two for each block of
     128 along a row (``moe_quant_rows``)."""
-    _check_dev("x", x, torch.bfloat16)
+    _check_dev("x", x, _BF16)
     if x.dim() != 2:
         raise ValueError("x must be [rows][K], got %s" % (tuple(x.shape),))
     rows, K = x.shape
     dev = x.device
     if out is None:
-        out = Quantized(_empty((rows, K), torch.float8_e4m3fn, dev, stream),
-                        _empty((rows, _blocks(K)), torch.uint8, dev, stream))
-    else:
-        _check_quantized("out", out, rows, K)
-        _same(dev, q=out.q, scale=out.scale)
+        out = Quantized(_empty((rows, K), _E4M3, dev, stream), _empty((rows, _blocks(K)), _U8, dev, stream))
+    q, s = _check_quantized("out", out, rows, K, dev)
     with _guard(dev):
-        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, K, out.q.data_ptr(), out.scale.data_ptr(),
-                                                     _on(dev, stream)))
+        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, K, q, s, _on(dev, stream)))
     return out
 
 
@@ -170,17 +182,14 @@ def dequant_rows(v, out=None, stream=None):
     if not isinstance(v, Quantized) or v.q.dim() != 2:
         raise TypeError("dequant_rows takes Quantized rows")
     rows, K = v.q.shape
-    _check_quantized("v", v, rows, K)
     dev = v.q.device
-    _same(dev, scale=v.scale)
+    _check_dev("v.q", v.q)
+    q, s = _check_quantized("v", v, rows, K, dev)
     if out is None:
-        out = _empty((rows, K), torch.bfloat16, dev, stream)
-    else:
-        _check_dev("out", out, torch.bfloat16, (rows, K))
-        _same(dev, out=out)
+        out = _empty((rows, K), _BF16, dev, stream)
+    x = _check("out", out, _BF16, (rows, K), dev)
     with _guard(dev):
-        check("moe_dequant_rows", lib().moe_dequant_rows(v.q.data_ptr(), v.scale.data_ptr(), rows, K, out.data_ptr(),
-                                                         _on(dev, stream)))
+        check("moe_dequant_rows", lib().moe_dequant_rows(q, s, rows, K, x, _on(dev, stream)))
     return out
 
 
@@ -195,27 +204,24 @@ def group_workspace(n, m, N, device="cuda"):
 def group_slots(ids, N, out=None, ws=None, stream=None):
     """``route_group`` for any number of slots (``moe_group_slots``): ids int32 [n][m];
     ids outside [0, N) take no part."""
-    _check_dev("ids", ids, torch.int32)
+    _check_dev("ids", ids, _I32)
     if ids.dim() != 2:
         raise ValueError("ids must be [n][m], got %s" % (tuple(ids.shape),))
     n, m = ids.shape
-    dev = ids.device
-    ws = _ws(ws, lib().moe_group_workspace_bytes(n, m, int(N)), "moe_group_workspace_bytes", dev, stream)
-    sizes = (N, N + 1, n * m, N, 2)
+    N, dev = int(N), ids.device
+    if ws is None:
+        nb = lib().moe_group_workspace_bytes(n, m, N)
+        if nb == 0:
+            raise _abi.MoeError("moe_group_workspace_bytes", _abi.MOE_E_INVAL)
+        ws = _empty(nb, _U8, dev, stream)
     if out is None:
-        out = Grouping(*(_empty(k, torch.int32, dev, stream) for k in sizes))
-    else:
-        _check_grouping(out, n, m, N, dev)
+        out = Grouping(*(_empty(k, _I32, dev, stream) for k in (N, N + 1, n * m, N, 2)))
+    ptrs = _check_grouping(out, n, m, N, dev)
+    wsp = _check("ws", ws, _U8, ws.shape, dev)
     with _guard(dev):
-        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), n, m, int(N), *(t.data_ptr() for t in out),
-                                                       ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), n, m, N, *ptrs, wsp, ws.numel(),
+                                                       _on(dev, stream)))
     return out
-
-
-def _check_grouping(g, n, m, N, dev):
-    for name, t, k in zip(Grouping._fields, g, (N, N + 1, n * m, N, 2)):
-        _check_dev(name, t, torch.int32, (k,))
-        _same(dev, **{name: t})
 
 
 def _kind(layer):
@@ -224,7 +230,7 @@ def _kind(layer):
         return True, layer.device
     if not isinstance(layer, Layer):
         raise TypeError("layer must be Layer or Fp8Layer, got %s" % type(layer).__name__)
-    if layer.dtype != torch.bfloat16:
+    if layer.dtype != _BF16:
         raise TypeError("grouped calls take bf16 or 8-bit weights, got %s" % layer.dtype)
     if layer.packed:
         raise ValueError("grouped calls take plain or tiled weights, not a packed W_down")
@@ -237,10 +243,7 @@ def _kind(layer):
 def grouped_workspace(layer, n):
     """Workspace of the grouped calls for passes of up to n tokens."""
     _, dev = _kind(layer)
-    nb = lib().moe_grouped_workspace_bytes(ctypes.byref(layer.desc()), int(n))
-    if nb == 0:
-        raise _abi.MoeError("moe_grouped_workspace_bytes", _abi.MOE_E_INVAL)
-    return torch.empty(nb, dtype=torch.uint8, device=dev)
+    return _ws(None, layer.desc(), int(n), dev, None)
 
 
 def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
@@ -249,49 +252,34 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
     offset[N] on are left as they were."""
     fp8, dev = _kind(layer)
     n = (x.q if isinstance(x, Quantized) else x).shape[0]
-    S, f = n * layer.m, layer.d_ff
-    _check_grouping(grouping, n, layer.m, layer.N, dev)
+    S, d, f = n * layer.m, layer.d, layer.d_ff
+    _, offset, slots, _, _ = _check_grouping(grouping, n, layer.m, layer.N, dev)
     desc, L = layer.desc(), lib()
-    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
-    if not fp8:
-        _check_dev("x", x, torch.bfloat16, (n, layer.d))
+    if fp8:
+        xs = _check_quantized("x", x, n, d, dev)
         if out is None:
-            out = _empty((S, f), torch.bfloat16, dev, stream)
-        _check_dev("out", out, torch.bfloat16, (S, f))
-        _same(dev, x=x, out=out)
-        with _guard(dev):
-            check("moe_grouped_gate_up", L.moe_grouped_gate_up(
-                ctypes.byref(desc), ctypes.byref(layer._weights), x.data_ptr(), n, grouping.offset.data_ptr(),
-                grouping.slot_by_expert.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream)))
-        return out
-    _check_quantized("x", x, n, layer.d)
-    if out is None:
-        out = Quantized(_empty((S, f), torch.float8_e4m3fn, dev, stream),
-                        _empty((S, _blocks(f)), torch.uint8, dev, stream))
-    _check_quantized("out", out, S, f)
-    _same(dev, x=x.q, x_scale=x.scale, out=out.q, out_scale=out.scale)
+            out = Quantized(_empty((S, f), _E4M3, dev, stream), _empty((S, _blocks(f)), _U8, dev, stream))
+        hs = _check_quantized("out", out, S, f, dev)
+        name, call = "moe_grouped_gate_up_fp8", L.moe_grouped_gate_up_fp8
+    else:
+        xs = (_check("x", x, _BF16, (n, d), dev),)
+        if out is None:
+            out = _empty((S, f), _BF16, dev, stream)
+        hs = (_check("out", out, _BF16, (S, f), dev),)
+        name, call = "moe_grouped_gate_up", L.moe_grouped_gate_up
+    ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check("moe_grouped_gate_up_fp8", L.moe_grouped_gate_up_fp8(
-            ctypes.byref(desc), ctypes.byref(layer._weights), x.q.data_ptr(), x.scale.data_ptr(), n,
-            grouping.offset.data_ptr(), grouping.slot_by_expert.data_ptr(), out.q.data_ptr(), out.scale.data_ptr(),
-            ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *xs, n, offset, slots, *hs, ws.data_ptr(),
+                         ws.numel(), _on(dev, stream)))
     return out
-
-
-def _check_routing(layer, ids, w, n, dev):
-    _check_dev("ids", ids, torch.int32, (n, layer.m))
-    _check_dev("w", w, torch.float32, (n, layer.m))
-    _same(dev, ids=ids, w=w)
 
 
 def _check_y(layer, y, n, dev, accumulate, stream):
     if y is None:
         if accumulate:
             raise ValueError("accumulate=True needs y")
-        return _empty((n, layer.d), torch.bfloat16, dev, stream)
-    _check_dev("y", y, torch.bfloat16, (n, layer.d))
-    _same(dev, y=y)
-    return y
+        y = _empty((n, layer.d), _BF16, dev, stream)
+    return y, _check("y", y, _BF16, (n, layer.d), dev)
 
 
 def grouped_down(layer, h, ids, w, grouping, y=None, ws=None, accumulate=False, stream=None):
@@ -299,24 +287,20 @@ def grouped_down(layer, h, ids, w, grouping, y=None, ws=None, accumulate=False, 
     the routing weights w (``moe_grouped_down``); ``accumulate`` adds to y."""
     fp8, dev = _kind(layer)
     n, m, f = ids.shape[0], layer.m, layer.d_ff
-    _check_routing(layer, ids, w, n, dev)
-    _check_grouping(grouping, n, m, layer.N, dev)
-    y = _check_y(layer, y, n, dev, accumulate, stream)
+    idp, wp = _check("ids", ids, _I32, (n, m), dev), _check("w", w, _F32, (n, m), dev)
+    _, offset, slots, _, _ = _check_grouping(grouping, n, m, layer.N, dev)
+    y, yp = _check_y(layer, y, n, dev, accumulate, stream)
     desc, L = layer.desc(accumulate), lib()
-    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
-    tail = (ids.data_ptr(), w.data_ptr(), n, grouping.offset.data_ptr(), grouping.slot_by_expert.data_ptr(),
-            y.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream))
+    if fp8:
+        hs = _check_quantized("h", h, n * m, f, dev)
+        name, call = "moe_grouped_down_fp8", L.moe_grouped_down_fp8
+    else:
+        hs = (_check("h", h, _BF16, (n * m, f), dev),)
+        name, call = "moe_grouped_down", L.moe_grouped_down
+    ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        if fp8:
-            _check_quantized("h", h, n * m, f)
-            _same(dev, h=h.q, h_scale=h.scale)
-            check("moe_grouped_down_fp8", L.moe_grouped_down_fp8(
-                ctypes.byref(desc), ctypes.byref(layer._weights), h.q.data_ptr(), h.scale.data_ptr(), *tail))
-        else:
-            _check_dev("h", h, torch.bfloat16, (n * m, f))
-            _same(dev, h=h)
-            check("moe_grouped_down", L.moe_grouped_down(ctypes.byref(desc), ctypes.byref(layer._weights), h.data_ptr(),
-                                                         *tail))
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *hs, idp, wp, n, offset, slots, yp,
+                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return y
 
 
@@ -325,18 +309,16 @@ def expert_grouped(layer, x, ids, w, y=None, ws=None, info=None, accumulate=Fals
     ``moe_expert_grouped_fp8`` for an ``Fp8Layer``, which quantises x first).  x and y
     bf16 [n][d]; ids outside [0, N) add nothing; ``info`` int32 [3]: U, ids status, 0."""
     fp8, dev = _kind(layer)
-    n = x.shape[0]
-    _check_dev("x", x, torch.bfloat16, (n, layer.d))
-    _check_routing(layer, ids, w, n, dev)
-    y = _check_y(layer, y, n, dev, accumulate, stream)
-    if info is not None:
-        _check_dev("info", info, torch.int32, (3,))
-    _same(dev, x=x, info=info)
+    n, m = x.shape[0], layer.m
+    xp = _check("x", x, _BF16, (n, layer.d), dev)
+    idp, wp = _check("ids", ids, _I32, (n, m), dev), _check("w", w, _F32, (n, m), dev)
+    y, yp = _check_y(layer, y, n, dev, accumulate, stream)
+    infop = None if info is None else _check("info", info, _I32, (3,), dev)
     desc, L = layer.desc(accumulate), lib()
-    ws = _ws(ws, L.moe_grouped_workspace_bytes(ctypes.byref(desc), n), "moe_grouped_workspace_bytes", dev, stream)
-    name = "moe_expert_grouped_fp8" if fp8 else "moe_expert_grouped"
+    name, call = (("moe_expert_grouped_fp8", L.moe_expert_grouped_fp8) if fp8 else
+                  ("moe_expert_grouped", L.moe_expert_grouped))
+    ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, getattr(L, name)(
-            ctypes.byref(desc), ctypes.byref(layer._weights), x.data_ptr(), ids.data_ptr(), w.data_ptr(), n,
-            y.data_ptr(), None if info is None else info.data_ptr(), ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), xp, idp, wp, n, yp, infop, ws.data_ptr(),
+                         ws.numel(), _on(dev, stream)))
     return y

@@ -329,7 +329,7 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
 /*
  * moe_group_slots -- the grouping of moe_route_group for any number of slots: the same
  * outputs, bit for bit (count [N], offset [N+1], slot_by_expert [n*m], distinct [N],
- * u_and_err [2]), from the same ids.  Two launches, deterministic.
+ * u_and_err [2]), from the same ids.  One launch, or two above 8192 slots; deterministic.
  *   ws   device workspace, ws_bytes >= moe_group_workspace_bytes(n, m, N), 256-byte
  *        aligned; no zero-fill needed, nothing kept between calls
  * Returns MOE_OK, MOE_E_INVAL, MOE_E_WORKSPACE (nothing enqueued) or MOE_E_HIP.
