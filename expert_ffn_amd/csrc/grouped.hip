@@ -178,8 +178,8 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.R = d->d_model;
     a.K = d->d_ff;
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
-    const int64_t work = (int64_t)n * (d->d_model / 8);
-    hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 255) / 256, 16384)), dim3(256), 0, st,
+    const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
+    hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
                        reinterpret_cast<const char*>(o), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }

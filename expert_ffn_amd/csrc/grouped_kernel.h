@@ -116,6 +116,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f(c), f(d), p, true);
 }
 
+__device__ __forceinline__ uint32_t finite_codes4(f32x4 v, float inv) {
+    const int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, p, true);
+}
+
 // Rows of bf16 (or float32) values to codes and scale bytes, in blocks of 128 along the row:
 // sixteen lanes a block, eight values a lane; work group g of G.
 template <bool F32>
@@ -632,6 +637,11 @@ struct Place {
 // way), then more with every 64 (clocks / 100, measured).
 __device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 14 : rows <= 128 ? 17 : rows <= 192 ? 23 : 29; }
 
+struct Groups {
+    const int32_t* offset;
+    int N, S;
+};
+
 struct Tiles {
     int sum, upto, cost, cost_upto;  // of this lane's experts; up to and with them
     int total, cost_total, C;
@@ -639,7 +649,7 @@ struct Tiles {
     struct Span {
         int lo, hi, tiles, cost;
     };
-    __device__ __forceinline__ static Span span(const Args& a, int lo, int hi) {
+    __device__ __forceinline__ static Span span(const Groups& a, int lo, int hi) {
         lo = min(max(lo, 0), a.S);
         hi = min(max(hi, lo), a.S);
         const int n = hi - lo, rest = n & (kTM - 1);
@@ -654,7 +664,7 @@ struct Tiles {
         }
         return v;
     }
-    __device__ __forceinline__ void count(const Args& a) {
+    __device__ __forceinline__ void count(const Groups& a) {
         const int lane = threadIdx.x & 63;
         C = (a.N + 63) / 64;
         sum = cost = 0;
@@ -673,7 +683,7 @@ struct Tiles {
     }
 
     // The tile (row tiles times CT) at cost x / 8 of all.
-    __device__ __forceinline__ int bound(const Args& a, int CT, int x) const {
+    __device__ __forceinline__ int bound(const Groups& a, int CT, int x) const {
         if (x >= 8) return total * CT;
         const int64_t target = (int64_t)cost_total * CT * x / 8;
         const uint64_t past = __ballot((int64_t)cost_upto * CT > target);
@@ -692,7 +702,7 @@ struct Tiles {
     }
 
     // Tile t of CT column tiles each: the column tiles of up to 8 row tiles are neighbours.
-    __device__ __forceinline__ Place place(const Args& a, int CT, int t) const {
+    __device__ __forceinline__ Place place(const Groups& a, int CT, int t) const {
         const uint64_t past = __ballot(upto * CT > t);
         if (t >= total * CT || !past) return Place{0, 0, 0, 0};
         const int from = __ffsll((unsigned long long)past) - 1;
@@ -712,17 +722,31 @@ struct Tiles {
     }
 };
 
+constexpr int kMaxKB = MOE_MAX_GROUP_WIDTH / kBlk;
+
 struct TileLds {
     char stage[2][kStage];  // rows, then weight rows
-    uint8_t xs[2][kTM];     // e4m3: scale bytes of a unit's rows, [wm][row % 16][i]
-    float red[4][kTM];      // e4m3 gate/up: |h| maxima of a row's four column groups
+    uint8_t xs[2][4][kTM];  // e4m3: scale bytes of four units' rows, [wm][row % 16][i]
+    uint32_t red[4][kTM];   // e4m3 gate/up: |h| maxima (their bits) of a row's four column groups
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
+    uint8_t ws[2][2][kMaxKB];  // e4m3: a tile's weight scale bytes: of both matrices, or of 128 rows each
     int after;              // the tile after the next
 };
 
 template <bool FP8, bool TILED, bool GU>
 __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     constexpr int ES = FP8 ? 1 : 2;
+    // The arguments that are needed now and then are loaded again each time: kept, they would
+    // push others out of the scalar registers.
+    auto arg = [] {
+        auto k = (const __attribute__((address_space(4))) Args*)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(k));
+        return k;
+    };
+    auto groups = [&] {
+        const auto k = arg();
+        return Groups{k->offset, k->N, k->S};
+    };
     constexpr int TC = GU ? kTN / 2 : kTN;  // weight rows of each matrix in a tile
     __shared__ TileLds lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -733,12 +757,12 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     // eighth of the cost, of which its work groups take two each and then whoever is free
     // the next (which tile runs where does not change its result).
     Tiles tiles;
-    tiles.count(a);
+    tiles.count(groups());
     const int xcd = blockIdx.x & 7, mine = blockIdx.x >> 3, step = gridDim.x >> 3;
-    const int run = uni(tiles.bound(a, CT, xcd)), run_end = uni(tiles.bound(a, CT, xcd + 1));
+    const int run = uni(tiles.bound(groups(), CT, xcd)), run_end = uni(tiles.bound(groups(), CT, xcd + 1));
     auto take = [&](int k) {  // in scalar registers: buffer descriptors and loops go by it
         Place t{0, 0, 0, 0};
-        if (k < run_end - run) t = tiles.place(a, CT, run + k);
+        if (k < run_end - run) t = tiles.place(groups(), CT, run + k);
         return Place{uni(t.e), uni(t.r0), uni(t.rows), uni(t.ct)};
     };
     int after = mine + step;  // the tile after this one
@@ -754,24 +778,22 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     struct Weights {
         __amdgpu_buffer_rsrc_t r;
         int row, rows;  // first matrix row of the tile; rows of the matrix, 0 for no tile
-        int at;         // the first scale byte (e4m3)
     };
     struct Rows {
         __amdgpu_buffer_rsrc_t r;
         int rows;
     };
-    auto token = [&](int slot) { return min(max(slot, 0), a.S - 1) / a.m; };
+    auto token = [&](int slot) { return min(max(slot, 0), arg()->S - 1) / arg()->m; };
     auto rows_of = [&](const Place& t) {
-        return Rows{GU ? rsrc(a.x, (uint32_t)(a.S / a.m) * (uint32_t)KBy)
-                       : rsrc(a.x + (int64_t)t.r0 * KBy, (uint32_t)t.rows * (uint32_t)KBy),
+        return Rows{GU ? rsrc(arg()->x, (uint32_t)(arg()->S / arg()->m) * (uint32_t)KBy)
+                       : rsrc(arg()->x + (int64_t)t.r0 * KBy, (uint32_t)t.rows * (uint32_t)KBy),
                     t.rows};
     };
     auto weights_of = [&](const Place& t) {
         Weights o;
-        o.r = rsrc((GU && wm ? a.w1 : a.w0) + (int64_t)t.e * wbytes, wbytes);
+        o.r = rsrc((GU && wm ? arg()->w1 : arg()->w0) + (int64_t)t.e * wbytes, wbytes);
         o.row = t.ct * TC;
         o.rows = t.rows ? a.R : 0;
-        o.at = (t.e * RB + min(t.ct * TC + (GU ? 0 : wn * 64), a.R - 1) / kBlk) * KB;
         return o;
     };
     // load i of a wave's four row and four weight loads of unit u
@@ -804,11 +826,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         const int last = max(t.rows - 1, 0);
         if (GU) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = a.slot[t.r0 + min((i * 8 + wave) * 8 + (lane >> 3), last)];
+            for (int i = 0; i < 4; ++i) g[i] = arg()->slot[t.r0 + min((i * 8 + wave) * 8 + (lane >> 3), last)];
         }
         if (FP8) {
             const int r = t.r0 + min(tid & (kTM - 1), last);
-            x = GU ? a.slot[r] : r;
+            x = GU ? arg()->slot[r] : r;
         }
     };
     auto address = [&](uint32_t (&g)[4], uint32_t& x) {
@@ -816,26 +838,42 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) g[i] = (uint32_t)token(g[i]) * KBy + ca;
         }
-        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, a.S - 1)) * KB;
+        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, arg()->S - 1)) * KB;
     };
     ask(p, gather, xrow);
     address(gather, xrow);
-    const auto rs0 = rsrc(a.s0, (uint32_t)a.N * RB * KB), rs1 = rsrc(a.s1, (uint32_t)a.N * RB * KB);
-    const auto rxs = rsrc(a.xs, (uint32_t)(GU ? a.S / a.m : a.S) * KB);
-    auto byte_of = [](__amdgpu_buffer_rsrc_t r, uint32_t vo, int so) {
-        return (int)__builtin_amdgcn_raw_buffer_load_b8(r, (int)vo, so, 0);
+    // e4m3 scale bytes.  Weights: a tile's, of 128 rows of each matrix or of two 128 rows, at
+    // once.  Rows: a thread a row, four units at a time, the word that ends with the array
+    // where it has fewer left.
+    const uint32_t xs_bytes = (uint32_t)(GU ? arg()->S / arg()->m : arg()->S) * KB;
+    auto row_scales = [&](uint32_t row, int u) {
+        const uint32_t o = row + u, o4 = min(o, xs_bytes - 4);  // KB >= 4: whole words exist
+        uint32_t v;
+        __builtin_memcpy(&v, a.xs + o4, 4);
+        return v >> (8 * (o - o4));
+    };
+    auto weight_scale = [&](const Place& t, int i) {  // byte i of a tile's two rows of KB
+        const int half = i >= KB, k = min(i - half * KB, KB - 1);
+        const int rb = min(t.ct * TC + (GU ? 0 : half * kBlk), a.R - 1) / kBlk;
+        return (GU && half ? arg()->s1 : arg()->s0)[((int64_t)t.e * RB + rb) * KB + k];
+    };
+    auto keep_weight_scale = [&](int par, int i, uint8_t v) {
+        if (i < 2 * KB) lds.ws[par][i >= KB][i >= KB ? i - KB : i] = v;
     };
     const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
-    int nx = 0, n0 = 0, n1 = 0;  // scale bytes on their way: rows of v + 2, weights of v + 1
+    uint32_t nx = 0;  // row scale bytes on their way to shared memory
+    auto keep_rows = [&](int par) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds.xs[par][i][sxat] = (uint8_t)(nx >> (8 * i));
+    };
     {
     const Rows xr = rows_of(p);
     const Weights wr = weights_of(p);
     if (FP8) {
-        n0 = byte_of(rs0, 0, wr.at);
-        if (GU) n1 = byte_of(rs1, 0, wr.at);
+        for (int i = tid; i < 2 * KB; i += kTileThreads) keep_weight_scale(0, i, weight_scale(p, i));
         if (!wm) {
-            lds.xs[0][sxat] = (uint8_t)byte_of(rxs, xrow, 0);
-            nx = byte_of(rxs, xrow, 1);
+            nx = row_scales(xrow, 0);
+            keep_rows(0);
         }
     }
 #pragma unroll
@@ -854,16 +892,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
 
     int par = 0;      // the stage of the unit at hand
     int stores = 0;   // of the tile before, which may still be on their way
-    constexpr int kScale = FP8 ? (GU ? 2 : 1) : 0;  // loads of weight scale bytes, in Ra
+    int xpar = 0, spar = 0;  // where the scale bytes of the rows and weights at hand are
     auto tile = [&](auto nb) {
         constexpr int NB = decltype(nb)::value, H = NB < 4 ? NB : 4;  // row blocks of a wave; of Ra and Ma
         // its own stores, the same number whatever the rows: those of no row are dropped by their bounds
         constexpr int kStores = GU ? (FP8 ? NB / 2 + 1 : NB) : 2 * NB;
         Place pn{0, 0, 0, 0};  // the next tile
         int got = 0;
+        uint8_t wsn[2] = {0, 0};  // the next tile's weight scale bytes
         Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
         Weights wr = weights_of(p);
-        int at = wr.at;  // of the weights' scale bytes that come next
         f32x4 acc[NB][4];
 #pragma unroll
         for (int i = 0; i < NB; ++i)
@@ -882,7 +920,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         x[i - first][kk] =
                             *reinterpret_cast<const u32x4*>(here + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
             };
-            int e0 = n0, e1 = n1;
+            int e0 = 0, e1 = 0;
             // the products of row blocks first .. end, `loads` after the first half of them
             auto products = [&](auto first, auto end, auto loads) {
                 constexpr int F = decltype(first)::value, E = decltype(end)::value;
@@ -912,7 +950,6 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 xb = rows_of(pn);
                 gather[2] = gather_n[2];
                 gather[3] = gather_n[3];
-                if (FP8) at = wr.at;
                 ua = 0;
             }
 #pragma unroll
@@ -924,16 +961,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
             read_rows(0, H);
             if (FP8) {
-                const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[par][wm * 128 + lr * 8]);
+                const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[xpar][u & 3][wm * 128 + lr * 8]);
                 ex[0] = v[0];
                 ex[1] = v[1];
-                n0 = byte_of(rs0, 0, at + ua);
-                if (GU) n1 = byte_of(rs1, 0, at + ua);
+                e0 = lds.ws[spar][GU ? 0 : wn >> 1][u];
+                if (GU) e1 = lds.ws[spar][1][u];
             }
             wait_lds();
-            if (u == 0 && stores == 16) wait_vm<6 + kScale + 16>();
-            else if (u == 0 && stores >= 5) wait_vm<6 + kScale + 5>();
-            else wait_vm<6 + kScale>();
+            if (u == 0 && stores == 16) wait_vm<6 + 16>();
+            else if (u == 0 && stores >= 5) wait_vm<6 + 5>();
+            else wait_vm<6>();
             block_barrier();
             // Ma
             products(std::integral_constant<int, 0>(), std::integral_constant<int, H>(), [&] {
@@ -945,8 +982,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             if (u == 0) {
                 pn = take(after);
                 ask(pn, gather_n, xrow_n);
-                if (tid == 0) got = atomicAdd(&a.queue[xcd * kLine], 1);
+                if (tid == 0) got = atomicAdd(&arg()->queue[xcd * kLine], 1);
+                if (FP8) {
+                    wsn[0] = weight_scale(pn, tid);
+                    if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
+                }
             } else if (u == 1) {
+                if (FP8) {
+                    keep_weight_scale(spar ^ 1, tid, wsn[0]);
+                    if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
+                }
                 address(gather_n, xrow_n);
                 if (tid == 0) lds.after = got + 2 * step;
             } else if (ub == U) {
@@ -959,17 +1004,23 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             }
             if (ub >= U) ub -= U;
             read_rows(H, NB);
-            if (FP8 && !wm) {
-                lds.xs[par ^ 1][sxat] = (uint8_t)nx;
-                nx = byte_of(rxs, xrow, ub);
+            if (FP8) {
+                // The next four units' row scales (or the next tile's first) are asked for two units
+                // ahead and kept one ahead.
+                const bool turn4 = u + 1 == U || ((u + 1) & 3) == 0, ask4 = u + 2 == U || (((u + 2) & 3) == 0 && u + 2 < U);
+                if (turn4) {
+                    if (!wm) keep_rows(xpar ^ 1);
+                    xpar ^= 1;
+                }
+                if (ask4 && !wm) nx = row_scales(xrow, ub);
             }
             load_weights(wr, ub, here, 0);
             load_weights(wr, ub, here, 1);
             load_rows(xa, gather, ub, here, 0);
             wait_lds();
-            if (u == 0 && stores == 16) wait_vm<5 + kScale + 16>();
-            else if (u == 0 && stores >= 5) wait_vm<5 + kScale + 5>();
-            else wait_vm<5 + kScale>();
+            if (u == 0 && stores == 16) wait_vm<5 + 16>();
+            else if (u == 0 && stores >= 5) wait_vm<5 + 5>();
+            else wait_vm<5>();
             block_barrier();
             // Mb
             products(std::integral_constant<int, H>(), nb, [&] {
@@ -987,32 +1038,46 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         asm volatile("" : "+v"(el));  // addresses below are formed here, not kept through the products
         const int er = el & 15, eq = el >> 4;
         if constexpr (GU) {
-            const auto ro = rsrc(a.out + (int64_t)p.r0 * a.R * ES, (uint32_t)p.rows * a.R * ES);
+            const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * ES, (uint32_t)p.rows * a.R * ES);
             const int c0 = p.ct * TC + wn * 32;  // this wave's 32 columns of h
-            float m[NB];
+            uint32_t m[NB];  // |h|'s largest bits: the order of the values, with what is not finite above
+            bool odd = false;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                m[i] = 0.f;
+                m[i] = 0;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float h = silu(acc[i][j][k]) * acc[i][j + 2][k];
                         acc[i][j][k] = h;
-                        if (FP8) m[i] = fmaxf(m[i], mag(h));  // columns past R: zero weights, h = 0
+                        if (FP8) m[i] = max(m[i], __float_as_uint(h) & 0x7fffffffu);  // columns past R: 0
                     }
+                odd |= m[i] >= 0x7f800000u;
             }
             if constexpr (FP8) {
+                odd = __any(odd);
+                if (odd) {  // rare: what is not finite takes no part
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        m[i] = 0;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) m[i] = max(m[i], __float_as_uint(mag(acc[i][j][k])));
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    m[i] = fmaxf(m[i], __shfl_xor(m[i], 16, 64));
-                    m[i] = fmaxf(m[i], __shfl_xor(m[i], 32, 64));
+                    m[i] = max(m[i], (uint32_t)__shfl_xor((int)m[i], 16, 64));
+                    m[i] = max(m[i], (uint32_t)__shfl_xor((int)m[i], 32, 64));
                     if (eq == 0) lds.red[wn][(i * 2 + wm) * 16 + er] = m[i];
                 }
                 wait_lds();
                 block_barrier();
                 auto exp_of = [&](int rr) {
-                    return block_exp(fmaxf(fmaxf(lds.red[0][rr], lds.red[1][rr]), fmaxf(lds.red[2][rr], lds.red[3][rr])));
+                    return block_exp(__uint_as_float(
+                        max(max(lds.red[0][rr], lds.red[1][rr]), max(lds.red[2][rr], lds.red[3][rr]))));
                 };
                 // codes, two blocks of rows at a time: 32 rows of 32 bytes
 #pragma unroll
@@ -1024,7 +1089,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         for (int j = 0; j < 2; ++j) {
                             const f32x4 h = acc[i + k][j];
                             *reinterpret_cast<uint32_t*>(turn + (k * 16 + er) * 48 + j * 16 + 4 * eq) =
-                                codes4(h[0], h[1], h[2], h[3], inv);
+                                odd ? codes4(h[0], h[1], h[2], h[3], inv) : finite_codes4(h, inv);
                         }
                     }
                     const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 1) * 48 + (el & 1) * 16);
@@ -1033,7 +1098,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 }
                 // scale bytes: wave column wn those of two blocks
                 const int i = wn * 2 + (el >> 4), rr = (i * 2 + wm) * 16 + er;
-                const auto rso = rsrc(a.outs + (int64_t)p.r0 * CT, (uint32_t)p.rows * CT);
+                const auto rso = rsrc(arg()->outs + (int64_t)p.r0 * CT, (uint32_t)p.rows * CT);
                 __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(exp_of(rr & (kTM - 1)) + 127), rso,
                                                      el < 32 && i < NB ? rr * CT + p.ct : kOOB, 0, 0);
             } else {
@@ -1051,7 +1116,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 }
             }
         } else {
-            const auto ro = rsrc(a.out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
+            const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
             const int c0 = p.ct * TC + wn * 64;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -1071,6 +1136,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             }
         }
         stores = kStores;
+        spar ^= 1;
         return pn;
     };
     while (p.rows) {
@@ -1084,6 +1150,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         after = uni(after);
         par = uni(par);
         stores = uni(stores);
+        xpar = uni(xpar);
+        spar = uni(spar);
     }
     if (!wm) block_barrier();
 }
@@ -1099,32 +1167,60 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 }
 
 // y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
-// to bf16 once; eight columns a thread.  info (may be null): U, ids status, MOE_OK.
+// to bf16 once.  A wave takes 512 columns of a token (eight a lane); the lanes look up the
+// token's slots together, so that the loads of O go out eight at a time: they are the time.
+// info (may be null): U, ids status, MOE_OK.
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
                                                 int m, int N, int d,
                                                 int accumulate, char* __restrict__ y, const int32_t* __restrict__ u_err,
                                                 int32_t* __restrict__ info) {
-    const int D8 = d / 8;
+    const int lane = threadIdx.x & 63, CW = (d + 511) / 512, last = (int)(n * m) - 1;
     if (info && blockIdx.x == 0 && threadIdx.x < 3) info[threadIdx.x] = threadIdx.x < 2 ? u_err[threadIdx.x] : MOE_OK;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * D8; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / D8;
-        const int c = (int)(i - t * D8) * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + uni(threadIdx.x >> 6); i < n * CW; i += (int64_t)gridDim.x * 4) {
+        const int64_t t = i / CW;
+        const int c = (int)(i - t * CW) * 512 + lane * 8;
+        const bool in = c < d;
         float s[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[k] = 0.f;
-        for (int j = 0; j < m; ++j) {
-            const int id = ids[t * m + j];
-            if (id < 0 || id >= N) continue;
-            const float wj = w[t * m + j];
-            const int64_t r = min(max(row_of[t * m + j], 0), (int)(n * m) - 1);
-            const u32x4 o = *reinterpret_cast<const u32x4*>(O + (r * d + c) * 2);
+        for (int j0 = 0; j0 < m; j0 += 64) {
+            // this lane's slot: its row (-1: none) and weight
+            int row = -1;
+            float wj = 0.f;
+            if (j0 + lane < m) {
+                const int64_t slot = t * m + j0 + lane;
+                const int id = ids[slot], r = min(max(row_of[slot], 0), last);
+                wj = w[slot];
+                row = id >= 0 && id < N ? r : -1;
+            }
+            uint64_t live = __ballot(row >= 0);
+            while (live) {
+                u32x4 o[8];
+                float wt[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[2 * k] += wj * bf16_lo(o[k]);
-                s[2 * k + 1] += wj * bf16_hi(o[k]);
+                for (int k = 0; k < 8; ++k) {
+                    const int l = live ? __ffsll((unsigned long long)live) - 1 : 64;
+                    live &= live - 1;
+                    o[k] = u32x4{0u, 0u, 0u, 0u};
+                    wt[k] = 0.f;
+                    if (l < 64) {
+                        const int64_t r = __builtin_amdgcn_readlane(row, l);
+                        wt[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(wj), l));
+                        if (in) o[k] = *reinterpret_cast<const u32x4*>(O + (r * d + c) * 2);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        s[2 * v] += wt[k] * bf16_lo(o[k][v]);
+                        s[2 * v + 1] += wt[k] * bf16_hi(o[k][v]);
+                    }
+                }
             }
         }
+        if (!in) continue;
         u32x4* p = reinterpret_cast<u32x4*>(y + (t * d + c) * 2);
         if (accumulate) {
             const u32x4 v = *p;
