@@ -637,6 +637,7 @@ struct Place {
 // way), then more with every 64 (clocks / 100, measured).
 __device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 14 : rows <= 128 ? 17 : rows <= 192 ? 23 : 29; }
 
+// offset, kept in shared memory: a load from memory would wait for every operand's before it
 struct Groups {
     const int32_t* offset;
     int N, S;
@@ -731,11 +732,13 @@ struct TileLds {
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
     uint8_t ws[2][2][kMaxKB];  // e4m3: a tile's weight scale bytes: of both matrices, or of 128 rows each
     int after;              // the tile after the next
+    int32_t offset[MOE_MAX_EXPERTS + 1];
 };
 
 template <bool FP8, bool TILED, bool GU>
 __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     constexpr int ES = FP8 ? 1 : 2;
+    __shared__ TileLds lds;
     // The arguments that are needed now and then are loaded again each time: kept, they would
     // push others out of the scalar registers.
     auto arg = [] {
@@ -745,10 +748,9 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     };
     auto groups = [&] {
         const auto k = arg();
-        return Groups{k->offset, k->N, k->S};
+        return Groups{lds.offset, k->N, k->S};
     };
     constexpr int TC = GU ? kTN / 2 : kTN;  // weight rows of each matrix in a tile
-    __shared__ TileLds lds;
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int lr = lane & 15, q = lane >> 4, wm = wave >> 2, wn = wave & 3;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
@@ -756,6 +758,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     // Work groups b, b + 8, ... share an XCD and its L2: each XCD has a run of tiles of an
     // eighth of the cost, of which its work groups take two each and then whoever is free
     // the next (which tile runs where does not change its result).
+    for (int e = tid; e <= a.N; e += kTileThreads) lds.offset[e] = a.offset[e];
+    __syncthreads();
     Tiles tiles;
     tiles.count(groups());
     const int xcd = blockIdx.x & 7, mine = blockIdx.x >> 3, step = gridDim.x >> 3;
@@ -846,25 +850,26 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     // once.  Rows: a thread a row, four units at a time, the word that ends with the array
     // where it has fewer left.
     const uint32_t xs_bytes = (uint32_t)(GU ? arg()->S / arg()->m : arg()->S) * KB;
+    uint32_t nx = 0, nx_shift = 0;  // row scale bytes on their way to shared memory
     auto row_scales = [&](uint32_t row, int u) {
         const uint32_t o = row + u, o4 = min(o, xs_bytes - 4);  // KB >= 4: whole words exist
-        uint32_t v;
-        __builtin_memcpy(&v, a.xs + o4, 4);
-        return v >> (8 * (o - o4));
+        __builtin_memcpy(&nx, a.xs + o4, 4);
+        nx_shift = 8 * (o - o4);
     };
     auto weight_scale = [&](const Place& t, int i) {  // byte i of a tile's two rows of KB
         const int half = i >= KB, k = min(i - half * KB, KB - 1);
         const int rb = min(t.ct * TC + (GU ? 0 : half * kBlk), a.R - 1) / kBlk;
-        return (GU && half ? arg()->s1 : arg()->s0)[((int64_t)t.e * RB + rb) * KB + k];
+        const uint8_t *s0 = arg()->s0, *s1 = GU ? arg()->s1 : s0;  // both pointers, then a lane's choice
+        return (half ? s1 : s0)[((int64_t)t.e * RB + rb) * KB + k];
     };
     auto keep_weight_scale = [&](int par, int i, uint8_t v) {
         if (i < 2 * KB) lds.ws[par][i >= KB][i >= KB ? i - KB : i] = v;
     };
     const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
-    uint32_t nx = 0;  // row scale bytes on their way to shared memory
     auto keep_rows = [&](int par) {
+        const uint32_t v = nx >> nx_shift;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lds.xs[par][i][sxat] = (uint8_t)(nx >> (8 * i));
+        for (int i = 0; i < 4; ++i) lds.xs[par][i][sxat] = (uint8_t)(v >> (8 * i));
     };
     {
     const Rows xr = rows_of(p);
@@ -872,7 +877,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     if (FP8) {
         for (int i = tid; i < 2 * KB; i += kTileThreads) keep_weight_scale(0, i, weight_scale(p, i));
         if (!wm) {
-            nx = row_scales(xrow, 0);
+            row_scales(xrow, 0);
             keep_rows(0);
         }
     }
@@ -982,7 +987,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             if (u == 0) {
                 pn = take(after);
                 ask(pn, gather_n, xrow_n);
-                if (tid == 0) got = atomicAdd(&arg()->queue[xcd * kLine], 1);
+                if (tid == 0) {
+                    int at = xcd * kLine;
+                    asm volatile("" : "+v"(at));  // a lane's address: a wave's would be waited for at once
+                    got = atomicAdd(&arg()->queue[at], 1);
+                }
                 if (FP8) {
                     wsn[0] = weight_scale(pn, tid);
                     if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
@@ -1012,7 +1021,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     if (!wm) keep_rows(xpar ^ 1);
                     xpar ^= 1;
                 }
-                if (ask4 && !wm) nx = row_scales(xrow, ub);
+                if (ask4 && !wm) row_scales(xrow, ub);
             }
             load_weights(wr, ub, here, 0);
             load_weights(wr, ub, here, 1);
