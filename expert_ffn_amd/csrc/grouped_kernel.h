@@ -712,10 +712,12 @@ struct Tiles {
             const int e = from * C + i;
             const Span s = span(a, uni(a.offset[e]), uni(a.offset[e + 1]));
             if (k < s.tiles * CT) {
-                const int sg = k / (8 * CT), in = min(8, s.tiles - 8 * sg);
+                const int sg = k < 8 * CT ? 0 : k / (8 * CT), in = min(8, s.tiles - 8 * sg);
                 k -= sg * 8 * CT;
-                const int r0 = s.lo + (8 * sg + k % in) * kTM;
-                return Place{e, r0, min(s.hi - r0, kTM), k / in};
+                // k / in: k < 8 * 512 and in <= 8, so 65536 / in + 1 for 1 / in is exact
+                const int ct = k * ((int)(65536.f * __builtin_amdgcn_rcpf((float)in)) + 1) >> 16;
+                const int r0 = s.lo + (8 * sg + k - ct * in) * kTM;
+                return Place{e, r0, min(s.hi - r0, kTM), ct};
             }
             k -= s.tiles * CT;
         }
@@ -784,14 +786,19 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         int row, rows;  // first matrix row of the tile; rows of the matrix, 0 for no tile
     };
     struct Rows {
-        __amdgpu_buffer_rsrc_t r;
+        __amdgpu_buffer_rsrc_t r;  // down: the tile's rows of h
         int rows;
     };
-    auto token = [&](int slot) { return min(max(slot, 0), arg()->S - 1) / arg()->m; };
+    const auto rx = rsrc(a.x, GU ? (uint32_t)(a.S / a.m) * (uint32_t)KBy : 0u);  // gate/up: all of x
+    // slot / m: with ceil(2^32 / m) for 2^32 / m it is exact as slot * m < 2^32
+    const int last_slot = a.S - 1;
+    const uint32_t inv_m = a.m > 1 ? 0xffffffffu / (uint32_t)a.m + 1 : 0;
+    auto token = [&](int slot) {
+        const uint32_t v = (uint32_t)min(max(slot, 0), last_slot);
+        return inv_m ? __umulhi(v, inv_m) : v;
+    };
     auto rows_of = [&](const Place& t) {
-        return Rows{GU ? rsrc(arg()->x, (uint32_t)(arg()->S / arg()->m) * (uint32_t)KBy)
-                       : rsrc(arg()->x + (int64_t)t.r0 * KBy, (uint32_t)t.rows * (uint32_t)KBy),
-                    t.rows};
+        return Rows{GU ? rx : rsrc(arg()->x + (int64_t)t.r0 * KBy, (uint32_t)t.rows * (uint32_t)KBy), t.rows};
     };
     auto weights_of = [&](const Place& t) {
         Weights o;
@@ -805,7 +812,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         const int in = i * 8 + wave;
         uint32_t vo = GU ? gather[i] : v8;
         if (u == U - 1) vo |= cut;
-        to_lds(w.r, stage + in * 1024, in * 8 < w.rows ? vo : kOOB, u * kUnit + (GU ? 0 : in * 8 * KBy));
+        to_lds(GU ? rx : w.r, stage + in * 1024, in * 8 < w.rows ? vo : kOOB, u * kUnit + (GU ? 0 : in * 8 * KBy));
     };
     auto load_weights = [&](const Weights& w, int u, char* stage, int i) {
         const int in = i * 8 + wave;
@@ -842,14 +849,14 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) g[i] = (uint32_t)token(g[i]) * KBy + ca;
         }
-        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, arg()->S - 1)) * KB;
+        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, last_slot)) * KB;
     };
     ask(p, gather, xrow);
     address(gather, xrow);
     // e4m3 scale bytes.  Weights: a tile's, of 128 rows of each matrix or of two 128 rows, at
     // once.  Rows: a thread a row, four units at a time, the word that ends with the array
     // where it has fewer left.
-    const uint32_t xs_bytes = (uint32_t)(GU ? arg()->S / arg()->m : arg()->S) * KB;
+    const uint32_t xs_bytes = (uint32_t)(GU ? a.S / a.m : a.S) * KB;
     uint32_t nx = 0, nx_shift = 0;  // row scale bytes on their way to shared memory
     auto row_scales = [&](uint32_t row, int u) {
         const uint32_t o = row + u, o4 = min(o, xs_bytes - 4);  // KB >= 4: whole words exist
@@ -895,13 +902,21 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     block_barrier();
     if (wm) block_barrier();
 
+    // a wave's stores of a tile: the same number whatever its rows, those of no row are dropped by their bounds
+    constexpr auto stores_of = [](int nb) { return GU ? (FP8 ? nb / 2 + 1 : nb) : 2 * nb; };
     int par = 0;      // the stage of the unit at hand
-    int stores = 0;   // of the tile before, which may still be on their way
+    int before = 0;   // row blocks of a wave in the tile before, whose stores may still be on their way
+    auto wait_past = [&](auto n, int nb) {
+        constexpr int N = decltype(n)::value;
+        if (nb == 0) wait_vm<N>();
+        else if (nb == 2) wait_vm<N + stores_of(2)>();
+        else if (nb == 4) wait_vm<N + stores_of(4)>();
+        else if (nb == 6) wait_vm<N + stores_of(6)>();
+        else wait_vm<N + stores_of(8)>();
+    };
     int xpar = 0, spar = 0;  // where the scale bytes of the rows and weights at hand are
     auto tile = [&](auto nb) {
         constexpr int NB = decltype(nb)::value, H = NB < 4 ? NB : 4;  // row blocks of a wave; of Ra and Ma
-        // its own stores, the same number whatever the rows: those of no row are dropped by their bounds
-        constexpr int kStores = GU ? (FP8 ? NB / 2 + 1 : NB) : 2 * NB;
         Place pn{0, 0, 0, 0};  // the next tile
         int got = 0;
         uint8_t wsn[2] = {0, 0};  // the next tile's weight scale bytes
@@ -973,9 +988,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 if (GU) e1 = lds.ws[spar][1][u];
             }
             wait_lds();
-            if (u == 0 && stores == 16) wait_vm<6 + 16>();
-            else if (u == 0 && stores >= 5) wait_vm<6 + 5>();
-            else wait_vm<6>();
+            wait_past(std::integral_constant<int, 6>(), u == 0 ? before : 0);
             block_barrier();
             // Ma
             products(std::integral_constant<int, 0>(), std::integral_constant<int, H>(), [&] {
@@ -1027,9 +1040,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             load_weights(wr, ub, here, 1);
             load_rows(xa, gather, ub, here, 0);
             wait_lds();
-            if (u == 0 && stores == 16) wait_vm<5 + 16>();
-            else if (u == 0 && stores >= 5) wait_vm<5 + 5>();
-            else wait_vm<5>();
+            wait_past(std::integral_constant<int, 5>(), u == 0 ? before : 0);
             block_barrier();
             // Mb
             products(std::integral_constant<int, H>(), nb, [&] {
@@ -1144,7 +1155,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 }
             }
         }
-        stores = kStores;
+        before = NB;
         spar ^= 1;
         return pn;
     };
@@ -1158,7 +1169,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         p = Place{uni(pn.e), uni(pn.r0), uni(pn.rows), uni(pn.ct)};
         after = uni(after);
         par = uni(par);
-        stores = uni(stores);
+        before = uni(before);
         xpar = uni(xpar);
         spar = uni(spar);
     }
