@@ -635,7 +635,7 @@ struct Place {
 // Every expert's row tiles and what they cost, one scan kept by the wave: lane l holds
 // N / 64 experts.  A unit of a tile takes about the same time up to 64 rows (the weights'
 // way), then more with every 64 (clocks / 100, measured).
-__device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 14 : rows <= 128 ? 17 : rows <= 192 ? 23 : 29; }
+__device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 23 : rows <= 128 ? 26 : rows <= 192 ? 28 : 30; }
 
 // offset, kept in shared memory: a load from memory would wait for every operand's before it
 struct Groups {
