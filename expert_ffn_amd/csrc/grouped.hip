@@ -98,11 +98,31 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     return p;
 }
 
-// Square tiles from 16 rows an expert on average; their loads run up to two units ahead
-// into the next tile, which takes four units a tile, with buffer offsets of 31 bits.
+// Square or thin tiles.  Square ones read the weights at the memory's pace from few rows on
+// if there are tiles for all compute units: 128 experts of 2048 x 768, gate and up, at 2 / 4 /
+// 8 / 16 / 32 rows an expert 153 / 133 / 133 / 134 / 137 us square and 142 / 143 / 145 / 150 /
+// 218 us thin.  With fewer tiles than units, thin ones spread them: 8 experts of 4096 x 14336, down,
+// at 8 / 16 rows 254 / 255 us square and 167 / 204 us thin (which doubles with every 16 rows).
+// Square tiles' loads run up to two units ahead into the next tile, which takes four
+// units a tile, and have buffer offsets of 31 bits; thin tiles address all of memory.
 bool square(const Args& a, bool fp8, bool gu) {
     const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
-    return kby > 3 * kUnit && a.S >= 16 * (int64_t)a.N && a.R * kby <= most && (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
+    const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
+    return kby > 3 * kUnit && a.S >= (tiles >= 1024 ? 4 : 24) * (int64_t)a.N && a.R * kby <= most &&
+           (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
+}
+
+Args shape_of(int N, int m, int n, int R, int K) {
+    Args a{};
+    a.N = N;
+    a.m = m;
+    a.S = n * m;
+    a.R = R;
+    a.K = K;
+    return a;
+}
+bool square_gate_up(const moe_layer_desc* d, int n) {
+    return square(shape_of(d->N, d->m, n, d->d_ff, d->d_model), d->dtype == MOE_FP8, true);
 }
 
 template <bool FP8, bool GU>
@@ -117,11 +137,22 @@ void launch_product(const Args& a, bool tiled, hipStream_t st) {
         return;
     }
     const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
-    const int grid = (int)(tiles * ((a.R + 15) / 16));
+    const int64_t cols = (a.R + 15) / 16, units = ((int64_t)a.K * (FP8 ? 1 : 2) + kUnit - 1) / kUnit;
+    if constexpr (!GU) {
+        if (units <= kThinWhole && tiles * cols >= 16 * kCUs) {  // (one token's 1024 tiles: 1.5 us better split)
+            const int grid = (int)(tiles * ((cols + kThinWaves - 1) / kThinWaves));
+            if (tiled)
+                hipLaunchKernelGGL((k_thin<FP8, true, GU, false>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+            else
+                hipLaunchKernelGGL((k_thin<FP8, false, GU, false>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+            return;
+        }
+    }
+    const int grid = (int)(tiles * cols);
     if (tiled)
-        hipLaunchKernelGGL((k_thin<FP8, true, GU>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+        hipLaunchKernelGGL((k_thin<FP8, true, GU, true>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
     else
-        hipLaunchKernelGGL((k_thin<FP8, false, GU>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+        hipLaunchKernelGGL((k_thin<FP8, false, GU, true>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
 }
 
 struct Weights {
@@ -133,7 +164,7 @@ template <bool FP8>
 void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const uint8_t* xs, int32_t n,
                  const int32_t* offset, const int32_t* sbe, void* h, uint8_t* hs, void* hf, int32_t* queue,
                  hipStream_t st) {
-    Args a{};
+    Args a = shape_of(d->N, d->m, n, d->d_ff, d->d_model);
     a.x = reinterpret_cast<const char*>(x);
     a.xs = xs;
     a.w0 = reinterpret_cast<const char*>(w.w0);
@@ -145,12 +176,7 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
     a.out = reinterpret_cast<char*>(h);
     a.outs = hs;
     a.queue = queue;
-    a.N = d->N;
-    a.m = d->m;
-    a.S = n * d->m;
-    a.R = d->d_ff;
-    a.K = d->d_model;
-    const bool by16 = FP8 && !square(a, FP8, true);  // thin tiles leave h in fp32
+    const bool by16 = FP8 && !square_gate_up(d, n);  // thin tiles leave h in fp32
     if (by16) a.out = reinterpret_cast<char*>(hf);
     launch_product<FP8, true>(a, d->flags & MOE_FLAG_TILED, st);
     if (by16)
@@ -163,7 +189,7 @@ template <bool FP8>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
               const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, const int32_t* row_of, void* y,
               void* o, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
-    Args a{};
+    Args a = shape_of(d->N, d->m, n, d->d_model, d->d_ff);
     a.x = reinterpret_cast<const char*>(h);
     a.xs = hs;
     a.w0 = reinterpret_cast<const char*>(w.w0);
@@ -172,11 +198,6 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.slot = sbe;
     a.out = reinterpret_cast<char*>(o);
     a.queue = queue;
-    a.N = d->N;
-    a.m = d->m;
-    a.S = n * d->m;
-    a.R = d->d_model;
-    a.K = d->d_ff;
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
     hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
@@ -216,8 +237,8 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     run_group(g, st);
     run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
                      b + p.h, u8(p.hs), b + p.hf, i32(p.queue), st);
-    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y,
-                  b + p.o, i32(p.queue) + kQueue, i32(p.u_err), info, st);
+    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y, b + p.o,
+                  i32(p.queue) + kQueue, i32(p.u_err), info, st);
     return launched();
 }
 

@@ -482,24 +482,43 @@ __device__ __forceinline__ TileAt find_tile(const int32_t* __restrict__ offset, 
 
 // Thin tiles: 16 rows by 16 output columns (gate/up: of both matrices), the contraction
 // split over the four waves, operands straight from memory.  For passes of few rows an
-// expert, where the weights' bytes are the time.
-constexpr int kThinWaves = 4, kThinAhead = 4;  // units of a wave's loads in flight
+// expert, where the weights' bytes are the time: there is time for the e4m3 operands to
+// be widened to bf16 (exact, their power of two with them), whose products and sums the
+// matrix instruction rounds only to fp32, where its e4m3 form cuts small ones (see the
+// note at k_tile).
+//
+// SPLIT: the four waves share a tile's contraction.  Without, each has a tile of its own and
+// all its units (at most kThinWhole) in flight: a split contraction of six units left two waves one
+// unit each, and 128 e4m3 experts' down tiles (d_ff 768) took 73 us for 201 MB.
+constexpr int kThinWaves = 4, kThinAhead = 4, kThinWhole = 8;  // units of a wave's loads in flight
 
-template <bool FP8, bool TILED, bool GU>
+// Two words of codes (eight values) to bf16, scaled.
+__device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float f) {
+    struct Eight {
+        bf16x2_t v[4];
+    };
+    return __builtin_bit_cast(bf16x8_t, Eight{{__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false),
+                                               __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true),
+                                               __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false),
+                                               __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true)}});
+}
+
+template <bool FP8, bool TILED, bool GU, bool SPLIT>
 __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
-    constexpr int ES = FP8 ? 1 : 2, NW = GU ? 2 : 1;
-    __shared__ f32x4 red[kThinWaves][NW][64];
+    constexpr int ES = FP8 ? 1 : 2, NW = GU ? 2 : 1, AHEAD = SPLIT ? kThinAhead : kThinWhole;
+    __shared__ f32x4 red[SPLIT ? kThinWaves : 1][NW][64];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int lr = lane & 15, q = lane >> 4;
-    const int CB = (a.R + 15) / 16;
-    const int tile = blockIdx.x / CB, cb = blockIdx.x - tile * CB;
+    const int CB = (a.R + 15) / 16, CW = SPLIT ? CB : (CB + kThinWaves - 1) / kThinWaves;  // work groups a row tile
+    const int tile = blockIdx.x / CW, cw = blockIdx.x - tile * CW;
+    const int cb = SPLIT ? cw : cw * kThinWaves + wave;
+    if (!SPLIT && cb >= CB) return;  // (no barrier without SPLIT)
     const TileAt t = find_tile(a.offset, a.N, a.S, kTile16, tile);
     if (t.e < 0) return;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
     const int row = min(t.r0 + lr, t.end - 1);
-    const int slot = min(max(a.slot[row], 0), a.S - 1);
-    const int64_t xrow = GU ? slot / a.m : row;
-    const char* xp = a.x + xrow * KBy;
+    int64_t xrow = row;
+    if (GU) xrow = min(max(a.slot[row], 0), a.S - 1) / a.m;
     const char* wp[2];
     const int wr = min(cb * 16 + lr, a.R - 1);
 #pragma unroll
@@ -507,54 +526,80 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
         const char* w = (i ? a.w1 : a.w0) + (int64_t)t.e * a.R * KBy;
         wp[i] = TILED ? w + (int64_t)cb * 16 * KBy + lane * 16 : w + (int64_t)wr * KBy;
     }
-    const uint8_t* sx = FP8 ? a.xs + xrow * KB : nullptr;
     const int RB = (a.R + kBlk - 1) / kBlk;
     const int64_t sw = FP8 ? ((int64_t)t.e * RB + cb * 16 / kBlk) * KB : 0;
     f32x4 acc[NW];
 #pragma unroll
     for (int i = 0; i < NW; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int u0 = wave; u0 < U; u0 += kThinWaves * kThinAhead) {
-        u32x4 b[kThinAhead][2], w[kThinAhead][NW][2];
-        int eb[kThinAhead], ew[kThinAhead][NW];
+    constexpr int STEP = SPLIT ? kThinWaves : 1;
+    for (int u0 = SPLIT ? wave : 0; u0 < U; u0 += STEP * AHEAD) {
+        u32x4 b[AHEAD][2], w[AHEAD][NW][2];
+        int eb[AHEAD], ew[AHEAD][NW];
+        // the weights first: they wait for nothing but the tile
 #pragma unroll
-        for (int p = 0; p < kThinAhead; ++p) {
-            const int u = u0 + p * kThinWaves;
-            eb[p] = 0;
+        for (int p = 0; p < AHEAD; ++p) {
+            const int u = u0 + p * STEP;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) ew[p][i] = 0;
-            if (FP8 && u < U) {
-                eb[p] = sx[u];
-                ew[p][0] = a.s0[sw + u];
-                if (GU) ew[p][NW - 1] = a.s1[sw + u];
-            }
+            for (int i = 0; i < NW; ++i) {
+                ew[p][i] = 0;
+                if (FP8 && u < U) ew[p][i] = (i ? a.s1 : a.s0)[sw + u];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int k = u * kUnit + kk * 64 + q * 16;
-                const bool ok = u < U && k < KBy;
-                b[p][kk] = ok ? *reinterpret_cast<const u32x4*>(xp + k) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int i = 0; i < NW; ++i)
-                    w[p][i][kk] = ok ? *reinterpret_cast<const u32x4*>(
-                                           wp[i] + (TILED ? (int64_t)(2 * u + kk) * 1024 : (int64_t)k))
-                                     : u32x4{0u, 0u, 0u, 0u};
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int k = u * kUnit + kk * 64 + q * 16;
+                    w[p][i][kk] = u < U && k < KBy ? *reinterpret_cast<const u32x4*>(
+                                                         wp[i] + (TILED ? (int64_t)(2 * u + kk) * 1024 : (int64_t)k))
+                                                   : u32x4{0u, 0u, 0u, 0u};
+                }
             }
         }
 #pragma unroll
-        for (int p = 0; p < kThinAhead; ++p)
+        for (int p = 0; p < AHEAD; ++p) {
+            const int u = u0 + p * STEP;
+            eb[p] = 0;
+            if (FP8 && u < U) eb[p] = a.xs[xrow * KB + u];
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                acc[i] = mma_unit<FP8>(w[p][i][0], w[p][i][1], b[p][0], b[p][1], acc[i], ew[p][i], eb[p]);
+            for (int kk = 0; kk < 2; ++kk) {
+                const int k = u * kUnit + kk * 64 + q * 16;
+                b[p][kk] = u < U && k < KBy ? *reinterpret_cast<const u32x4*>(a.x + xrow * KBy + k)
+                                            : u32x4{0u, 0u, 0u, 0u};
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p) {
+            if constexpr (FP8) {
+                const float fb = pow2(eb[p] - 127);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int v = 0; v < 4; v += 2) {
+                        const bf16x8_t x = widen(b[p][kk][v], b[p][kk][v + 1], fb);
+#pragma unroll
+                        for (int i = 0; i < NW; ++i)
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                widen(w[p][i][kk][v], w[p][i][kk][v + 1], pow2(ew[p][i] - 127)), x, acc[i], 0, 0, 0);
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i)
+                    acc[i] = mma_unit<false>(w[p][i][0], w[p][i][1], b[p][0], b[p][1], acc[i], 0, 0);
+            }
+        }
     }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) red[wave][i][lane] = acc[i];
-    __syncthreads();
-    if (wave) return;
     f32x4 v[NW];
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        v[i] = red[0][i][lane];
+        for (int i = 0; i < NW; ++i) red[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (wave) return;
 #pragma unroll
-        for (int k = 1; k < kThinWaves; ++k) v[i] += red[k][i][lane];
+        for (int i = 0; i < NW; ++i) {
+            v[i] = red[0][i][lane];
+#pragma unroll
+            for (int k = 1; k < kThinWaves; ++k) v[i] += red[k][i][lane];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) v[i] = acc[i];
     }
     const int c = cb * 16 + 4 * q;
     if (t.r0 + lr >= t.end || c >= a.R) return;
@@ -562,7 +607,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
         float h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = silu(v[0][i]) * v[NW - 1][i];
-        if (FP8)  // float32, quantised by a launch of its own: a block's maximum is over 128 columns
+        if (FP8)  // float32, quantised later: a block's maximum is over 128 columns
             *reinterpret_cast<f32x4*>(a.out + ((int64_t)row * a.R + c) * 4) = f32x4{h[0], h[1], h[2], h[3]};
         else
             *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
@@ -592,6 +637,11 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 // (each read ends before the barrier of its phase, and wm = 1 reads one phase later, before
 // these).  They are waited for at the end of Ra (the last 128 rows of v) and of Rb (the rest
 // of v + 1), one phase before wm = 0 reads them: the counts are of what was issued since.
+//
+// The e4m3 matrix instruction adds the products of 8 consecutive k after cutting each to
+// multiples of 2^-13 of the power of two of the group's largest (measured: 2^16 + 2^2 in
+// one group gives 2^16, across groups the sum).  That is 2^-9 of the step that quantising the
+// operands has already taken (half of 2^-3); sums across groups, units and waves are fp32.
 constexpr int kTM = 256, kTN = 256, kTileThreads = 512;
 constexpr int kStageA = kTM * kUnit, kStage = (kTM + kTN) * kUnit;
 constexpr uint32_t kOOB = 0x80000000u;  // beyond every buffer: reads give zero

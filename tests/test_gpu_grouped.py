@@ -320,6 +320,17 @@ def test_pass(N, m, d, f, layout, n, typ):
     _check_pass(case, x, ids, w, "pass")
 
 
+@pytest.mark.parametrize("layout", ["plain", "tiled"])
+@pytest.mark.parametrize("n", [1, 3, 8, 40])
+def test_small_8_bit_passes_sum_in_32_bits(n, layout):
+    """Passes of few rows an expert widen the codes: their products carry no cut."""
+    case = Case(64, 4, 1024, 640, "fp8", layout, seed=n)
+    case.eps = lambda K: K * 2.0 ** -23
+    x = (_randn(70 + n, n, 1024) * torch.exp(2 * _randn(71, 1, 1024))).to(BF).cuda()
+    ids, w = _ids(72 + n, n, 4, 64, zipf=1.0)
+    _check_pass(case, x, ids, w, "small")
+
+
 COUNTS = [0, 1, 15, 16, 17, 0, 31, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300, 511, 513, 0]
 
 
