@@ -46,7 +46,7 @@ int check_desc(const moe_layer_desc* d, int32_t n, int32_t dtype) {
 
 // Grouping workspace: [chunks][N + 1] counts
 int group_chunks(int64_t S) { return (int)((S + group_chunk(S) - 1) / group_chunk(S)); }
-size_t group_ws(int64_t S, int N) { return align_up((size_t)group_chunks(S) * (N + 1) * 4); }
+size_t group_ws(int chunks, int N) { return align_up((size_t)chunks * (N + 1) * 4); }
 
 int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
     return (int)std::min<int64_t>((rows * blocks_of(K) + 15) / 16, 16384);
@@ -65,7 +65,7 @@ void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of,
     hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of, queue);
 }
 
-// Workspace of a whole pass, and of the products alone (which use hf and O).
+// Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf and O).
 struct Space {
     size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
 };
@@ -81,13 +81,13 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
         return a;
     };
     p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
-    p.o = take(S * d->d_model * 2);
-    p.hf = take(fp8 ? S * d->d_ff * 4 : 0);
+    // gate/up's fp32 h (quantised before down begins), then O
+    p.hf = p.o = take(std::max(S * d->d_model * 2, fp8 ? S * d->d_ff * 4 : 0));
     p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
     p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
     p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
     p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : 0);
-    p.hist = take(group_ws(S, d->N));
+    p.hist = take(group_ws(kGMaxChunks, d->N));  // (a longer pass may have fewer chunks)
     p.count = take((size_t)d->N * 4);
     p.offset = take((size_t)(d->N + 1) * 4);
     p.sbe = take(S * 4);
@@ -104,11 +104,12 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
 // 218 us thin.  With fewer tiles than units, thin ones spread them: 8 experts of 4096 x 14336, down,
 // at 8 / 16 rows 254 / 255 us square and 167 / 204 us thin (which doubles with every 16 rows).
 // Square tiles' loads run up to two units ahead into the next tile, which takes four
-// units a tile, and have buffer offsets of 31 bits; thin tiles address all of memory.
+// units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
+// tile has beyond it); thin tiles address all of memory.
 bool square(const Args& a, bool fp8, bool gu) {
     const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
-    return kby > 3 * kUnit && a.S >= (tiles >= 1024 ? 4 : 24) * (int64_t)a.N && a.R * kby <= most &&
+    return kby > 3 * kUnit && a.S >= (tiles >= 1024 ? 4 : 24) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
            (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
 }
 
@@ -136,23 +137,27 @@ void launch_product(const Args& a, bool tiled, hipStream_t st) {
             hipLaunchKernelGGL((k_tile<FP8, false, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
         return;
     }
-    const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
+    // A launch holds 2^32 threads at most: as many row tiles at once as keep below that.
     const int64_t cols = (a.R + 15) / 16, units = ((int64_t)a.K * (FP8 ? 1 : 2) + kUnit - 1) / kUnit;
-    if constexpr (!GU) {
-        if (units <= kThinWhole && tiles * cols >= 16 * kCUs) {  // (one token's 1024 tiles: 1.5 us better split)
-            const int grid = (int)(tiles * ((cols + kThinWaves - 1) / kThinWaves));
+    const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
+    auto launch = [&](auto split) {
+        constexpr bool SPLIT = decltype(split)::value;
+        const int64_t wide = SPLIT ? cols : (cols + kThinWaves - 1) / kThinWaves, most = (1 << 23) / wide;
+        Args b = a;
+        for (int64_t t = 0; t < tiles; t += most) {
+            b.tile0 = (int)t;
+            const int grid = (int)(std::min(most, tiles - t) * wide);
             if (tiled)
-                hipLaunchKernelGGL((k_thin<FP8, true, GU, false>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+                hipLaunchKernelGGL((k_thin<FP8, true, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
             else
-                hipLaunchKernelGGL((k_thin<FP8, false, GU, false>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
-            return;
+                hipLaunchKernelGGL((k_thin<FP8, false, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
         }
+    };
+    if constexpr (!GU) {
+        if (units <= kThinWhole && tiles * cols >= 16 * kCUs)  // (one token's 1024 tiles: 1.5 us better split)
+            return launch(std::false_type());
     }
-    const int grid = (int)(tiles * cols);
-    if (tiled)
-        hipLaunchKernelGGL((k_thin<FP8, true, GU, true>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_thin<FP8, false, GU, true>), dim3(grid), dim3(64 * kThinWaves), 0, st, a);
+    launch(std::true_type());
 }
 
 struct Weights {
@@ -255,7 +260,7 @@ extern "C" {
 
 size_t moe_group_workspace_bytes(int32_t n, int32_t m, int32_t N) {
     if (check_slots(n, m, N) != MOE_OK) return 0;
-    return align_up((size_t)kGMaxChunks * (N + 1) * 4);
+    return group_ws(kGMaxChunks, N);
 }
 
 int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t* count, int32_t* offset,
@@ -264,7 +269,7 @@ int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t
     if (!ids || !count || !offset || !slot_by_expert || !distinct || !u_and_err) return MOE_E_INVAL;
     int rc = check_slots(n, m, N);
     if (rc != MOE_OK) return rc;
-    rc = check_ws(ws, ws_bytes, group_ws((int64_t)n * m, N));
+    rc = check_ws(ws, ws_bytes, group_ws(group_chunks((int64_t)n * m), N));
     if (rc != MOE_OK) return rc;
     (void)hipGetLastError();
     Group g{};

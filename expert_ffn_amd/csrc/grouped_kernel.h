@@ -54,6 +54,7 @@ struct Args {
     int32_t* queue;       // square tiles: [8][kLine], tiles taken from each XCD's run, zero at the start
     uint8_t* outs;        // e4m3 gate/up: scale bytes of h
     int N, m, S, R, K;
+    int tile0;            // thin tiles: the launch's first row tile
 };
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -513,7 +514,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
     const int tile = blockIdx.x / CW, cw = blockIdx.x - tile * CW;
     const int cb = SPLIT ? cw : cw * kThinWaves + wave;
     if (!SPLIT && cb >= CB) return;  // (no barrier without SPLIT)
-    const TileAt t = find_tile(a.offset, a.N, a.S, kTile16, tile);
+    const TileAt t = find_tile(a.offset, a.N, a.S, kTile16, a.tile0 + tile);
     if (t.e < 0) return;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
     const int row = min(t.r0 + lr, t.end - 1);

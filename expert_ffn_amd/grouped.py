@@ -48,6 +48,8 @@ def _empty(shape, dtype, dev, stream):
 def _check(name, t, dtype, shape, dev):
     """One tensor of a call: contiguous, of this type, shape and device.  Small calls are
     bound by the host, so what is right is found right in one expression."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor, got %s" % (name, type(t).__name__))
     if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
         return t.data_ptr()
     _check_dev(name, t, dtype, shape)
@@ -251,7 +253,9 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
     with 8-bit weights ``Quantized`` from ``Quantized`` x (``quant_rows``).  Rows from
     offset[N] on are left as they were."""
     fp8, dev = _kind(layer)
-    n = (x.q if isinstance(x, Quantized) else x).shape[0]
+    if isinstance(x, Quantized) != fp8:
+        raise TypeError("x must be %s for this layer" % ("Quantized (quant_rows)" if fp8 else "a bf16 tensor"))
+    n = (x.q if fp8 else x).shape[0]
     S, d, f = n * layer.m, layer.d, layer.d_ff
     _, offset, slots, _, _ = _check_grouping(grouping, n, layer.m, layer.N, dev)
     desc, L = layer.desc(), lib()

@@ -542,3 +542,165 @@ def test_side_streams(typ):
     for i in range(2):
         for y in got[i]:
             assert torch.equal(y, want[i])
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("layout,d,f", [("tiled", 512, 576), ("plain", 528, 640), ("plain", 784, 720),
+                                        ("tiled", 896, 960), ("plain", 33040, 128), ("plain", 128, 33168)])
+def test_contractions_of_every_length(layout, d, f, typ):
+    """From four units of 128 bytes a tile, the fewest of the square tiles, to more scale
+    bytes than a work group has threads."""
+    say("lengths", layout, d, f, typ)
+    counts = [300, 0, 41, 7]
+    case = Case(len(counts), 1, d // (1 if typ == "fp8" else 2), f // (1 if typ == "fp8" else 2), typ, layout, seed=5)
+    ids = _ids_of_counts(counts, 6)
+    n = ids.shape[0]
+    _check_pass(case, _randn(7, n, case.d).to(BF).cuda(), ids, _randn(8, n, 1).cuda(), "lengths")
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+def test_square_tiles_of_many_experts(typ):
+    N, m, n = 1000, 3, 1500
+    case = Case(N, m, 512, 528, typ, "plain", seed=4)
+    ids, w = _ids(5, n, m, N, zipf=0.7, pad=11)
+    _check_pass(case, _randn(6, n, 512).to(BF).cuda(), ids, w, "many experts")
+
+
+def _gpu_layer(N, m, d, f, typ, layout, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    W = [torch.randn(N, *s, generator=g, device="cuda", dtype=BF).mul_(0.05) for s in ((f, d), (f, d), (d, f))]
+    layer = efa.Layer(*W, m=m)
+    if typ == "fp8":
+        layer = layer.fp8_copy()
+    return layer, layer.tiled_copy() if layout == "tiled" else layer
+
+
+def _columns(layer, which, e, cols):
+    """Rows `cols` of expert e's matrix in 64 bits (plain layers)."""
+    if isinstance(layer, efa.Fp8Layer):
+        q, s = (layer.gate, layer.up, layer.down)[which]
+        K = q.shape[2]
+        return q[e, cols].double() * _pow2(s[e, cols // 128].long() - 127).repeat_interleave(128, dim=1)[:, :K]
+    return (layer.w_gate, layer.w_up, layer.w_down)[which][e, cols].double()
+
+
+def _check_sample(plain, x, ids, w, g, h, y, rows, hc, yc, fp8):
+    """h at rows x hc against x, y at those rows' tokens x yc against h (m = 1: a token a row)."""
+    token = g.slot_by_expert[rows].long()
+    assert plain.m == 1
+    xq = efa.quant_rows(x[token].contiguous()) if fp8 else x[token]
+    xv = _row_values(xq) if fp8 else xq.double()
+    hq = efa.Quantized(h.q[rows], h.scale[rows]) if fp8 else h[rows]
+    hv = _row_values(hq) if fp8 else hq.double()
+    cut = 7 * 2.0 ** -13 if fp8 else 0.0
+    ex, eh = xv.shape[1] * 2.0 ** -23 + cut, hv.shape[1] * 2.0 ** -23 + cut
+    for i in range(rows.numel()):
+        e = int(ids[token[i], 0])
+        W = [_columns(plain, k, e, hc) for k in (0, 1)]
+        a, b = (xv[i] @ m_.T for m_ in W)
+        da, db = (ex * (xv[i].abs() @ m_.abs().T) for m_ in W)
+        s = a * torch.sigmoid(a)
+        want = s * b
+        tol = 1.1 * b.abs() * da + s.abs() * db + 1.1 * da * db + 2.0 ** -20 * want.abs()
+        if fp8:
+            step = _pow2(hq.scale[i, hc // 128].long() - 127) * 2.0 ** -10
+            tol = tol + torch.maximum(2.0 ** -4 * (want.abs() + tol), step)
+        else:
+            tol = tol + 2.0 ** -8 * (want.abs() + tol)
+        _within(hv[i, hc], want, tol, "h %d" % i)
+        D = _columns(plain, 2, e, yc)
+        o = D @ hv[i]
+        do = eh * (D.abs() @ hv[i].abs())
+        wt = w[token[i], 0].double()
+        tol = wt.abs() * (do + (2.0 ** -8 + 2.0 ** -22) * o.abs())
+        want = wt * o
+        _within(y[token[i], yc], want, tol + 2.0 ** -8 * (want.abs() + tol), "y %d" % i)
+
+
+def _spread(n, k):
+    return torch.linspace(0, n - 1, k, dtype=torch.float64, device="cuda").long().unique()
+
+
+def _run_parts(layer, x, ids, w, fp8):
+    g = efa.group_slots(ids, layer.N)
+    h = efa.grouped_gate_up(layer, efa.quant_rows(x) if fp8 else x, g)
+    return g, h, efa.grouped_down(layer, h, ids, w, g)
+
+
+@pytest.mark.parametrize("typ,n", [("bf16", 140001), ("fp8", 270001)])
+def test_x_beyond_31_bits(typ, n):
+    """More than 2 GiB of x."""
+    say("x beyond 31 bits", typ)
+    d, f = 8192, 1040
+    plain, layer = _gpu_layer(2, 1, d, f, typ, "plain", 1)
+    x = torch.randn(n, d, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda", dtype=BF)
+    ids = (torch.arange(n, device="cuda", dtype=torch.int32) % 2)[:, None].contiguous()
+    w = torch.rand(n, 1, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    fp8 = typ == "fp8"
+    g, h, y = _run_parts(layer, x, ids, w, fp8)
+    _check_sample(plain, x, ids, w, g, h, y, _spread(n, 12), _spread(f, 40), _spread(d, 40), fp8)
+
+
+@pytest.mark.parametrize("layout,d,f,typ", [("plain", 16384, 65272, "bf16"), ("tiled", 16384, 65248, "bf16"),
+                                            ("plain", 16384, 65408, "bf16"), ("tiled", 16384, 65408, "bf16"),
+                                            ("plain", 32752, 65536, "fp8"), ("tiled", 32640, 65472, "fp8")])
+def test_matrices_of_31_bits(layout, d, f, typ):
+    """Matrices of almost and of more than 2 GiB, less and more than a tile below it."""
+    say("matrices of 31 bits", layout, d, f, typ)
+    n = 300
+    plain, layer = _gpu_layer(1, 1, d, f, typ, layout, 1)
+    x = torch.randn(n, d, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda", dtype=BF)
+    ids = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    w = torch.rand(n, 1, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    fp8 = typ == "fp8"
+    g, h, y = _run_parts(layer, x, ids, w, fp8)
+    _check_sample(plain, x, ids, w, g, h, y, _spread(n, 6), _spread(f, 60), _spread(d, 60), fp8)
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+def test_a_million_rows(typ):
+    """More thin tiles than one launch holds, and O and h beyond 32 bits."""
+    say("a million rows", typ)
+    n, d, f = (1 << 20) + 1, 64, 4096
+    plain, layer = _gpu_layer(5, 1, d, f, typ, "tiled", 1)
+    x = torch.randn(n, d, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda", dtype=BF)
+    ids = torch.randint(0, 5, (n, 1), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda",
+                        dtype=torch.int32)
+    w = torch.rand(n, 1, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    fp8 = typ == "fp8"
+    g, h, y = _run_parts(layer, x, ids, w, fp8)
+    _check_sample(plain, x, ids, w, g, h, y, _spread(n, 40), _spread(f, 60), _spread(d, 60), fp8)
+    assert torch.equal(efa.expert_grouped(layer, x, ids, w), y)
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("n", [2, 700])
+def test_captured_parts(typ, n):
+    """Grouping, quantisation and the products captured one after the other, replayed on
+    other values with eager calls between."""
+    case = Case(8, 2, 256, 320, typ, "tiled")
+    fp8 = typ == "fp8"
+    x = _randn(1, n, 256).to(BF).cuda()
+    ids, w = _ids(2, n, 2, 8)
+    _run_parts(case.layer, x, ids, w, fp8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g, h, y = _run_parts(case.layer, x, ids, w, fp8)
+    for i in range(3):
+        x.copy_(_randn(30 + i, n, 256).to(BF))
+        ids.copy_(_ids(40 + i, n, 2, 8)[0])
+        _, _, want = _run_parts(case.layer, x, ids, w, fp8)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_x_is_of_the_layers_type():
+    x = _randn(1, 4, 64).to(BF).cuda()
+    ids, _ = _ids(2, 4, 1, 2)
+    for typ, xin in (("bf16", efa.quant_rows(x)), ("fp8", x), ("bf16", x.float())):
+        case = Case(2, 1, 64, 64, typ)
+        with pytest.raises(TypeError):
+            efa.grouped_gate_up(case.layer, xin, efa.group_slots(ids, 2))

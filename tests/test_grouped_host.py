@@ -149,3 +149,13 @@ def test_python_refusals_without_a_gpu():
     with pytest.raises(ValueError):
         efa.Fp8Layer((torch.zeros(2, 16, 16),), (x, x), (x, x), m=1)
     assert grouped._blocks(128) == 1 and grouped._blocks(129) == 2
+
+
+@pytest.mark.parametrize("dtype", [_abi.MOE_BF16, _abi.MOE_FP8])
+def test_a_longer_pass_needs_no_less(dtype):
+    """The workspace of n tokens serves fewer, also where the grouping takes fewer and
+    longer chunks for more slots (from 8193 and 65537 slots on)."""
+    d = _desc(N=1024, m=1, d_model=16, d_ff=16, dtype=dtype)
+    ns = [1, 2, 8191, 8192, 8193, 65535, 65536, 65537, 70000, 131072, 131073, 262144, 262145, 1 << 22]
+    sizes = [_abi.lib().moe_grouped_workspace_bytes(ctypes.byref(d), n) for n in ns]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])), sizes
