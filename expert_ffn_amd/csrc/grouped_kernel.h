@@ -628,16 +628,20 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 // The two waves of a SIMD (wm = 0, 1) take turns: while one reads its operands of half a
 // unit from shared memory, the other runs the products of its own.  A unit has four
 // phases, a barrier after each: Ra (all weight rows and the first 128 rows), Ma (their
-// products), Rb (the other 128), Mb; wm = 1 is one phase behind.  Two units of
-// each operand fit in shared memory.  A wave's eight loads of a unit go out as soon as what
-// they overwrite has been read, and none in Ra, which reads the most:
+// products), Rb (the other 128), Mb; wm = 1 is one phase behind.  In Ma a block's place is free
+// after its products, and a block of the other 128 rows is asked for at once (gate/up in e4m3 has
+// no registers for that: in Rb).  Two units of each operand fit in shared memory.  A wave's eight
+// loads of a unit go out as soon as what they overwrite has been read:
 //     phase of unit v     loads                                       overwrites, last read
-//     Ma                  last 128 rows of v + 1 (two)                of v - 1, in Rb (v - 1)
+//     Ra                  last 128 rows of v + 1 (two)                of v - 1, in Ma / Rb (v - 1)
 //     Rb, Mb              weight rows, first 128 rows of v + 2        of v, in Ra (v)
 //                         (three each)
-// (each read ends before the barrier of its phase, and wm = 1 reads one phase later, before
-// these).  They are waited for at the end of Ra (the last 128 rows of v) and of Rb (the rest
-// of v + 1), one phase before wm = 0 reads them: the counts are of what was issued since.
+// (each read has ended before the barrier of Ra or Rb, and wm = 1 reads one phase later, before
+// these).  They are waited for at the end of Mb (the last 128 rows of the next unit) and of Rb
+// (the rest of it), one phase before wm = 0 reads them: the counts are of what was issued since.
+// With the last 128 rows read in Rb alone and loaded in Ma, gate/up of 4096 tokens (128 bf16 experts of
+// 2048 x 768) took 298 us for 292, 8-bit down 133 for 128; with the first 128 rows also read a phase ahead
+// (and so waited for a phase earlier) 313.
 //
 // The e4m3 matrix instruction adds the products of 8 consecutive k after cutting each to
 // multiples of 2^-13 of the power of two of the group's largest (measured: 2^16 + 2^2 in
@@ -785,6 +789,7 @@ struct TileLds {
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
     uint8_t ws[2][2][kMaxKB];  // e4m3: a tile's weight scale bytes: of both matrices, or of 128 rows each
     int after;              // the tile after the next
+    int32_t token[kTM];     // gate/up: of the (next) tile's rows
     int32_t offset[MOE_MAX_EXPERTS + 1];
 };
 
@@ -882,28 +887,27 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
 
     Place p = take(mine);
     if (!p.rows) return;
-    uint32_t gather[4] = {0, 0, 0, 0}, gather_n[4] = {0, 0, 0, 0};  // gate/up: offsets of the rows' tokens
-    uint32_t xrow = 0, xrow_n = 0;                                  // e4m3: of this thread's row's scale bytes
-    auto ask = [&](const Place& t, uint32_t (&g)[4], uint32_t& x) {  // the slots of a tile's rows
-        const int last = max(t.rows - 1, 0);
-        if (GU) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = arg()->slot[t.r0 + min((i * 8 + wave) * 8 + (lane >> 3), last)];
-        }
-        if (FP8) {
-            const int r = t.r0 + min(tid & (kTM - 1), last);
-            x = GU ? arg()->slot[r] : r;
-        }
+    // Gate/up: offsets of the tokens of a lane's rows; e4m3: of this thread's row's scale bytes.
+    uint32_t gather[4] = {0, 0, 0, 0}, xrow = 0;
+    auto row_of = [&](const Place& t) { return t.r0 + min(tid & (kTM - 1), max(t.rows - 1, 0)); };
+    auto ask = [&](const Place& t) { return arg()->slot[row_of(t)]; };  // the slot of this thread's row
+    auto keep = [&](int slot) {
+        if (tid < kTM) lds.token[tid] = (int)token(slot);
     };
-    auto address = [&](uint32_t (&g)[4], uint32_t& x) {
-        if (GU) {
+    auto address = [&](int first, int end) {  // of loads first .. end
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = (uint32_t)token(g[i]) * KBy + ca;
-        }
-        if (FP8) x = (uint32_t)(GU ? token(x) : min((int)x, last_slot)) * KB;
+        for (int i = first; i < end; ++i)
+            gather[i] = (uint32_t)lds.token[(i * 8 + wave) * 8 + (lane >> 3)] * KBy + ca;
     };
-    ask(p, gather, xrow);
-    address(gather, xrow);
+    auto row_address = [&](const Place& t) {
+        if (FP8) xrow = (uint32_t)(GU ? lds.token[tid & (kTM - 1)] : min(row_of(t), last_slot)) * KB;
+    };
+    if (GU) {
+        keep(ask(p));
+        __syncthreads();
+        address(0, 4);
+    }
+    row_address(p);
     // e4m3 scale bytes.  Weights: a tile's, of 128 rows of each matrix or of two 128 rows, at
     // once.  Rows: a thread a row, four units at a time, the word that ends with the array
     // where it has fewer left.
@@ -968,9 +972,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     int xpar = 0, spar = 0;  // where the scale bytes of the rows and weights at hand are
     auto tile = [&](auto nb) {
         constexpr int NB = decltype(nb)::value, H = NB < 4 ? NB : 4;  // row blocks of a wave; of Ra and Ma
+        constexpr int EARLY = FP8 && GU ? 0 : 4;  // row blocks of the second half read in Ma
         Place pn{0, 0, 0, 0};  // the next tile
         int got = 0;
-        uint8_t wsn[2] = {0, 0};  // the next tile's weight scale bytes
+        int slot_n = 0;           // the next tile's, as asked for
+        uint8_t wsn[2] = {0, 0};  // its weight scale bytes
         Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
         Weights wr = weights_of(p);
         f32x4 acc[NB][4];
@@ -983,32 +989,26 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             char* there = lds.stage[par ^ 1];
             u32x4 b[4][2], x[H][2];
             uint32_t ex[2] = {0u, 0u};
-            auto read_rows = [&](int first, int end) {
+            auto read_rows = [&](int i) {  // row block i, into its place among the H
 #pragma unroll
-                for (int i = first; i < end; ++i)
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-                        x[i - first][kk] =
-                            *reinterpret_cast<const u32x4*>(here + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
+                for (int kk = 0; kk < 2; ++kk)
+                    x[i % H][kk] = *reinterpret_cast<const u32x4*>(here + swz((i * 2 + wm) * 16 + lr, kk * 4 + q));
             };
             int e0 = 0, e1 = 0;
-            // the products of row blocks first .. end, `loads` after the first half of them
-            auto products = [&](auto first, auto end, auto loads) {
+            // the products of row blocks first .. end, `then(i)` after those of block i
+            auto products = [&](auto first, auto end, auto then) {
                 constexpr int F = decltype(first)::value, E = decltype(end)::value;
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = F; i < E; ++i) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i - F][0], x[i - F][1], acc[i][j],
+                        acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i % H][0], x[i % H][1], acc[i][j],
                                                   GU && j >= 2 ? e1 : e0, (int)ex[i / 4], i);
-                    if (i == (F + E - 1) / 2) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        loads();
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    then(i);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (E <= F) loads();
                 __builtin_amdgcn_s_setprio(0);
 #pragma unroll
                 for (int i = F; i < E; ++i)
@@ -1019,8 +1019,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             int ua = u + 1, ub = u + 2;  // past the last unit: the next tile's first
             if (ua >= U) {
                 xb = rows_of(pn);
-                gather[2] = gather_n[2];
-                gather[3] = gather_n[3];
+                if (GU) address(2, 4);
                 ua = 0;
             }
 #pragma unroll
@@ -1030,7 +1029,10 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     b[j][kk] = *reinterpret_cast<const u32x4*>(
                         here + kStageA +
                         (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
-            read_rows(0, H);
+#pragma unroll
+            for (int i = 0; i < H; ++i) read_rows(i);
+            load_rows(xb, gather, ua, there, 2);
+            load_rows(xb, gather, ua, there, 3);
             if (FP8) {
                 const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[xpar][u & 3][wm * 128 + lr * 8]);
                 ex[0] = v[0];
@@ -1039,18 +1041,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 if (GU) e1 = lds.ws[spar][1][u];
             }
             wait_lds();
-            wait_past(std::integral_constant<int, 6>(), u == 0 ? before : 0);
             block_barrier();
             // Ma
-            products(std::integral_constant<int, 0>(), std::integral_constant<int, H>(), [&] {
-                load_rows(xb, gather, ua, there, 2);
-                load_rows(xb, gather, ua, there, 3);
+            products(std::integral_constant<int, 0>(), std::integral_constant<int, H>(), [&](int i) {
+                if (i < EARLY && i + H < NB) read_rows(i + H);
             });
             block_barrier();
             // Rb
             if (u == 0) {
                 pn = take(after);
-                ask(pn, gather_n, xrow_n);
+                if (GU) slot_n = ask(pn);
                 if (tid == 0) {
                     int at = xcd * kLine;
                     asm volatile("" : "+v"(at));  // a lane's address: a wave's would be waited for at once
@@ -1065,18 +1065,18 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     keep_weight_scale(spar ^ 1, tid, wsn[0]);
                     if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
                 }
-                address(gather_n, xrow_n);
+                if (GU) keep(slot_n);
                 if (tid == 0) lds.after = got + 2 * step;
             } else if (ub == U) {
                 wr = weights_of(pn);
                 xa = rows_of(pn);
-                gather[0] = gather_n[0];
-                gather[1] = gather_n[1];
-                if (FP8) xrow = xrow_n;
+                if (GU) address(0, 2);
+                row_address(pn);
                 after = uni(lds.after);
             }
             if (ub >= U) ub -= U;
-            read_rows(H, NB);
+#pragma unroll
+            for (int i = H + EARLY; i < NB; ++i) read_rows(i);
             if (FP8) {
                 // The next four units' row scales (or the next tile's first) are asked for two units
                 // ahead and kept one ahead.
@@ -1094,11 +1094,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             wait_past(std::integral_constant<int, 5>(), u == 0 ? before : 0);
             block_barrier();
             // Mb
-            products(std::integral_constant<int, H>(), nb, [&] {
+            auto last = [&] {
                 load_weights(wr, ub, here, 2);
                 load_weights(wr, ub, here, 3);
                 load_rows(xa, gather, ub, here, 1);
+            };
+            if (NB <= H) last();
+            products(std::integral_constant<int, H>(), nb, [&](int i) {
+                if (i == (H + NB - 1) / 2) last();
             });
+            wait_vm<6>();
             block_barrier();
             par ^= 1;
         }
