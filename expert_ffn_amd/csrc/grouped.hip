@@ -98,18 +98,25 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     return p;
 }
 
-// Square or thin tiles.  Square ones read the weights at the memory's pace from few rows on
-// if there are tiles for all compute units: 128 experts of 2048 x 768, gate and up, at 2 / 4 /
-// 8 / 16 / 32 rows an expert 153 / 133 / 133 / 134 / 137 us square and 142 / 143 / 145 / 150 /
-// 218 us thin.  With fewer tiles than units, thin ones spread them: 8 experts of 4096 x 14336, down,
-// at 8 / 16 rows 254 / 255 us square and 167 / 204 us thin (which doubles with every 16 rows).
+// Square or thin tiles.  Thin ones take as long again with every 16 rows of an expert, square ones the
+// same from few rows on.  At 8 / 16 / 24 rows of every expert, thin against square, us:
+//     128 experts of 2048 x 768   gate/up bf16   141 / 150 / 205   148 / 134 / 136
+//                                 gate/up e4m3    77 /  90 / 119    82 /  83 /  83
+//                                 down bf16       84 /  98 / 131    89 /  88 /  94
+//                                 down e4m3       42 /  49 /  71    52 /  53 /  56
+//     8 experts of 4096 x 14336   down bf16              204 / 301         234 / 238
+// (the last with fewer square tiles than compute units).  Routing is never that even, and an expert of
+// 17 rows already takes two thin tiles: passes of the first layer at a mean of 7 / 9 / 11 rows, ids uniform,
+// bf16 223 / 226 / 234 against 235 / 220 / 221, e4m3 126 / 130 / 137 against 142 / 142 / 143; with
+// popularity falling as 1 / rank^1.1, bf16 151 / 171 / 190 against 139 / 156 / 158, e4m3 89 / 102 / 117 against
+// 94 / 107 / 110.
 // Square tiles' loads run up to two units ahead into the next tile, which takes four
 // units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
 // tile has beyond it); thin tiles address all of memory.
 bool square(const Args& a, bool fp8, bool gu) {
     const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
-    return kby > 3 * kUnit && a.S >= (tiles >= 1024 ? 4 : 24) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
+    return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? (fp8 ? 12 : 8) : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
            (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
 }
 

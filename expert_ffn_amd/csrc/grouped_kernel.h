@@ -123,7 +123,9 @@ __device__ __forceinline__ uint32_t finite_codes4(f32x4 v, float inv) {
 }
 
 // Rows of bf16 (or float32) values to codes and scale bytes, in blocks of 128 along the row:
-// sixteen lanes a block, eight values a lane; work group g of G.
+// sixteen lanes a block, eight values a lane (16 bytes of bf16), so that a block's maximum takes
+// four exchanges and no shared memory; work group g of G.  Bound by memory: 16384 x 2048 in 22-24 us,
+// 101 MB at 4.2-4.6 TB/s (a large copy here: 4.9).
 template <bool F32>
 __device__ __forceinline__ void quant_rows(const char* __restrict__ x, int64_t rows, int K, uint8_t* __restrict__ q,
                                            uint8_t* __restrict__ s, int64_t g, int64_t G) {
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(256) void k_quant_rows(const char* __restrict__ x, 
 }
 
 // Codes and scale bytes of rows back to bf16: four bits of significand fit bf16's eight,
-// so this is exact down to bf16's own least value.
+// so this is exact down to bf16's own least value.  16384 x 2048 in 17 us: 101 MB at 5.9 TB/s.
 __global__ __launch_bounds__(256) void k_dequant_rows(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                      int64_t rows, int K, char* __restrict__ x) {
     const int KB = (K + kBlk - 1) / kBlk;
@@ -240,8 +242,10 @@ __global__ __launch_bounds__(256) void k_quant_weights(const char* __restrict__ 
 // one launch.  The rank of a slot among equal ids of its wave's 64 comes from one ballot
 // for each bit of the id, so the order is that of the slots, whatever the timing.
 //
-// Latency is the time (a few loads, scans and barriers), so a pass's other preparation
-// rides along: work groups from G on quantise x, and the first clears the queues.
+// Latency is the time (a few loads, scans and barriers: 576 slots 5.4 us, 131072 slots 4.6 + 7.6 us,
+// where the memory's share is 0.2 us), so a pass's other preparation rides along: work groups
+// from G on quantise x, and the first clears the queues.  One chunk up to 8192 slots: of 576 slots two launches
+// took 15.4 us with the host's share, one 9.8; beyond, one work group's loads take longer than a launch.
 constexpr int kGThreads = 1024, kGWaves = kGThreads / 64;
 constexpr int kGMaxChunks = 64, kGOne = 8192;  // slots of one chunk
 
@@ -488,10 +492,18 @@ __device__ __forceinline__ TileAt find_tile(const int32_t* __restrict__ offset, 
 // matrix instruction rounds only to fp32, where its e4m3 form cuts small ones (see the
 // note at k_tile).
 //
-// SPLIT: the four waves share a tile's contraction.  Without, each has a tile of its own and
-// all its units (at most kThinWhole) in flight: a split contraction of six units left two waves one
-// unit each, and 128 e4m3 experts' down tiles (d_ff 768) took 73 us for 201 MB.
-constexpr int kThinWaves = 4, kThinAhead = 4, kThinWhole = 8;  // units of a wave's loads in flight
+// SPLIT: the four waves share a tile's contraction.  Without, for short contractions of many tiles,
+// each has a tile of its own: 128 experts of 2048 x 768 at 2 rows, down, 85 -> 76 us in bf16 (12 units),
+// 73 -> 37 in e4m3 (6 units; 201 MB at 5.5 TB/s), but 22 units in bf16 67 -> 70.  Few units of a wave's loads in
+// flight leave registers for more waves: of 2 / 3 / 4 / 6 / 8 without SPLIT that e4m3 down took
+// 36 / 37 / 40 / 43 / 51 us, one of 1408 columns 36 / 33 / 34 / 36 / 44; e4m3 gate/up with SPLIT at 1 / 2 / 3 / 4
+// 72 / 70 / 76 / 79; bf16 differs by 1-3 %.
+// Memory bounds them: gate/up and down of 32 tokens (skewed over 128 bf16 experts of 2048 x 768) 48 + 38 us;
+// of one token on 8 e4m3 experts (25 + 13 MB in all) 9.8 + 7.0 us, where the latency of a launch and its first
+// loads is most.  Quantising h inside e4m3 down tiles, which spares a launch, made each of
+// them read 128 columns of fp32 h first: one token's pass 29 us for 24.
+constexpr int kThinWaves = 4;
+constexpr int kThinWhole = 16;  // most units of a contraction without SPLIT
 
 // Two words of codes (eight values) to bf16, scaled.
 __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float f) {
@@ -506,7 +518,7 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float f) {
 
 template <bool FP8, bool TILED, bool GU, bool SPLIT>
 __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
-    constexpr int ES = FP8 ? 1 : 2, NW = GU ? 2 : 1, AHEAD = SPLIT ? kThinAhead : kThinWhole;
+    constexpr int ES = FP8 ? 1 : 2, NW = GU ? 2 : 1, AHEAD = !SPLIT ? 3 : GU ? 2 : 4;
     __shared__ f32x4 red[SPLIT ? kThinWaves : 1][NW][64];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int lr = lane & 15, q = lane >> 4;
@@ -643,6 +655,12 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 // 2048 x 768) took 298 us for 292, 8-bit down 133 for 128; with the first 128 rows also read a phase ahead
 // (and so waited for a phase earlier) 313.
 //
+// What they reach: one expert's 4096 rows (gate/up, bf16) 1.1-1.16 PFLOP/s, 0.83 of what a large library
+// product reaches here.  128 experts of 2048 x 768 with 32768 skewed rows: bf16 gate/up 291 us (0.71
+// PFLOP/s), e4m3 down 110 us; 43 % of those tiles' rows are missing (a unit costs the
+// same), each compute unit has 5 or 6 tiles, and a tile's change and results, 2 of its 32 units' time
+// at this width, are not hidden.  Tiles of 128 rows instead: 366 us for 297 and 165 for 134.
+//
 // The e4m3 matrix instruction adds the products of 8 consecutive k after cutting each to
 // multiples of 2^-13 of the power of two of the group's largest (measured: 2^16 + 2^2 in
 // one group gives 2^16, across groups the sum).  That is 2^-9 of the step that quantising the
@@ -688,8 +706,10 @@ struct Place {
 };
 
 // Every expert's row tiles and what they cost, one scan kept by the wave: lane l holds
-// N / 64 experts.  A unit of a tile takes about the same time up to 64 rows (the weights'
-// way), then more with every 64 (clocks / 100, measured).
+// N / 64 experts.  A unit of a tile takes about the same time whatever its rows (the four
+// phases' reads, loads and barriers; clocks / 100, measured): shares by 14 / 17 / 23 / 29 for up to
+// 64 / 128 / 192 / 256 rows, nearer to the rows' own work, cost 8-bit down of 4096 tokens 142 us for 133
+// and the 8-bit pass of 8191 tokens 531 for 510.
 __device__ __forceinline__ int tile_cost(int rows) { return rows <= 64 ? 23 : rows <= 128 ? 26 : rows <= 192 ? 28 : 30; }
 
 // offset, kept in shared memory: a load from memory would wait for every operand's before it
@@ -1229,6 +1249,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         xpar = uni(xpar);
         spar = uni(spar);
     }
+    wait_vm<0>();  // the zeros of no tile are still on their way to shared memory
     if (!wm) block_barrier();
 }
 
@@ -1244,7 +1265,10 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 
 // y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
 // to bf16 once.  A wave takes 512 columns of a token (eight a lane); the lanes look up the
-// token's slots together, so that the loads of O go out eight at a time: they are the time.
+// token's slots together, so that the loads of O go out eight at a time: they are the time
+// (4096 tokens of 8 x 2048 in 25 us: 151 MB at 6 TB/s).  O is bf16: in fp32 the products would write
+// and this read 134 MB more each for those tokens, 45-50 us of their 128 + 25.  That rounding of each
+// term is independent of y's own, so the two together are about sqrt(1 + sum w^2) of one.
 // info (may be null): U, ids status, MOE_OK.
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
