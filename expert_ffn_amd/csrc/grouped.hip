@@ -60,11 +60,6 @@ void run_group(Group g, hipStream_t st) {
     hipLaunchKernelGGL(k_group_scatter, dim3(g.G > 1 ? g.G : 1 + quant), dim3(kGThreads), 0, st, g);
 }
 
-void run_row_of(const int32_t* sbe, const int32_t* rows, int S, int32_t* row_of, int32_t* queue, hipStream_t st) {
-    static_assert(kQueue == 256, "");
-    hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, rows, S, row_of, queue);
-}
-
 // Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf and O).
 struct Space {
     size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
@@ -131,6 +126,22 @@ Args shape_of(int N, int m, int n, int R, int K) {
 }
 bool square_gate_up(const moe_layer_desc* d, int n) {
     return square(shape_of(d->N, d->m, n, d->d_ff, d->d_model), d->dtype == MOE_FP8, true);
+}
+bool square_down(const moe_layer_desc* d, int n) {
+    return square(shape_of(d->N, d->m, n, d->d_model, d->d_ff), d->dtype == MOE_FP8, false);
+}
+
+// What a pass's grouping leaves for the products, where they run by themselves: an empty queue for
+// square tiles, and the rows of the slots, which thin down tiles write themselves.
+void before_gate_up(const moe_layer_desc* d, int n, int32_t* queue, hipStream_t st) {
+    if (square_gate_up(d, n)) hipLaunchKernelGGL(k_zero_queue, dim3(1), dim3(kQueue), 0, st, queue);
+}
+void before_down(const moe_layer_desc* d, int n, const int32_t* sbe, const int32_t* offset, int32_t* row_of,
+                 int32_t* queue, hipStream_t st) {
+    static_assert(kQueue == 256, "");
+    const int S = n * d->m;
+    if (square_down(d, n))
+        hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, offset + d->N, S, row_of, queue);
 }
 
 template <bool FP8, bool GU>
@@ -199,7 +210,7 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
 
 template <bool FP8>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
-              const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, const int32_t* row_of, void* y,
+              const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, int32_t* row_of, void* y,
               void* o, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
     Args a = shape_of(d->N, d->m, n, d->d_model, d->d_ff);
     a.x = reinterpret_cast<const char*>(h);
@@ -210,6 +221,7 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.slot = sbe;
     a.out = reinterpret_cast<char*>(o);
     a.queue = queue;
+    if (!u_err) a.row_of = row_of;  // (a pass's grouping has left them)
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
     hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
@@ -313,7 +325,7 @@ int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* wei
     if (rc != MOE_OK) return rc;
     int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
-    hipLaunchKernelGGL(k_zero_queue, dim3(1), dim3(kQueue), 0, stream_of(hip_stream), queue);
+    before_gate_up(desc, n, queue, stream_of(hip_stream));
     run_gate_up<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr}, x, nullptr, n, offset,
                        slot_by_expert, h, nullptr, nullptr, queue, stream_of(hip_stream));
     return launched();
@@ -332,7 +344,7 @@ int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* w
     if (rc != MOE_OK) return rc;
     int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
-    hipLaunchKernelGGL(k_zero_queue, dim3(1), dim3(kQueue), 0, stream_of(hip_stream), queue);
+    before_gate_up(desc, n, queue, stream_of(hip_stream));
     run_gate_up<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up}, xq, x_scale, n,
                       offset, slot_by_expert, hq, h_scale, reinterpret_cast<char*>(ws) + p.hf, queue,
                       stream_of(hip_stream));
@@ -353,7 +365,7 @@ int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weight
     char* b = reinterpret_cast<char*>(ws);
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
-    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, queue, stream_of(hip_stream));
+    before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
     run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
                     slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
     return launched();
@@ -374,7 +386,7 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
     char* b = reinterpret_cast<char*>(ws);
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
-    run_row_of(slot_by_expert, offset + desc->N, n * desc->m, row_of, queue, stream_of(hip_stream));
+    before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
     run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
                    slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
     return launched();

@@ -55,6 +55,7 @@ struct Args {
     uint8_t* outs;        // e4m3 gate/up: scale bytes of h
     int N, m, S, R, K;
     int tile0;            // thin tiles: the launch's first row tile
+    int32_t* row_of;      // thin down tiles: null, or the row of each slot, to be written
 };
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -530,6 +531,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
     if (t.e < 0) return;
     const int KBy = a.K * ES, U = (KBy + kUnit - 1) / kUnit, KB = (a.K + kBlk - 1) / kBlk;
     const int row = min(t.r0 + lr, t.end - 1);
+    if (!GU && a.row_of && cb == 0 && threadIdx.x < kTile16) a.row_of[min(max(a.slot[row], 0), a.S - 1)] = row;
     int64_t xrow = row;
     if (GU) xrow = min(max(a.slot[row], 0), a.S - 1) / a.m;
     const char* wp[2];
