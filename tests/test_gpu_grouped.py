@@ -704,3 +704,26 @@ def test_x_is_of_the_layers_type():
         case = Case(2, 1, 64, 64, typ)
         with pytest.raises(TypeError):
             efa.grouped_gate_up(case.layer, xin, efa.group_slots(ids, 2))
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("n", [3, 400])
+def test_many_slots_a_token(typ, n):
+    """More slots a token than a wave has lanes, some of them empty."""
+    N, m = 160, 130
+    case = Case(N, m, 256, 208, typ, "plain", seed=n)
+    ids, w = _ids(5, n, m, N)
+    ids[n // 2, 1:129] = -1
+    ids[0, :64] = N
+    _check_pass(case, _randn(6, n, 256).to(BF).cuda(), ids, w, "many slots")
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("n", [20, 1300])
+def test_the_same_bits_every_time(typ, n):
+    case = Case(32, 4, 512, 384, typ, "tiled")
+    x = _randn(1, n, 512).to(BF).cuda()
+    ids, w = _ids(2, n, 4, 32, zipf=1.0, pad=n // 9)
+    first = efa.expert_grouped(case.layer, x, ids, w)
+    for _ in range(8):
+        assert torch.equal(efa.expert_grouped(case.layer, x, ids, w), first)
