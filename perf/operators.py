@@ -194,7 +194,8 @@ def prepare(case, seed):
         st["x"] = x.to(torch.bfloat16)
         if own:
             import expert_ffn_amd as efa
-            st["out"] = efa.quant_rows(st["x"])
+            st["out"] = efa.Quantized(torch.empty(case["n"], case["d"], dtype=torch.float8_e4m3fn, device="cuda"),
+                                      torch.empty(case["n"], -(-case["d"] // 128), dtype=torch.uint8, device="cuda"))
             st["values"] = torch.empty_like(st["x"])
         return st
     ids, w = _routing(case, seed)
@@ -202,7 +203,8 @@ def prepare(case, seed):
     if op == "group":
         if own:
             import expert_ffn_amd as efa
-            st["out"] = efa.group_slots(ids, case["N"])
+            N = case["N"]
+            st["out"] = efa.Grouping(*(torch.empty(k, dtype=torch.int32, device="cuda") for k in (N, N + 1, ids.numel(), N, 2)))
             st["ws"] = efa.group_workspace(case["n"], case["m"], case["N"])
         return st
     n, m, d, f = case["n"], case["m"], case["d"], case["d_ff"]
