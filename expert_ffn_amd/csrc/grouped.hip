@@ -60,39 +60,6 @@ void run_group(Group g, hipStream_t st) {
     hipLaunchKernelGGL(k_group_scatter, dim3(g.G > 1 ? g.G : 1 + quant), dim3(kGThreads), 0, st, g);
 }
 
-// Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf and O).
-struct Space {
-    size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
-};
-
-Space space_of(const moe_layer_desc* d, int32_t n) {
-    const size_t S = (size_t)n * d->m;
-    const bool fp8 = d->dtype == MOE_FP8;
-    Space p;
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-        const size_t a = at;
-        at += align_up(bytes);
-        return a;
-    };
-    p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
-    // gate/up's fp32 h (quantised before down begins), then O
-    p.hf = p.o = take(std::max(S * d->d_model * 2, fp8 ? S * d->d_ff * 4 : 0));
-    p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
-    p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
-    p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
-    p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : 0);
-    p.hist = take(group_ws(kGMaxChunks, d->N));  // (a longer pass may have fewer chunks)
-    p.count = take((size_t)d->N * 4);
-    p.offset = take((size_t)(d->N + 1) * 4);
-    p.sbe = take(S * 4);
-    p.row_of = take(S * 4);
-    p.distinct = take((size_t)d->N * 4);
-    p.u_err = take(8);
-    p.total = at;
-    return p;
-}
-
 // Square or thin tiles.  Thin ones take as long again with every 16 rows of an expert, square ones the
 // same from few rows on.  At 8 / 16 / 24 rows of every expert, thin against square, us:
 //     128 experts of 2048 x 768   gate/up bf16   141 / 150 / 205   148 / 134 / 136
@@ -129,6 +96,42 @@ bool square_gate_up(const moe_layer_desc* d, int n) {
 }
 bool square_down(const moe_layer_desc* d, int n) {
     return square(shape_of(d->N, d->m, n, d->d_model, d->d_ff), d->dtype == MOE_FP8, false);
+}
+
+// Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf and O).
+struct Space {
+    size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
+};
+
+Space space_of(const moe_layer_desc* d, int32_t n) {
+    const size_t S = (size_t)n * d->m;
+    const bool fp8 = d->dtype == MOE_FP8;
+    Space p;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t a = at;
+        at += align_up(bytes);
+        return a;
+    };
+    p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
+    // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert), bf16 from square ones
+    size_t o = S * d->d_model * 4;
+    if (square_down(d, n)) o = std::max(o / 2, (size_t)16 * d->N * d->d_model * 4);
+    // gate/up's fp32 h (quantised before down begins), then O
+    p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : 0));
+    p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
+    p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
+    p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
+    p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : 0);
+    p.hist = take(group_ws(kGMaxChunks, d->N));  // (a longer pass may have fewer chunks)
+    p.count = take((size_t)d->N * 4);
+    p.offset = take((size_t)(d->N + 1) * 4);
+    p.sbe = take(S * 4);
+    p.row_of = take(S * 4);
+    p.distinct = take((size_t)d->N * 4);
+    p.u_err = take(8);
+    p.total = at;
+    return p;
 }
 
 // What a pass's grouping leaves for the products, where they run by themselves: an empty queue for
@@ -224,7 +227,8 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     if (!u_err) a.row_of = row_of;  // (a pass's grouping has left them)
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
-    hipLaunchKernelGGL(k_combine, dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
+    hipLaunchKernelGGL(square_down(d, n) ? k_combine<false> : k_combine<true>,
+                       dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
                        reinterpret_cast<const char*>(o), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }

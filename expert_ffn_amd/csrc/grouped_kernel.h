@@ -50,7 +50,7 @@ struct Args {
     const uint8_t* s1;
     const int32_t* offset;
     const int32_t* slot;
-    char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order
+    char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order (square tiles bf16, thin ones fp32)
     int32_t* queue;       // square tiles: [8][kLine], tiles taken from each XCD's run, zero at the start
     uint8_t* outs;        // e4m3 gate/up: scale bytes of h
     int N, m, S, R, K;
@@ -627,9 +627,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
         else
             *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
                 u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
-    } else {
-        *reinterpret_cast<u32x2*>(a.out + ((int64_t)row * a.R + c) * 2) =
-            u32x2{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3])};
+    } else {  // float32: O is a partial sum of y
+        *reinterpret_cast<f32x4*>(a.out + ((int64_t)row * a.R + c) * 4) = v[0];
     }
 }
 
@@ -1269,10 +1268,16 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 // y_t = sum_j w_tj O_tj over the slots with a valid id, in increasing j, in fp32, rounded
 // to bf16 once.  A wave takes 512 columns of a token (eight a lane); the lanes look up the
 // token's slots together, so that the loads of O go out eight at a time: they are the time
-// (4096 tokens of 8 x 2048 in 25 us: 151 MB at 6 TB/s).  O is bf16: in fp32 the products would write
-// and this read 134 MB more each for those tokens, 45-50 us beside the 104 + 25 of 8-bit down.  That rounding of each
-// term is independent of y's own, so the two together are about sqrt(1 + sum w^2) of one.
+// (4096 tokens of 8 x 2048 in 25 us: 151 MB at 6 TB/s).
+//
+// O, a partial sum of y, is fp32 from thin tiles, which costs them nothing that shows (passes of one token
+// 26 us, of 32 tokens 91 us either way).  From square tiles it is bf16, as fp32 is 134 MB more each way for 4096 tokens
+// of 8 x 2048: 8-bit down of those 129 us, with fp32 170; the 8-bit pass of 8191 tokens 491, 589; bf16 down of
+// 2777 x 6 162, 181; the wide bf16 pass 1605, 1630.  Its rounding puts term j off by at most half a step,
+// 2^-8 |w_j O_j|, the sum by about 2^-9 sqrt(sum (w_j O_j)^2): about y's own rounding where the terms add up,
+// more than that, without a limit relative to y, where they cancel.
 // info (may be null): U, ids status, MOE_OK.
+template <bool F32>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
                                                 int m, int N, int d,
@@ -1299,26 +1304,36 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
             }
             uint64_t live = __ballot(row >= 0);
             while (live) {
-                u32x4 o[8];
+                u32x4 o[8][F32 ? 2 : 1];
                 float wt[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int l = live ? __ffsll((unsigned long long)live) - 1 : 64;
                     live &= live - 1;
-                    o[k] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (auto& p : o[k]) p = u32x4{0u, 0u, 0u, 0u};
                     wt[k] = 0.f;
                     if (l < 64) {
                         const int64_t r = __builtin_amdgcn_readlane(row, l);
                         wt[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(wj), l));
-                        if (in) o[k] = *reinterpret_cast<const u32x4*>(O + (r * d + c) * 2);
+                        const u32x4* at = reinterpret_cast<const u32x4*>(O + (r * d + c) * (F32 ? 4 : 2));
+                        if (in) o[k][0] = at[0];
+                        if constexpr (F32) {
+                            if (in) o[k][1] = at[1];
+                        }
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        s[2 * v] += wt[k] * bf16_lo(o[k][v]);
-                        s[2 * v + 1] += wt[k] * bf16_hi(o[k][v]);
+                        if constexpr (F32) {
+                            s[v] += wt[k] * __uint_as_float(o[k][0][v]);
+                            s[4 + v] += wt[k] * __uint_as_float(o[k][1][v]);
+                        } else {
+                            s[2 * v] += wt[k] * bf16_lo(o[k][0][v]);
+                            s[2 * v + 1] += wt[k] * bf16_hi(o[k][0][v]);
+                        }
                     }
                 }
             }

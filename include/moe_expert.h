@@ -312,10 +312,12 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  *   down      y_t = round( sum_j w_tj W_down[e_tj] h_row(t,j) ), j increasing; a token
  *             without a valid id gets zeros
  * y is bf16 (these passes feed the next layer), every sum is fp32; round is to bf16, or,
- * for h with 8-bit weights, the quantisation below.  W_down h is rounded to bf16 too before it
- * is weighted (the terms pass through memory); y's error is about that of two roundings.  On
- * more than a few rows an expert, 8-bit products go through a matrix instruction that
- * cuts each product to 2^-13 of the largest of its 8 neighbours along the contraction.
+ * for h with 8-bit weights, the quantisation below.  The two kinds of tiles that the products
+ * run on differ in their arithmetic.  Thin tiles (passes of few rows an expert) keep the terms
+ * W_down h in fp32, so that y is rounded once.  Square tiles (from 8 to 16 rows an expert on average,
+ * by type and size) hand them on in bf16: each term is off by up to 2^-8 |w_tj W_down h|, whatever is left of
+ * their sum.  8-bit products on square tiles go through a matrix instruction that
+ * cuts each product to 2^-13 of the largest of its 8 neighbours along the contraction; thin tiles do not cut.
  * Results are deterministic.
  *
  * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=

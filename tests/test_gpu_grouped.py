@@ -727,3 +727,66 @@ def test_the_same_bits_every_time(typ, n):
     first = efa.expert_grouped(case.layer, x, ids, w)
     for _ in range(8):
         assert torch.equal(efa.expert_grouped(case.layer, x, ids, w), first)
+
+
+# --- the terms of a token's sum ---------------------------------------------------------
+
+def _exact_sum(case, hv, ids, w, g, eps, rounding):
+    """y and the bound of its error: sums of K products in fp32 (``eps`` of their
+    magnitudes), each term rounded to ``rounding`` of itself on its way, m weighted
+    additions in fp32 (2^-22 a term), and one rounding to bf16."""
+    at, slot = g.offset.tolist(), g.slot_by_expert.long()
+    y = torch.zeros(ids.shape[0], case.d, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(y)
+    for e in range(case.N):
+        s = slot[at[e]:at[e + 1]]
+        h = hv[at[e]:at[e + 1]]
+        o, mag = h @ case.W[2][e].T, h.abs() @ case.W[2][e].abs().T
+        wt = w.reshape(-1)[s].double()[:, None]
+        y.index_add_(0, s // case.m, wt * o)
+        tol.index_add_(0, s // case.m, wt.abs() * (eps * mag + (rounding + case.m * 2.0 ** -22) * o.abs()))
+    return y, tol + 2.0 ** -8 * (y.abs() + tol)
+
+
+def _down_case(N, m, d, f, typ, layout, seed):
+    """A layer whose experts differ in the sign of one column of W_down: two of them with
+    weights 1 and -1 leave 2 w_c h_c of sums that are about sqrt(f) / 2 times as large.
+    (A sign leaves a block's maximum, and so every code's magnitude, as it is.)"""
+    case = Case(N, m, d, f, typ, layout, seed=seed)
+    W = [(_randn(seed + i, *s) * 0.05).to(BF).repeat(N, 1, 1).cuda() for i, s in enumerate(((f, d), (f, d), (d, f)))]
+    W[2][1::2, :, f // 3] *= -1
+    layer = efa.Layer(*W, m=m)
+    if case.fp8:
+        layer = layer.fp8_copy()
+        case.W = [_weight_values(*p) for p in (layer.gate, layer.up, layer.down)]
+    else:
+        case.W = [v.double() for v in W]
+    case.layer = layer.tiled_copy() if layout == "tiled" else layer
+    return case
+
+
+def _cancelling(case, n, seed):
+    """Every token on neighbouring experts with weights 1, -1, 1, ..., one h for all its slots."""
+    first = torch.randint(0, case.N, (n, 1), generator=torch.Generator().manual_seed(seed))
+    ids = ((first + torch.arange(case.m)) % case.N).to(torch.int32).cuda().contiguous()
+    w = (1.0 - 2.0 * (torch.arange(case.m) % 2)).repeat(n, 1).cuda().contiguous()
+    g = efa.group_slots(ids, case.N)
+    h = _randn(seed + 1, n, case.f).to(BF).cuda()[g.slot_by_expert.long() // case.m].contiguous()
+    hq = efa.quant_rows(h) if case.fp8 else h
+    return ids, w, g, hq, _row_values(hq) if case.fp8 else h.double()
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("layout", ["plain", "tiled"])
+@pytest.mark.parametrize("N,m,n", [(2, 2, 1), (2, 2, 15), (8, 4, 9), (128, 8, 1), (128, 8, 32)])
+def test_terms_that_cancel(N, m, n, layout, typ):
+    """Passes of few rows an expert hold the terms of a token's sum in fp32: y is rounded
+    once, whatever the terms are next to it."""
+    say("cancel", N, m, n, layout, typ)
+    case = _down_case(N, m, 512, 768, typ, layout, seed=n)
+    ids, w, g, h, hv = _cancelling(case, n, 80 + n)
+    y = efa.grouped_down(case.layer, h, ids, w, g)
+    want, tol = _exact_sum(case, hv, ids, w, g, 768 * 2.0 ** -23, 0.0)
+    _within(y, want, tol, "y")
+    # one rounding: at most 2^-8 of the norm, on average less than half of that
+    assert (y.double() - want).norm() <= 2.0 ** -8 * want.norm()

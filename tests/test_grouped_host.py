@@ -159,3 +159,12 @@ def test_a_longer_pass_needs_no_less(dtype):
     ns = [1, 2, 8191, 8192, 8193, 65535, 65536, 65537, 70000, 131072, 131073, 262144, 262145, 1 << 22]
     sizes = [_abi.lib().moe_grouped_workspace_bytes(ctypes.byref(d), n) for n in ns]
     assert all(a <= b for a, b in zip(sizes, sizes[1:])), sizes
+
+
+@pytest.mark.parametrize("dtype", [_abi.MOE_BF16, _abi.MOE_FP8])
+@pytest.mark.parametrize("N,m,d,f", [(2, 2, 512, 768), (64, 4, 1024, 640), (128, 8, 2048, 768), (8, 2, 4096, 14336)])
+def test_a_longer_pass_needs_no_less_where_tiles_change(N, m, d, f, dtype):
+    """Also where a longer pass takes other tiles, which hold their terms in other types."""
+    desc = _desc(N=N, m=m, d_model=d, d_ff=f, dtype=dtype)
+    sizes = [_abi.lib().moe_grouped_workspace_bytes(ctypes.byref(desc), n) for n in range(1, 24 * N // m + 24)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
