@@ -15,5 +15,5 @@ from .ops import (  # noqa: F401
 )
 from .grouped import (  # noqa: F401
     Fp8Layer, Quantized, dequant_rows, expert_grouped, group_slots, group_workspace, grouped_down, grouped_gate_up,
-    quant_rows, quant_weights,
+    grouped_square, quant_rows, quant_weights,
 )

@@ -34,7 +34,7 @@ EXPORTS = ("moe_route_group", "moe_workspace_bytes", "moe_expert_perslot", "moe_
            "moe_group_workspace_bytes", "moe_group_slots", "moe_quant_rows", "moe_dequant_rows",
            "moe_quant_weights", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
            "moe_grouped_gate_up_fp8", "moe_grouped_down", "moe_grouped_down_fp8", "moe_expert_grouped",
-           "moe_expert_grouped_fp8")
+           "moe_expert_grouped_fp8", "moe_grouped_square")
 
 
 class MoeError(RuntimeError):
@@ -156,6 +156,7 @@ def lib():
             L.moe_quant_weights.argtypes = [vp, i32, i32, i32, vp, vp, vp]
             L.moe_grouped_workspace_bytes.argtypes = [pdesc, i32]
             L.moe_grouped_workspace_bytes.restype = sz
+            L.moe_grouped_square.argtypes = [pdesc, i32, i32]
             L.moe_grouped_gate_up.argtypes = [pdesc, pw, vp, i32, vp, vp, vp, vp, sz, vp]
             L.moe_grouped_gate_up_fp8.argtypes = [pdesc, pw8, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
             L.moe_grouped_down.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
@@ -164,7 +165,7 @@ def lib():
             L.moe_expert_grouped_fp8.argtypes = [pdesc, pw8, vp, vp, vp, i32, vp, vp, vp, sz, vp]
             for f in (L.moe_group_slots, L.moe_quant_rows, L.moe_dequant_rows, L.moe_quant_weights,
                       L.moe_grouped_gate_up, L.moe_grouped_gate_up_fp8, L.moe_grouped_down, L.moe_grouped_down_fp8,
-                      L.moe_expert_grouped, L.moe_expert_grouped_fp8):
+                      L.moe_expert_grouped, L.moe_expert_grouped_fp8, L.moe_grouped_square):
                 f.restype = ctypes.c_int
             _LIB = L
     return _LIB

@@ -316,6 +316,14 @@ size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
     return space_of(desc, n).total;
 }
 
+int moe_grouped_square(const moe_layer_desc* desc, int32_t n, int32_t mat) {
+    if (!desc || (mat != MOE_MAT_GATE_UP && mat != MOE_MAT_DOWN)) return MOE_E_INVAL;
+    if (desc->dtype != MOE_BF16 && desc->dtype != MOE_FP8) return MOE_E_DTYPE;
+    const int rc = check_desc(desc, n, desc->dtype);
+    if (rc != MOE_OK) return rc;
+    return mat == MOE_MAT_GATE_UP ? square_gate_up(desc, n) : square_down(desc, n);
+}
+
 int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, int32_t n,
                         const int32_t* offset, const int32_t* slot_by_expert, void* h, void* ws, size_t ws_bytes,
                         void* hip_stream) {

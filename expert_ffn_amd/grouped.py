@@ -248,6 +248,16 @@ def grouped_workspace(layer, n):
     return _ws(None, layer.desc(), int(n), dev, None)
 
 
+def grouped_square(layer, n, mat):
+    """Whether passes of n tokens take square tiles for ``mat`` (MOE_MAT_GATE_UP or
+    MOE_MAT_DOWN); thin ones otherwise (``moe_grouped_square``, host only)."""
+    _kind(layer)
+    v = lib().moe_grouped_square(ctypes.byref(layer.desc()), int(n), int(mat))
+    if v < 0:
+        raise _abi.MoeError("moe_grouped_square", v)
+    return bool(v)
+
+
 def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
     """h [n*m][d_ff] in row order (``moe_grouped_gate_up``): bf16 from bf16 x [n][d], or
     with 8-bit weights ``Quantized`` from ``Quantized`` x (``quant_rows``).  Rows from

@@ -315,7 +315,7 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  * for h with 8-bit weights, the quantisation below.  The two kinds of tiles that the products
  * run on differ in their arithmetic.  Thin tiles (passes of few rows an expert) keep the terms
  * W_down h in fp32, so that y is rounded once.  Square tiles (from 8 to 16 rows an expert on average,
- * by type and size) hand them on in bf16: each term is off by up to 2^-8 |w_tj W_down h|, whatever is left of
+ * by type and size: moe_grouped_square) hand them on in bf16: each term is off by up to 2^-8 |w_tj W_down h|, whatever is left of
  * their sum.  8-bit products on square tiles go through a matrix instruction that
  * cuts each product to 2^-13 of the largest of its 8 neighbours along the contraction; thin tiles do not cut.
  * Results are deterministic.
@@ -379,6 +379,10 @@ typedef struct {
  * with n, so a workspace for n serves fewer tokens too.  256-byte aligned; no zero-fill
  * needed, nothing kept between calls; calls that share one must not overlap in time. */
 size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n);
+
+/* Host only: 1 if a pass of n tokens takes square tiles for its gate/up (mat MOE_MAT_GATE_UP) or
+ * down (MOE_MAT_DOWN) product, 0 if thin ones; MOE_E_INVAL / MOE_E_DTYPE for invalid arguments. */
+int moe_grouped_square(const moe_layer_desc* desc, int32_t n, int32_t mat);
 
 /*
  * The two products by themselves.  offset and slot_by_expert come from moe_group_slots

@@ -168,3 +168,29 @@ def test_a_longer_pass_needs_no_less_where_tiles_change(N, m, d, f, dtype):
     desc = _desc(N=N, m=m, d_model=d, d_ff=f, dtype=dtype)
     sizes = [_abi.lib().moe_grouped_workspace_bytes(ctypes.byref(desc), n) for n in range(1, 24 * N // m + 24)]
     assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_which_tiles():
+    """moe_grouped_square: square tiles from 8, 12 or 16 rows an expert, by type and tiles, for
+    contractions of more than 384 bytes and matrices of 31 bits."""
+    L = _abi.lib()
+
+    def square(n, mat, **kw):
+        return L.moe_grouped_square(ctypes.byref(_desc(**kw)), n, mat)
+    G, D = _abi.MOE_MAT_GATE_UP, _abi.MOE_MAT_DOWN
+    few = dict(N=8, m=2, d_model=512, d_ff=512)        # fewer tiles than two a compute unit
+    many = dict(N=1000, m=2, d_model=512, d_ff=528)
+    for dtype, least in ((_abi.MOE_BF16, 8), (_abi.MOE_FP8, 12)):
+        for mat in (G, D):
+            assert square(63, mat, dtype=dtype, **few) == 0 and square(64, mat, dtype=dtype, **few) == 1
+            n = least * 1000 // 2
+            assert square(n - 1, mat, dtype=dtype, **many) == 0 and square(n, mat, dtype=dtype, **many) == 1
+    for dtype, es in ((_abi.MOE_BF16, 2), (_abi.MOE_FP8, 1)):
+        short = dict(N=8, m=2, dtype=dtype, d_model=384 // es, d_ff=400 // es)
+        assert square(4000, G, **short) == 0 and square(4000, D, **short) == 1
+    assert square(4000, G, N=1, m=1, dtype=_abi.MOE_BF16, d_model=16384, d_ff=65408) == 0
+    for bad in (dict(N=0), dict(m=9), dict(n_shared=1), dict(flags=8)):
+        assert square(4, G, **{"dtype": _abi.MOE_BF16, **bad}) == INVAL
+    assert square(0, G, dtype=_abi.MOE_BF16) == INVAL and square(4, 2, dtype=_abi.MOE_BF16) == INVAL
+    assert square(4, G, dtype=_abi.MOE_F32) == DTYPE and square(4, G, dtype=_abi.MOE_BF16, d_ff=100) == DTYPE
+    assert L.moe_grouped_square(None, 4, G) == INVAL
