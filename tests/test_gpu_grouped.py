@@ -832,3 +832,42 @@ def test_products_of_one_group_of_eight(small, at, n, square, layout):
     y = efa.grouped_down(layer, h, ids, torch.ones(n, 1, device="cuda"), efa.group_slots(ids, 1))
     lost = square and small < 8.0 and max(at) < 8
     assert (y.double() == (0.0 if lost else small)).all(), y.unique()
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,square", [(3, False), (15, False), (200, True)])
+@pytest.mark.parametrize("tiny", ["weights", "inputs"])
+def test_the_least_values(tiny, n, square, typ):
+    """Values down to bf16's least, 2^-133 (scale byte 0 where they are codes), next to values
+    of about 2^120, so that the sums are ordinary numbers: none of their bits are lost."""
+    say("least values", tiny, n, typ)
+    N, d, f = 1, 512, 576
+    ints = [torch.randint(-255, 256, s, generator=torch.Generator().manual_seed(i))
+            for i, s in enumerate(((N, f, d), (N, f, d), (N, d, f), (n, d), (n, f)))]
+    small = [(v.double() * 2.0 ** -133).float().to(BF) for v in ints]
+    large = [(_randn(20 + i, *v.shape) * 2.0 ** 120).to(BF) for i, v in enumerate(ints)]
+    W, (x, h) = (small[:3], large[3:]) if tiny == "weights" else (large[:3], small[3:])
+    assert all(float(v.float().abs().max()) <= 2.0 ** -125 for v in small)
+    case = Case(N, 1, d, f, typ)
+    layer = efa.Layer(*(v.cuda() for v in W), m=1)
+    if case.fp8:
+        layer = layer.fp8_copy()
+        case.W = [_weight_values(*p) for p in (layer.gate, layer.up, layer.down)]
+        q = efa.quant_rows(small[3].cuda()).scale if tiny == "inputs" else layer.gate[1]
+        assert (q == 0).all()
+    else:
+        case.W = [v.double().cuda() for v in W]
+    case.layer = layer
+    for mat in (_abi.MOE_MAT_GATE_UP, _abi.MOE_MAT_DOWN):
+        assert efa.grouped_square(layer, n, mat) is square
+    x, h = x.cuda(), h.cuda()
+    ids = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    g, got = case.gate_up(x, ids)
+    _check_h(case, got, x, g, "h")
+    w = torch.ones(n, 1, device="cuda")
+    hq = efa.quant_rows(h) if case.fp8 else h
+    y = efa.grouped_down(layer, hq, ids, w, g)
+    want, tol = _exact_sum(case, _row_values(hq) if case.fp8 else h.double(), ids, w, g, case.eps(f),
+                           2.0 ** -8 if square else 0.0)
+    assert want.abs().median() > 2.0 ** -10
+    _within(y, want, tol, "y")
