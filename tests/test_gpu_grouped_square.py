@@ -1,5 +1,6 @@
 """The grouped calls on square tiles, whose rule every test here asks for: what the tests of
-``test_gpu_grouped`` with narrow layers ask of thin tiles, and the most experts.  Tolerances are those that ``test_gpu_grouped`` derives."""
+``test_gpu_grouped`` with narrow layers ask of thin tiles, the most experts, and the shapes
+of the timed layers.  Tolerances are those that ``test_gpu_grouped`` derives."""
 import pytest
 import torch
 
@@ -8,7 +9,7 @@ from expert_ffn_amd import _abi
 
 from .gpu_cases import say
 from .test_gpu_grouped import (
-    BF, H8, Case, _check_h, _check_pass, _ids, _pow2, _randn, _row_values, _run_parts, _within,
+    BF, H8, Case, _check_h, _check_pass, _gpu_layer, _ids, _pow2, _randn, _row_values, _run_parts, _weight_values, _within,
 )
 
 pytestmark = pytest.mark.gpu
@@ -273,3 +274,24 @@ def test_side_streams(typ):
     torch.cuda.synchronize()
     for ys in got:
         assert all(torch.equal(y, v) for y, v in zip(ys, want))
+
+
+class _GpuCase(Case):
+    """A Case with weights made on the GPU."""
+
+    def __init__(self, N, m, d, f, typ, layout):
+        self.N, self.m, self.d, self.f, self.fp8 = N, m, d, f, typ == "fp8"
+        plain, self.layer = _gpu_layer(N, m, d, f, typ, layout, 1)
+        self.W = ([_weight_values(*p) for p in (plain.gate, plain.up, plain.down)] if self.fp8 else
+                  [v.double() for v in (plain.w_gate, plain.w_up, plain.w_down)])
+
+
+@pytest.mark.parametrize("typ", ["bf16", "fp8"])
+@pytest.mark.parametrize("N,m,d,f", [(128, 8, 2048, 768), (64, 6, 2048, 1408), (8, 2, 4096, 14336)])
+def test_layers_of_the_timed_shapes(N, m, d, f, typ):
+    say("shapes", N, m, d, f, typ)
+    case = _GpuCase(N, m, d, f, typ, "tiled")
+    for n, square in ((1, False), (5, False), (513, True)):
+        assert _tiles(case.layer, n) == (square, square)
+        ids, w = _ids(3, n, m, N, zipf=1.1, pad=n // 10)
+        _check_pass(case, _randn(4, n, d).to(BF).cuda(), ids, w, "n = %d" % n)
