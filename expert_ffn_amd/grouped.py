@@ -26,6 +26,12 @@ def _blocks(v):
     return -(-v // 128)
 
 
+def _int(v):
+    """A size as an argument of a call: one that C's int does not hold goes as the largest that
+    it does, which every call refuses."""
+    return v if -1 << 31 <= v < 1 << 31 else (1 << 31) - 1
+
+
 def _guard(dev):
     return _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
@@ -59,7 +65,7 @@ def _check(name, t, dtype, shape, dev):
 def _ws(ws, desc, n, dev, stream):
     """Workspace of a grouped call (its size is checked by the call itself)."""
     if ws is None:
-        nb = lib().moe_grouped_workspace_bytes(ctypes.byref(desc), n)
+        nb = lib().moe_grouped_workspace_bytes(ctypes.byref(desc), _int(n))
         if nb == 0:
             raise _abi.MoeError("moe_grouped_workspace_bytes", _abi.MOE_E_INVAL)
         return _empty(nb, _U8, dev, stream)
@@ -149,8 +155,8 @@ def quant_weights(w, stream=None):
     q = _empty((N, R, K), _E4M3, dev, stream)
     s = _empty((N, _blocks(R), _blocks(K)), _U8, dev, stream)
     with _guard(dev):
-        check("moe_quant_weights", lib().moe_quant_weights(w.data_ptr(), N, R, K, q.data_ptr(), s.data_ptr(),
-                                                           _on(dev, stream)))
+        check("moe_quant_weights", lib().moe_quant_weights(w.data_ptr(), _int(N), _int(R), _int(K), q.data_ptr(),
+                                                           s.data_ptr(), _on(dev, stream)))
     return q, s
 
 
@@ -175,7 +181,7 @@ def quant_rows(x, out=None, stream=None):
         out = Quantized(_empty((rows, K), _E4M3, dev, stream), _empty((rows, _blocks(K)), _U8, dev, stream))
     q, s = _check_quantized("out", out, rows, K, dev)
     with _guard(dev):
-        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, K, q, s, _on(dev, stream)))
+        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, _int(K), q, s, _on(dev, stream)))
     return out
 
 
@@ -191,13 +197,13 @@ def dequant_rows(v, out=None, stream=None):
         out = _empty((rows, K), _BF16, dev, stream)
     x = _check("out", out, _BF16, (rows, K), dev)
     with _guard(dev):
-        check("moe_dequant_rows", lib().moe_dequant_rows(q, s, rows, K, x, _on(dev, stream)))
+        check("moe_dequant_rows", lib().moe_dequant_rows(q, s, rows, _int(K), x, _on(dev, stream)))
     return out
 
 
 def group_workspace(n, m, N, device="cuda"):
     """Workspace of ``group_slots`` for n tokens of m slots and N experts."""
-    nb = lib().moe_group_workspace_bytes(int(n), int(m), int(N))
+    nb = lib().moe_group_workspace_bytes(_int(int(n)), _int(int(m)), _int(int(N)))
     if nb == 0:
         raise _abi.MoeError("moe_group_workspace_bytes", _abi.MOE_E_INVAL)
     return torch.empty(nb, dtype=torch.uint8, device=device)
@@ -212,7 +218,7 @@ def group_slots(ids, N, out=None, ws=None, stream=None):
     n, m = ids.shape
     N, dev = int(N), ids.device
     if ws is None:
-        nb = lib().moe_group_workspace_bytes(n, m, N)
+        nb = lib().moe_group_workspace_bytes(_int(n), _int(m), _int(N))
         if nb == 0:
             raise _abi.MoeError("moe_group_workspace_bytes", _abi.MOE_E_INVAL)
         ws = _empty(nb, _U8, dev, stream)
@@ -221,8 +227,8 @@ def group_slots(ids, N, out=None, ws=None, stream=None):
     ptrs = _check_grouping(out, n, m, N, dev)
     wsp = _check("ws", ws, _U8, ws.shape, dev)
     with _guard(dev):
-        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), n, m, N, *ptrs, wsp, ws.numel(),
-                                                       _on(dev, stream)))
+        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), _int(n), _int(m), _int(N), *ptrs, wsp,
+                                                       ws.numel(), _on(dev, stream)))
     return out
 
 
@@ -252,7 +258,7 @@ def grouped_square(layer, n, mat):
     """Whether passes of n tokens take square tiles for ``mat`` (MOE_MAT_GATE_UP or
     MOE_MAT_DOWN); thin ones otherwise (``moe_grouped_square``, host only)."""
     _kind(layer)
-    v = lib().moe_grouped_square(ctypes.byref(layer.desc()), int(n), int(mat))
+    v = lib().moe_grouped_square(ctypes.byref(layer.desc()), _int(int(n)), _int(int(mat)))
     if v < 0:
         raise _abi.MoeError("moe_grouped_square", v)
     return bool(v)
@@ -283,8 +289,8 @@ def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
         name, call = "moe_grouped_gate_up", L.moe_grouped_gate_up
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *xs, n, offset, slots, *hs, ws.data_ptr(),
-                         ws.numel(), _on(dev, stream)))
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *xs, _int(n), offset, slots, *hs,
+                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return out
 
 
@@ -313,7 +319,7 @@ def grouped_down(layer, h, ids, w, grouping, y=None, ws=None, accumulate=False, 
         name, call = "moe_grouped_down", L.moe_grouped_down
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *hs, idp, wp, n, offset, slots, yp,
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *hs, idp, wp, _int(n), offset, slots, yp,
                          ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return y
 
@@ -333,6 +339,6 @@ def expert_grouped(layer, x, ids, w, y=None, ws=None, info=None, accumulate=Fals
                   ("moe_expert_grouped", L.moe_expert_grouped))
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), xp, idp, wp, n, yp, infop, ws.data_ptr(),
-                         ws.numel(), _on(dev, stream)))
+        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), xp, idp, wp, _int(n), yp, infop,
+                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return y

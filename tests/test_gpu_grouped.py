@@ -871,3 +871,18 @@ def test_the_least_values(tiny, n, square, typ):
                            2.0 ** -8 if square else 0.0)
     assert want.abs().median() > 2.0 ** -10
     _within(y, want, tol, "y")
+
+
+def test_more_rows_than_an_int_holds():
+    """2^32 + 1 tokens, or 2^32 + 16 columns, are refused, not taken for one and sixteen."""
+    ids = torch.empty((1 << 32) + 1, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(_abi.MoeError):
+        efa.group_slots(ids, 8)
+    del ids
+    x = torch.empty(1, (1 << 32) + 16, dtype=BF, device="cuda")
+    with pytest.raises(_abi.MoeError):
+        efa.quant_rows(x)
+    with pytest.raises(_abi.MoeError):
+        efa.quant_weights(x.view(1, 1, -1).expand(1, 1, -1))
+    del x
+    torch.cuda.empty_cache()

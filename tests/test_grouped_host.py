@@ -194,3 +194,22 @@ def test_which_tiles():
     assert square(0, G, dtype=_abi.MOE_BF16) == INVAL and square(4, 2, dtype=_abi.MOE_BF16) == INVAL
     assert square(4, G, dtype=_abi.MOE_F32) == DTYPE and square(4, G, dtype=_abi.MOE_BF16, d_ff=100) == DTYPE
     assert L.moe_grouped_square(None, 4, G) == INVAL
+
+
+def test_sizes_beyond_an_int_are_refused():
+    """A size that C's int does not hold is not taken for what its lowest bits say."""
+    for n, m, N in (((1 << 32) + 1, 1, 8), (1, (1 << 32) + 1, 8), (1, 1, (1 << 32) + 8), (1 - (1 << 32), 1, 8)):
+        with pytest.raises(_abi.MoeError):
+            efa.group_workspace(n, m, N, device="cpu")
+
+    class Stub(efa.Fp8Layer):  # a layer that needs no memory
+        def __init__(self):
+            self.N, self.m, self.d, self.d_ff, self.tiled = 8, 2, 64, 128, False
+
+        device = torch.device("cpu")
+    for n in ((1 << 32) + 1, 1 - (1 << 32)):
+        with pytest.raises(_abi.MoeError):
+            Stub().grouped_workspace(n)
+        with pytest.raises(_abi.MoeError):
+            efa.grouped_square(Stub(), n, _abi.MOE_MAT_DOWN)
+    assert Stub().grouped_workspace(1).numel() > 0 and efa.grouped_square(Stub(), 1, _abi.MOE_MAT_DOWN) is False
