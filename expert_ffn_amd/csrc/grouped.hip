@@ -98,9 +98,9 @@ bool square_down(const moe_layer_desc* d, int n) {
     return square(shape_of(d->N, d->m, n, d->d_model, d->d_ff), d->dtype == MOE_FP8, false);
 }
 
-// Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf and O).
+// Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf, O and its bytes).
 struct Space {
-    size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, total;
+    size_t queue, hist, count, offset, sbe, row_of, distinct, u_err, xq, xs, h, hs, hf, o, os, total;
 };
 
 Space space_of(const moe_layer_desc* d, int32_t n) {
@@ -114,11 +114,12 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
         return a;
     };
     p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
-    // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert), bf16 from square ones
+    // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert), fp16 from square ones
     size_t o = S * d->d_model * 4;
     if (square_down(d, n)) o = std::max(o / 2, (size_t)16 * d->N * d->d_model * 4);
     // gate/up's fp32 h (quantised before down begins), then O
     p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : 0));
+    p.os = take(S * ((d->d_model + 63) / 64));
     p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
     p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
     p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
@@ -214,7 +215,7 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
 template <bool FP8>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
               const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, int32_t* row_of, void* y,
-              void* o, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
+              void* o, uint8_t* os, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
     Args a = shape_of(d->N, d->m, n, d->d_model, d->d_ff);
     a.x = reinterpret_cast<const char*>(h);
     a.xs = hs;
@@ -223,13 +224,14 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.offset = offset;
     a.slot = sbe;
     a.out = reinterpret_cast<char*>(o);
+    a.outs = os;
     a.queue = queue;
     if (!u_err) a.row_of = row_of;  // (a pass's grouping has left them)
     launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
     hipLaunchKernelGGL(square_down(d, n) ? k_combine<false> : k_combine<true>,
                        dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
-                       reinterpret_cast<const char*>(o), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       reinterpret_cast<const char*>(o), os, row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 
@@ -266,7 +268,7 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
                      b + p.h, u8(p.hs), b + p.hf, i32(p.queue), st);
     run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y, b + p.o,
-                  i32(p.queue) + kQueue, i32(p.u_err), info, st);
+                  u8(p.os), i32(p.queue) + kQueue, i32(p.u_err), info, st);
     return launched();
 }
 
@@ -379,7 +381,8 @@ int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weight
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
     before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
     run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
-                    slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
+                    slot_by_expert, row_of, y, b + p.o, reinterpret_cast<uint8_t*>(b + p.os), queue, nullptr, nullptr,
+                    stream_of(hip_stream));
     return launched();
 }
 
@@ -400,7 +403,8 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
     before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
     run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
-                   slot_by_expert, row_of, y, b + p.o, queue, nullptr, nullptr, stream_of(hip_stream));
+                   slot_by_expert, row_of, y, b + p.o, reinterpret_cast<uint8_t*>(b + p.os), queue, nullptr, nullptr,
+                   stream_of(hip_stream));
     return launched();
 }
 

@@ -31,6 +31,7 @@ namespace moe_g {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
@@ -50,9 +51,9 @@ struct Args {
     const uint8_t* s1;
     const int32_t* offset;
     const int32_t* slot;
-    char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order (square tiles bf16, thin ones fp32)
+    char* out;            // gate/up: h [S][R]; down: O [S][R], rows in group order (thin tiles fp32, square ones fp16)
     int32_t* queue;       // square tiles: [8][kLine], tiles taken from each XCD's run, zero at the start
-    uint8_t* outs;        // e4m3 gate/up: scale bytes of h
+    uint8_t* outs;        // e4m3 gate/up: scale bytes of h; square down tiles: those of O [S][ceil(R/64)]
     int N, m, S, R, K;
     int tile0;            // thin tiles: the launch's first row tile
     int32_t* row_of;      // thin down tiles: null, or the row of each slot, to be written
@@ -91,6 +92,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // to nearest
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {  // to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2_t));
+}
+__device__ __forceinline__ f32x2 f16_values(uint32_t v) {
+    return __builtin_convertvector(__builtin_bit_cast(f16x2_t, v), f32x2);
+}
 
 // --- block quantisation ------------------------------------------------------------
 // k = the smallest integer >= -127 with amax <= 448 * 2^k: 448 = 1.75 * 2^8, so for
@@ -703,6 +711,18 @@ __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// O of square tiles: blocks of 64 columns of a row as fp16 times a power of two, which puts the block's
+// largest into [2^14, 2^15).  `byte` is its exponent's byte in fp32, 14 at least so that 2^127 scales it.
+__device__ __forceinline__ int term_byte(uint32_t largest) { return max((int)(largest >> 23), 14); }
+
+// The largest of the four lanes l % 16 + 16 k.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    const u32x2 a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    const u32x2 b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max(b[0], b[1]);
+}
+
 struct Place {
     int e, r0, rows, ct;  // rows 0: no tile
 };
@@ -980,7 +1000,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     if (wm) block_barrier();
 
     // a wave's stores of a tile: the same number whatever its rows, those of no row are dropped by their bounds
-    constexpr auto stores_of = [](int nb) { return GU ? (FP8 ? nb / 2 + 1 : nb) : 2 * nb; };
+    constexpr auto stores_of = [](int nb) { return GU ? (FP8 ? nb / 2 + 1 : nb) : 2 * nb + (nb + 3) / 4; };
     int par = 0;      // the stage of the unit at hand
     int before = 0;   // row blocks of a wave in the tile before, whose stores may still be on their way
     auto wait_past = [&](auto n, int nb) {
@@ -1215,22 +1235,54 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             }
         } else {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
-            const int c0 = p.ct * TC + wn * 64;
+            const int c0 = p.ct * TC + wn * 64;  // this wave's 64 columns, a block of O
+            int byte[NB];
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
+                float v[4][4];  // read once from the accumulators
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[j][k] = acc[i][j][k];
+                        asm volatile("" : "+v"(v[j][k]));
+                        m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
+                    }
+                if (__any(m >= 0x7f800000u)) {  // rare: what is not finite takes no part
+                    m = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(v[j][k])));
+                }
+                byte[i] = term_byte(quad_max(m));
+                const float inv = __uint_as_float((uint32_t)(268 - byte[i]) << 23);  // 2^(141 - byte)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f32x4 o = acc[i][j];
+                    const float* o = v[j];
                     *reinterpret_cast<u32x2*>(turn + er * 144 + j * 32 + 8 * eq) =
-                        u32x2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+                        u32x2{f16_pair(o[0] * inv, o[1] * inv), f16_pair(o[2] * inv, o[3] * inv)};
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int r = k * 8 + (el >> 3);
-                    const u32x4 v = *reinterpret_cast<const u32x4*>(turn + r * 144 + (el & 7) * 16);
+                    const u32x4 row = *reinterpret_cast<const u32x4*>(turn + r * 144 + (el & 7) * 16);
                     const int rr = (i * 2 + wm) * 16 + r, c = c0 + (el & 7) * 8;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(row, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
                 }
+            }
+            // the bytes of four row blocks at a time, a lane a row
+            const int OB = (a.R + 63) / 64, ob = p.ct * (TC / 64) + wn;
+            const auto rso = rsrc(arg()->outs + (int64_t)p.r0 * OB, (uint32_t)p.rows * OB);
+#pragma unroll
+            for (int i = 0; i < NB; i += 4) {
+                int v = byte[i];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) v = i + k < NB && eq == k ? byte[min(i + k, NB - 1)] : v;
+                const int rr = ((i + eq) * 2 + wm) * 16 + er;
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, rso, i + eq < NB && ob < OB ? (uint32_t)rr * OB + ob : kOOB,
+                                                     0, 0);
             }
         }
         before = NB;
@@ -1271,23 +1323,29 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 // (4096 tokens of 8 x 2048 in 25 us: 151 MB at 6 TB/s).
 //
 // O, a partial sum of y, is fp32 from thin tiles, which costs them nothing that shows (passes of one token
-// 26 us, of 32 tokens 91 us either way).  From square tiles it is bf16, as fp32 is 134 MB more each way for 4096 tokens
-// of 8 x 2048: 8-bit down of those 129 us, with fp32 170; the 8-bit pass of 8191 tokens 491, 589; bf16 down of
-// 2777 x 6 162, 181; the wide bf16 pass 1605, 1630.  Its rounding puts term j off by at most half a step,
-// 2^-8 |w_j O_j|, the sum by about 2^-9 sqrt(sum (w_j O_j)^2): about y's own rounding where the terms add up,
-// more than that, without a limit relative to y, where they cancel.
+// 26 us, of 32 tokens 91 us either way).  From square tiles fp32 would be 134 MB more each way for 4096 tokens of
+// 8 x 2048, so there it is fp16 with a power of two for each 64 columns of a row (two bytes and 1/64 an element):
+// 11 bits, three more than bf16, each term off by at most 2^-11 |w_j O_j| (half a step; and 2^-39 of its block's largest).
+//                                            bf16   this   fp32
+//     8-bit down of 4096 x 8 tokens, us        129    142    168
+//     8-bit pass of 8191 x 8                   486    502    581
+//     bf16 down of 2777 x 6                    159    165    180
+//     wide bf16 pass of 2048 x 2              1602   1610   1625
+//     error of y (norm): bf16 down          0.0023 0.0017 0.0017
+// where the rounding of y itself is 0.0017.  What is not finite is itself in fp16 and takes no part in a
+// block's largest.
 // info (may be null): U, ids status, MOE_OK.
 template <bool F32>
-__global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const int32_t* __restrict__ row_of,
+__global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const uint8_t* __restrict__ os, const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
                                                 int m, int N, int d,
                                                 int accumulate, char* __restrict__ y, const int32_t* __restrict__ u_err,
                                                 int32_t* __restrict__ info) {
-    const int lane = threadIdx.x & 63, CW = (d + 511) / 512, last = (int)(n * m) - 1;
+    const int lane = threadIdx.x & 63, CW = (d + 511) / 512, OB = (d + 63) / 64, last = (int)(n * m) - 1;
     if (info && blockIdx.x == 0 && threadIdx.x < 3) info[threadIdx.x] = threadIdx.x < 2 ? u_err[threadIdx.x] : MOE_OK;
     for (int64_t i = (int64_t)blockIdx.x * 4 + uni(threadIdx.x >> 6); i < n * CW; i += (int64_t)gridDim.x * 4) {
         const int64_t t = i / CW;
-        const int c = (int)(i - t * CW) * 512 + lane * 8;
+        const int c0 = (int)(i - t * CW) * 512, c = c0 + lane * 8;
         const bool in = c < d;
         float s[8];
 #pragma unroll
@@ -1306,6 +1364,7 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
             while (live) {
                 u32x4 o[8][F32 ? 2 : 1];
                 float wt[8];
+                int rows8 = 0;  // of lane 8 k + b: row k of the eight
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int l = live ? __ffsll((unsigned long long)live) - 1 : 64;
@@ -1320,19 +1379,25 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                         if (in) o[k][0] = at[0];
                         if constexpr (F32) {
                             if (in) o[k][1] = at[1];
+                        } else {
+                            rows8 = lane >> 3 == k ? (int)r : rows8;
                         }
                     }
                 }
+                int byte = 0;
+                if (!F32) byte = os[(int64_t)rows8 * OB + min((c0 >> 6) + (lane & 7), OB - 1)];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
+                    const float f = F32 ? 1.f : pow2(__shfl(byte, k * 8 + (lane >> 3), 64) - 141);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         if constexpr (F32) {
                             s[v] += wt[k] * __uint_as_float(o[k][0][v]);
                             s[4 + v] += wt[k] * __uint_as_float(o[k][1][v]);
                         } else {
-                            s[2 * v] += wt[k] * bf16_lo(o[k][0][v]);
-                            s[2 * v + 1] += wt[k] * bf16_hi(o[k][0][v]);
+                            const f32x2 t2 = f16_values(o[k][0][v]);
+                            s[2 * v] += wt[k] * (t2[0] * f);
+                            s[2 * v + 1] += wt[k] * (t2[1] * f);
                         }
                     }
                 }

@@ -315,9 +315,10 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  * for h with 8-bit weights, the quantisation below.  The two kinds of tiles that the products
  * run on differ in their arithmetic.  Thin tiles (passes of few rows an expert) keep the terms
  * W_down h in fp32, so that y is rounded once.  Square tiles (from 8 to 16 rows an expert on average,
- * by type and size: moe_grouped_square) hand them on in bf16: each term is off by up to 2^-8 |w_tj W_down h|, whatever is left of
- * their sum.  8-bit products on square tiles go through a matrix instruction that
- * cuts each product to 2^-13 of the largest of its 8 neighbours along the contraction; thin tiles do not cut.
+ * by type and size: moe_grouped_square) hand them on in 11 bits: each term is off by up to 2^-11 |w_tj W_down h|
+ * (and 2^-39 of the largest of its 64 columns), whatever is left of their sum.  8-bit products on square tiles
+ * go through a matrix instruction that cuts each product to 2^-13 of the largest of its 8 neighbours along the
+ * contraction (which is small beside the 2^-4 of an operand's own quantisation); thin tiles do not cut.
  * Results are deterministic.
  *
  * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=

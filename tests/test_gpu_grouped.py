@@ -732,10 +732,11 @@ def test_the_same_bits_every_time(typ, n):
 
 # --- the terms of a token's sum ---------------------------------------------------------
 
-def _exact_sum(case, hv, ids, w, g, eps, rounding):
+def _exact_sum(case, hv, ids, w, g, eps, rounding, block=0.0):
     """y and the bound of its error: sums of K products in fp32 (``eps`` of their
-    magnitudes), each term rounded to ``rounding`` of itself on its way, m weighted
-    additions in fp32 (2^-22 a term), and one rounding to bf16."""
+    magnitudes), each term rounded on its way to ``rounding`` of itself or ``block`` of the
+    largest of its 64 columns, m weighted additions in fp32 (2^-22 a term), and one rounding
+    to bf16."""
     at, slot = g.offset.tolist(), g.slot_by_expert.long()
     y = torch.zeros(ids.shape[0], case.d, dtype=torch.float64, device="cuda")
     tol = torch.zeros_like(y)
@@ -744,8 +745,10 @@ def _exact_sum(case, hv, ids, w, g, eps, rounding):
         h = hv[at[e]:at[e + 1]]
         o, mag = h @ case.W[2][e].T, h.abs() @ case.W[2][e].abs().T
         wt = w.reshape(-1)[s].double()[:, None]
+        top = torch.nn.functional.pad(mag, (0, -case.d % 64)).view(mag.shape[0], -1, 64).amax(2) if s.numel() else mag
+        top = top.repeat_interleave(64, dim=1)[:, :case.d]  # (a bound of the largest |o|)
         y.index_add_(0, s // case.m, wt * o)
-        tol.index_add_(0, s // case.m, wt.abs() * (eps * mag + (rounding + case.m * 2.0 ** -22) * o.abs()))
+        tol.index_add_(0, s // case.m, wt.abs() * (eps * mag + (rounding + case.m * 2.0 ** -22) * o.abs() + block * top))
     return y, tol + 2.0 ** -8 * (y.abs() + tol)
 
 

@@ -9,7 +9,7 @@ from expert_ffn_amd import _abi
 
 from .gpu_cases import say
 from .test_gpu_grouped import (
-    BF, H8, Case, _check_h, _check_pass, _gpu_layer, _ids, _pow2, _randn, _row_values, _run_parts, _weight_values, _within,
+    BF, H8, Case, _cancelling, _check_h, _check_pass, _down_case, _exact_sum, _gpu_layer, _ids, _pow2, _randn, _row_values, _run_parts, _weight_values, _within,
 )
 
 pytestmark = pytest.mark.gpu
@@ -274,6 +274,79 @@ def test_side_streams(typ):
     torch.cuda.synchronize()
     for ys in got:
         assert all(torch.equal(y, v) for y, v in zip(ys, want))
+
+
+# --- the terms of a token's sum: 11 bits, a power of two for each 64 columns ----------------
+
+TERM = dict(rounding=2.0 ** -11, block=2.0 ** -39)  # half a step; half of fp16's least step against 2^14
+
+
+@pytest.mark.parametrize("typ,layout", BOTH)
+@pytest.mark.parametrize("N,m,n,d", [(8, 2, 400, 512), (16, 8, 300, 528), (64, 4, 500, 80)])
+def test_terms_that_cancel(N, m, n, d, typ, layout):
+    """Terms that leave little of their sum are off by their own roundings and no more."""
+    if layout == "tiled":
+        d = -(-d // 64) * 64
+    say("cancel", N, m, n, d, typ, layout)
+    case = _down_case(N, m, d, 768, typ, layout, seed=n)
+    assert efa.grouped_square(case.layer, n, _abi.MOE_MAT_DOWN)
+    ids, w, g, h, hv = _cancelling(case, n, 80 + n)
+    y = efa.grouped_down(case.layer, h, ids, w, g)
+    want, tol = _exact_sum(case, hv, ids, w, g, case.eps(768), **TERM)
+    _within(y, want, tol, "y")
+
+
+def _random_down(W, m, n, seed, fp8):
+    """A layer with this bf16 W_down [N][d][f] (any gate and up), and h, ids and w for it."""
+    N, d, f = W.shape
+    gate = torch.zeros(N, f, d, dtype=BF, device="cuda")
+    layer = efa.Layer(gate, gate, W, m=m)
+    layer = layer.fp8_copy() if fp8 else layer
+    ids, w = _ids(seed, n, m, N)
+    g = efa.group_slots(ids, N)
+    h = _randn(seed + 1, n * m, f).to(BF).cuda()
+    h = efa.quant_rows(h) if fp8 else h
+    assert efa.grouped_square(layer, n, _abi.MOE_MAT_DOWN)
+    return layer, h, ids, w, g
+
+
+@pytest.mark.parametrize("power", [-118, -40, 0, 40, 110])
+@pytest.mark.parametrize("typ,spread", [("bf16", 0), ("bf16", 24), ("fp8", 0), ("fp8", 5)])
+def test_terms_of_every_magnitude(typ, spread, power):
+    """Columns of y up to 2^24 apart side by side, terms of 2^-118 to 2^110: each column to
+    its own precision."""
+    say("magnitudes", typ, spread, power)
+    N, m, d, f, n = 4, 2, 336, 512, 300
+    scale = torch.randint(-spread, 1, (1, d, 1), generator=torch.Generator().manual_seed(1))
+    W = (_randn(2, N, d, f) * _pow2(scale + power)).to(BF).cuda()
+    layer, h, ids, w, g = _random_down(W, m, n, 3, typ == "fp8")
+    case = Case.__new__(Case)
+    case.N, case.m, case.d, case.f, case.fp8 = N, m, d, f, typ == "fp8"
+    case.W = [None, None, _weight_values(*layer.down) if case.fp8 else W.double()]
+    y = efa.grouped_down(layer, h, ids, w, g)
+    want, tol = _exact_sum(case, _row_values(h) if case.fp8 else h.double(), ids, w, g, case.eps(f), **TERM)
+    _within(y, want, tol + 2.0 ** -134, "y")  # (bf16's least step is 2^-133)
+
+
+@pytest.mark.parametrize("layout", ["plain", "tiled"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_column_that_is_not_finite(bad, layout):
+    """A NaN or an infinity in one row of an expert's W_down reaches that column of the tokens
+    that use the expert; every other value has the bits of a layer where that row is zero."""
+    N, m, d, f, n, e, c = 8, 2, 576, 512, 600, 3, 130
+    W = (_randn(2, N, d, f) * 0.05).to(BF).cuda()
+    W[e, c] = 0
+    layer, h, ids, w, g = _random_down(W, m, n, 3, False)
+    h[:, 7] = 1.0
+    Wb = W.clone()
+    Wb[e, c, 7] = bad
+    other = efa.Layer(layer.w_gate, layer.w_up, Wb, m=m)
+    layer, other = (v.tiled_copy() if layout == "tiled" else v for v in (layer, other))
+    a, b = (efa.grouped_down(v, h, ids, w, g) for v in (layer, other))
+    hit = torch.zeros(n, d, dtype=torch.bool, device="cuda")
+    hit[(ids == e).any(1), c] = True
+    assert hit.any() and torch.isfinite(a).all() and torch.equal(a[~hit], b[~hit])
+    assert (b[hit].isnan() if bad != bad else b[hit] == bad).all()
 
 
 class _GpuCase(Case):
