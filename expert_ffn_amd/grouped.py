@@ -18,6 +18,7 @@ from .ops import Grouping, Layer, _check_dev
 # e4m3 codes [rows][K] and their scale bytes [rows][ceil(K/128)]: code * 2^(byte - 127)
 Quantized = namedtuple("Quantized", ["q", "scale"])
 
+_INT_MAX = (1 << 31) - 1
 _NO_GUARD = contextlib.nullcontext()
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
@@ -29,7 +30,7 @@ def _blocks(v):
 def _int(v):
     """A size as an argument of a call: one that C's int does not hold goes as the largest that
     it does, which every call refuses."""
-    return v if -1 << 31 <= v < 1 << 31 else (1 << 31) - 1
+    return v if -1 << 31 <= v <= _INT_MAX else _INT_MAX
 
 
 def _guard(dev):
@@ -217,8 +218,10 @@ def group_slots(ids, N, out=None, ws=None, stream=None):
         raise ValueError("ids must be [n][m], got %s" % (tuple(ids.shape),))
     n, m = ids.shape
     N, dev = int(N), ids.device
+    if n * m > _INT_MAX or N > _INT_MAX:  # (neither n nor m is more than their product, or one is 0)
+        raise _abi.MoeError("moe_group_slots", _abi.MOE_E_INVAL)
     if ws is None:
-        nb = lib().moe_group_workspace_bytes(_int(n), _int(m), _int(N))
+        nb = lib().moe_group_workspace_bytes(n, m, N)
         if nb == 0:
             raise _abi.MoeError("moe_group_workspace_bytes", _abi.MOE_E_INVAL)
         ws = _empty(nb, _U8, dev, stream)
@@ -227,8 +230,8 @@ def group_slots(ids, N, out=None, ws=None, stream=None):
     ptrs = _check_grouping(out, n, m, N, dev)
     wsp = _check("ws", ws, _U8, ws.shape, dev)
     with _guard(dev):
-        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), _int(n), _int(m), _int(N), *ptrs, wsp,
-                                                       ws.numel(), _on(dev, stream)))
+        check("moe_group_slots", lib().moe_group_slots(ids.data_ptr(), n, m, N, *ptrs, wsp, ws.numel(),
+                                                       _on(dev, stream)))
     return out
 
 
