@@ -378,7 +378,8 @@ typedef struct {
 
 /* Workspace bytes of the calls below for n tokens (0 for invalid arguments); it grows
  * with n, so a workspace for n serves fewer tokens too.  256-byte aligned; no zero-fill
- * needed, nothing kept between calls; calls that share one must not overlap in time. */
+ * needed, nothing kept between calls; calls that share one must not overlap in time.  The
+ * products by themselves take the whole pass's too. */
 size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n);
 
 /* Host only: 1 if a pass of n tokens takes square tiles for its gate/up (mat MOE_MAT_GATE_UP) or
