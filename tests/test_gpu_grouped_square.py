@@ -9,7 +9,8 @@ from expert_ffn_amd import _abi
 
 from .gpu_cases import say
 from .test_gpu_grouped import (
-    BF, H8, Case, _cancelling, _check_h, _check_pass, _down_case, _exact_sum, _gpu_layer, _ids, _pow2, _randn, _row_values, _run_parts, _weight_values, _within,
+    BF, H8, Case, _cancelling, _check_h, _check_pass, _down_case, _exact_sum, _gpu_layer, _ids, _pow2, _randn,
+    _row_values, _run_parts, _weight_values, _within,
 )
 
 pytestmark = pytest.mark.gpu
