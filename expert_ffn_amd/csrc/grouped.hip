@@ -62,16 +62,16 @@ void run_group(Group g, hipStream_t st) {
 
 // Square or thin tiles.  Thin ones take as long again with every 16 rows of an expert, square ones the
 // same from few rows on.  At 8 / 16 / 24 rows of every expert, thin against square, us:
-//     128 experts of 2048 x 768   gate/up bf16   141 / 150 / 205   148 / 134 / 136
-//                                 gate/up e4m3    77 /  90 / 119    82 /  83 /  83
-//                                 down bf16       84 /  98 / 131    89 /  88 /  94
-//                                 down e4m3       42 /  49 /  71    52 /  53 /  56
-//     8 experts of 4096 x 14336   down bf16              204 / 301         234 / 238
+//     128 experts of 2048 x 768   gate/up bf16   138 / 148 / 202   135 / 134 / 135
+//                                 gate/up e4m3    76 /  89 / 118    83 /  83 /  83
+//                                 down bf16       83 /  96 / 129    88 /  93 /  98
+//                                 down e4m3       48 /  56 /  77    60 /  62 /  66
+//     8 experts of 4096 x 14336   down bf16      169 / 198 / 297   261 / 236 / 239
 // (the last with fewer square tiles than compute units).  Routing is never that even, and an expert of
-// 17 rows already takes two thin tiles: passes of the first layer at a mean of 7 / 9 / 11 rows, ids uniform,
-// bf16 223 / 226 / 234 against 235 / 220 / 221, e4m3 126 / 130 / 137 against 142 / 142 / 143; with
-// popularity falling as 1 / rank^1.1, bf16 151 / 171 / 190 against 139 / 156 / 158, e4m3 89 / 102 / 117 against
-// 94 / 107 / 110.
+// 17 rows already takes two thin tiles: passes of the first layer at a mean of 7 / 9 / 11 / 13 rows, ids uniform,
+// bf16 230 / 229 / 235 / 248 against 227 / 228 / 229 / 230, e4m3 129 / 134 / 139 / 148 against 144 / 146 / 147 / 148;
+// with popularity falling as 1 / rank^1.1, bf16 147 / 173 / 191 / 213 against 146 / 160 / 159 / 165, e4m3
+// 93 / 107 / 118 / 130 against 100 / 113 / 112 / 117.
 // The mean counts padding, as only the device knows the groups.  4096 tokens of 8 slots of which 32 tokens are
 // live, thin against square, whole passes of the first layer: bf16 296 / 214, e4m3 232 / 151 (a thin tile's work
 // groups are launched for every row there could be).  900 of 1000 rows on one of the 128 experts: 179 / 166 and 103 / 107.
