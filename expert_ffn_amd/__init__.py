@@ -14,6 +14,6 @@ from .ops import (  # noqa: F401
     tree_select,
 )
 from .grouped import (  # noqa: F401
-    Fp8Layer, Quantized, dequant_rows, expert_grouped, group_slots, group_workspace, grouped_down, grouped_gate_up,
+    Fp8Layer, Int8Layer, Quantized, dequant_rows, expert_grouped, group_slots, group_workspace, grouped_down, grouped_gate_up,
     grouped_square, quant_rows, quant_weights,
 )

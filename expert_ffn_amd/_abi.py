@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SO_PATH = os.path.join(HERE, "libmoe_expert.so")
 
 MOE_OK, MOE_E_INVAL, MOE_E_DTYPE, MOE_E_WORKSPACE, MOE_E_HIP, MOE_E_IDS = 0, -1, -2, -3, -4, -5
-MOE_F32, MOE_BF16, MOE_FP8 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8, MOE_INT8 = 0, 1, 2, 4
 MOE_KIND_SLOT, MOE_KIND_DEDUP = 0, 1
 MOE_MAX_SLOTS, MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_SHARED = 256, 64, 1024, 16
 MOE_FLAG_ACCUMULATE = 1
@@ -34,7 +34,8 @@ EXPORTS = ("moe_route_group", "moe_workspace_bytes", "moe_expert_perslot", "moe_
            "moe_group_workspace_bytes", "moe_group_slots", "moe_quant_rows", "moe_dequant_rows",
            "moe_quant_weights", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
            "moe_grouped_gate_up_fp8", "moe_grouped_down", "moe_grouped_down_fp8", "moe_expert_grouped",
-           "moe_expert_grouped_fp8", "moe_grouped_square")
+           "moe_expert_grouped_fp8", "moe_grouped_square", "moe_quant_rows_int8", "moe_dequant_rows_int8",
+           "moe_grouped_gate_up_int8", "moe_grouped_down_int8", "moe_expert_grouped_int8")
 
 
 class MoeError(RuntimeError):
@@ -58,6 +59,10 @@ class LayerWeights(ctypes.Structure):
 class Fp8Weights(ctypes.Structure):
     _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
+
+
+class Int8Weights(ctypes.Structure):
+    _fields_ = Fp8Weights._fields_
 
 
 MOE_TREE_MAXV, MOE_TREE_MAXK, MOE_TREE_MAXW = 63, 16, 16
@@ -163,9 +168,17 @@ def lib():
             L.moe_grouped_down_fp8.argtypes = [pdesc, pw8, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
             L.moe_expert_grouped.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, sz, vp]
             L.moe_expert_grouped_fp8.argtypes = [pdesc, pw8, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+            pwi = ctypes.POINTER(Int8Weights)
+            L.moe_quant_rows_int8.argtypes = [vp, i64, i32, vp, vp, vp]
+            L.moe_dequant_rows_int8.argtypes = [vp, vp, i64, i32, vp, vp]
+            L.moe_grouped_gate_up_int8.argtypes = [pdesc, pwi, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_grouped_down_int8.argtypes = [pdesc, pwi, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+            L.moe_expert_grouped_int8.argtypes = [pdesc, pwi, vp, vp, vp, i32, vp, vp, vp, sz, vp]
             for f in (L.moe_group_slots, L.moe_quant_rows, L.moe_dequant_rows, L.moe_quant_weights,
                       L.moe_grouped_gate_up, L.moe_grouped_gate_up_fp8, L.moe_grouped_down, L.moe_grouped_down_fp8,
-                      L.moe_expert_grouped, L.moe_expert_grouped_fp8, L.moe_grouped_square):
+                      L.moe_expert_grouped, L.moe_expert_grouped_fp8, L.moe_grouped_square, L.moe_quant_rows_int8,
+                      L.moe_dequant_rows_int8, L.moe_grouped_gate_up_int8, L.moe_grouped_down_int8,
+                      L.moe_expert_grouped_int8):
                 f.restype = ctypes.c_int
             _LIB = L
     return _LIB

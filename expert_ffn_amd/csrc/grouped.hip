@@ -28,17 +28,20 @@ int check_slots(int32_t n, int32_t m, int32_t N) {
     return MOE_OK;
 }
 
+bool grouped_dtype(int32_t t) { return t == MOE_BF16 || t == MOE_FP8 || t == MOE_INT8; }
+int type_of(const moe_layer_desc* d) { return d->dtype == MOE_FP8 ? kFp8 : d->dtype == MOE_INT8 ? kInt8 : kBf16; }
+
 // The descriptor of a grouped product of `dtype` weights.
 int check_desc(const moe_layer_desc* d, int32_t n, int32_t dtype) {
     if (!d) return MOE_E_INVAL;
     if (d->dtype != dtype) return MOE_E_DTYPE;
-    const int per = dtype == MOE_FP8 ? 16 : 8;  // whole 16-byte pieces of a row
+    const int per = dtype == MOE_BF16 ? 8 : 16;  // whole 16-byte pieces of a row
     if (d->d_model < per || d->d_ff < per || d->d_model % per || d->d_ff % per) return MOE_E_DTYPE;
     const int rc = check_slots(n, d->m, d->N);
     if (rc != MOE_OK) return rc;
     if (d->flags & ~(MOE_FLAG_ACCUMULATE | MOE_FLAG_TILED)) return MOE_E_INVAL;
     if (d->n_shared != 0) return MOE_E_INVAL;
-    const int64_t es = dtype == MOE_FP8 ? 1 : 2;
+    const int64_t es = dtype == MOE_BF16 ? 2 : 1;
     if ((d->flags & MOE_FLAG_TILED) && (d->d_model % (64 / es) || d->d_ff % (64 / es))) return MOE_E_INVAL;
     if (d->d_model > MOE_MAX_GROUP_WIDTH || d->d_ff > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
     return MOE_OK;
@@ -54,8 +57,9 @@ int rows_grid(int64_t rows, int K) {  // sixteen blocks of 128 a work group
 
 void run_group(Group g, hipStream_t st) {
     g.G = group_chunks(g.S);
-    // work groups of 1024 threads for the rows to quantise: 64 blocks of 128 at a time
-    const int quant = g.x ? (int)std::min<int64_t>((g.n * blocks_of(g.d) + 63) / 64, 1024) : 0;
+    // work groups of 1024 threads for the rows to quantise: 64 blocks of 128 at a time, or whole rows
+    const int64_t at_once = g.xs8 ? kGThreads / row_lanes(g.d, kGThreads) : 64;
+    const int quant = g.x ? (int)std::min<int64_t>(((g.xs8 ? g.n : g.n * blocks_of(g.d)) + at_once - 1) / at_once, 1024) : 0;
     if (g.G > 1) hipLaunchKernelGGL(k_group_hist, dim3(g.G + quant), dim3(kGThreads), 0, st, g);
     hipLaunchKernelGGL(k_group_scatter, dim3(g.G > 1 ? g.G : 1 + quant), dim3(kGThreads), 0, st, g);
 }
@@ -78,8 +82,10 @@ void run_group(Group g, hipStream_t st) {
 // Square tiles' loads run up to two units ahead into the next tile, which takes four
 // units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
 // tile has beyond it); thin tiles address all of memory.
-bool square(const Args& a, bool fp8, bool gu) {
-    const int64_t kby = (int64_t)a.K * (fp8 ? 1 : 2), most = (1ll << 31) - 4096;
+bool square(const Args& a, int type, bool gu) {
+    const bool fp8 = type == kFp8;
+    if (type == kInt8) return false;
+    const int64_t kby = (int64_t)a.K * elem_size(type), most = (1ll << 31) - 4096;
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
     return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? (fp8 ? 12 : 8) : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
            (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
@@ -95,10 +101,10 @@ Args shape_of(int N, int m, int n, int R, int K) {
     return a;
 }
 bool square_gate_up(const moe_layer_desc* d, int n) {
-    return square(shape_of(d->N, d->m, n, d->d_ff, d->d_model), d->dtype == MOE_FP8, true);
+    return square(shape_of(d->N, d->m, n, d->d_ff, d->d_model), type_of(d), true);
 }
 bool square_down(const moe_layer_desc* d, int n) {
-    return square(shape_of(d->N, d->m, n, d->d_model, d->d_ff), d->dtype == MOE_FP8, false);
+    return square(shape_of(d->N, d->m, n, d->d_model, d->d_ff), type_of(d), false);
 }
 
 // Workspace of a whole pass, and of the products alone (which use the queue, row_of, hf, O and its bytes).
@@ -108,7 +114,7 @@ struct Space {
 
 Space space_of(const moe_layer_desc* d, int32_t n) {
     const size_t S = (size_t)n * d->m;
-    const bool fp8 = d->dtype == MOE_FP8;
+    const bool fp8 = d->dtype == MOE_FP8, i8 = d->dtype == MOE_INT8;
     Space p;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -120,13 +126,13 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert), fp16 from square ones
     size_t o = S * d->d_model * 4;
     if (square_down(d, n)) o = std::max(o / 2, (size_t)16 * d->N * d->d_model * 4);
-    // gate/up's fp32 h (quantised before down begins), then O
-    p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : 0));
+    // gate/up's fp32 h (int8: bf16; quantised before down begins), then O
+    p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : i8 ? S * d->d_ff * 2 : 0));
     p.os = take(S * ((d->d_model + 63) / 64));
-    p.h = take(S * d->d_ff * (fp8 ? 1 : 2));
-    p.hs = take(fp8 ? S * blocks_of(d->d_ff) : 0);
-    p.xq = take(fp8 ? (size_t)n * d->d_model : 0);
-    p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : 0);
+    p.h = take(S * d->d_ff * elem_size(type_of(d)));
+    p.hs = take(fp8 ? S * blocks_of(d->d_ff) : i8 ? S * 4 : 0);
+    p.xq = take(fp8 || i8 ? (size_t)n * d->d_model : 0);
+    p.xs = take(fp8 ? (size_t)n * blocks_of(d->d_model) : i8 ? (size_t)n * 4 : 0);
     p.hist = take(group_ws(kGMaxChunks, d->N));  // (a longer pass may have fewer chunks)
     p.count = take((size_t)d->N * 4);
     p.offset = take((size_t)(d->N + 1) * 4);
@@ -151,19 +157,21 @@ void before_down(const moe_layer_desc* d, int n, const int32_t* sbe, const int32
         hipLaunchKernelGGL(k_row_of, dim3((S + 255) / 256), dim3(256), 0, st, sbe, offset + d->N, S, row_of, queue);
 }
 
-template <bool FP8, bool GU>
+template <int T, bool GU>
 void launch_product(const Args& a, bool tiled, hipStream_t st) {
-    if (square(a, FP8, GU)) {
+    if constexpr (T != kInt8) {
+    if (square(a, T, GU)) {
         const int64_t tiles = (int64_t)a.S / kTM + std::min(a.N, a.S), tc = GU ? kTN / 2 : kTN;
         const int grid = (int)std::min<int64_t>(kCUs, (tiles * ((a.R + tc - 1) / tc) + 7) / 8 * 8);
         if (tiled)
-            hipLaunchKernelGGL((k_tile<FP8, true, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
+            hipLaunchKernelGGL((k_tile<T, true, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
         else
-            hipLaunchKernelGGL((k_tile<FP8, false, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
+            hipLaunchKernelGGL((k_tile<T, false, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
         return;
     }
+    }
     // A launch holds 2^32 threads at most: as many row tiles at once as keep below that.
-    const int64_t cols = (a.R + 15) / 16, units = ((int64_t)a.K * (FP8 ? 1 : 2) + kUnit - 1) / kUnit;
+    const int64_t cols = (a.R + 15) / 16, units = ((int64_t)a.K * elem_size(T) + kUnit - 1) / kUnit;
     const int64_t tiles = (int64_t)a.S / kTile16 + std::min(a.N, a.S);  // most there can be
     auto launch = [&](auto split) {
         constexpr bool SPLIT = decltype(split)::value;
@@ -173,9 +181,9 @@ void launch_product(const Args& a, bool tiled, hipStream_t st) {
             b.tile0 = (int)t;
             const int grid = (int)(std::min(most, tiles - t) * wide);
             if (tiled)
-                hipLaunchKernelGGL((k_thin<FP8, true, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
+                hipLaunchKernelGGL((k_thin<T, true, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
             else
-                hipLaunchKernelGGL((k_thin<FP8, false, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
+                hipLaunchKernelGGL((k_thin<T, false, GU, SPLIT>), dim3(grid), dim3(64 * kThinWaves), 0, st, b);
         }
     };
     if constexpr (!GU) {
@@ -185,12 +193,18 @@ void launch_product(const Args& a, bool tiled, hipStream_t st) {
     launch(std::true_type());
 }
 
+void launch_quant_i8(const void* x, int64_t rows, int K, const int32_t* limit, uint8_t* q, float* s, hipStream_t st) {
+    const int at_once = 256 / row_lanes(K, 256);
+    hipLaunchKernelGGL(k_quant_rows_i8, dim3((int)std::min<int64_t>((rows + at_once - 1) / at_once, 16384)), dim3(256), 0,
+                       st, reinterpret_cast<const char*>(x), rows, K, limit, q, s);
+}
+
 struct Weights {
     const void *w0, *w1;
     const uint8_t *s0, *s1;
 };
 
-template <bool FP8>
+template <int T>
 void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const uint8_t* xs, int32_t n,
                  const int32_t* offset, const int32_t* sbe, void* h, uint8_t* hs, void* hf, int32_t* queue,
                  hipStream_t st) {
@@ -206,16 +220,18 @@ void run_gate_up(const moe_layer_desc* d, const Weights& w, const void* x, const
     a.out = reinterpret_cast<char*>(h);
     a.outs = hs;
     a.queue = queue;
-    const bool by16 = FP8 && !square_gate_up(d, n);  // thin tiles leave h in fp32
-    if (by16) a.out = reinterpret_cast<char*>(hf);
-    launch_product<FP8, true>(a, d->flags & MOE_FLAG_TILED, st);
+    const bool by16 = T == kFp8 && !square_gate_up(d, n);  // thin tiles leave h in fp32
+    if (by16 || T == kInt8) a.out = reinterpret_cast<char*>(hf);  // (a row's scale takes all of it: bf16 first)
+    launch_product<T, true>(a, d->flags & MOE_FLAG_TILED, st);
+    if (T == kInt8)
+        launch_quant_i8(hf, a.S, a.R, offset + d->N, reinterpret_cast<uint8_t*>(h), reinterpret_cast<float*>(hs), st);
     if (by16)
         hipLaunchKernelGGL(k_quant_rows<true>, dim3(rows_grid(a.S, a.R)), dim3(256), 0, st,
                            reinterpret_cast<const char*>(hf), (int64_t)a.S, a.R, offset + d->N,
                            reinterpret_cast<uint8_t*>(h), hs);
 }
 
-template <bool FP8>
+template <int T>
 void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const uint8_t* hs, const int32_t* ids,
               const float* rw, int32_t n, const int32_t* offset, const int32_t* sbe, int32_t* row_of, void* y,
               void* o, uint8_t* os, int32_t* queue, const int32_t* u_err, int32_t* info, hipStream_t st) {
@@ -230,7 +246,7 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     a.outs = os;
     a.queue = queue;
     if (!u_err) a.row_of = row_of;  // (a pass's grouping has left them)
-    launch_product<FP8, false>(a, d->flags & MOE_FLAG_TILED, st);
+    launch_product<T, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
     hipLaunchKernelGGL(square_down(d, n) ? k_combine<false> : k_combine<true>,
                        dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
@@ -238,7 +254,7 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 
-template <bool FP8>
+template <int T>
 int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, const void* x, const int32_t* ids,
              const float* w, int32_t n, void* y, int32_t* info, void* ws, hipStream_t st) {
     const Space p = space_of(d, n);
@@ -260,17 +276,18 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     g.row_of = i32(p.row_of);
     g.queues = i32(p.queue);
     g.nq = 2 * kQueue;
-    if (FP8) {
+    if (T != kBf16) {
         g.x = reinterpret_cast<const char*>(x);
         g.xq = u8(p.xq);
-        g.xs = u8(p.xs);
+        if (T == kInt8) g.xs8 = reinterpret_cast<float*>(b + p.xs);
+        else g.xs = u8(p.xs);
         g.n = n;
         g.d = d->d_model;
     }
     run_group(g, st);
-    run_gate_up<FP8>(d, gu, FP8 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
+    run_gate_up<T>(d, gu, T != kBf16 ? static_cast<const void*>(b + p.xq) : x, u8(p.xs), n, i32(p.offset), i32(p.sbe),
                      b + p.h, u8(p.hs), b + p.hf, i32(p.queue), st);
-    run_down<FP8>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y, b + p.o,
+    run_down<T>(d, dn, b + p.h, u8(p.hs), ids, w, n, i32(p.offset), i32(p.sbe), i32(p.row_of), y, b + p.o,
                   u8(p.os), i32(p.queue) + kQueue, i32(p.u_err), info, st);
     return launched();
 }
@@ -281,6 +298,10 @@ int check_ws(const void* ws, size_t have, size_t need) {
 }
 
 bool fp8_ok(const void* w, const uint8_t* s) { return w && aligned(w, 16) && s; }
+bool int8_ok(const void* w, const float* s) { return w && aligned(w, 16) && s && aligned(s, 4); }
+Weights int8_weights(const void* w0, const void* w1, const float* s0, const float* s1) {
+    return Weights{w0, w1, reinterpret_cast<const uint8_t*>(s0), reinterpret_cast<const uint8_t*>(s1)};
+}
 
 }  // namespace
 
@@ -316,14 +337,14 @@ int moe_group_slots(const int32_t* ids, int32_t n, int32_t m, int32_t N, int32_t
 }
 
 size_t moe_grouped_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
-    if (!desc || (desc->dtype != MOE_BF16 && desc->dtype != MOE_FP8)) return 0;
+    if (!desc || !grouped_dtype(desc->dtype)) return 0;
     if (check_desc(desc, n, desc->dtype) != MOE_OK) return 0;
     return space_of(desc, n).total;
 }
 
 int moe_grouped_square(const moe_layer_desc* desc, int32_t n, int32_t mat) {
     if (!desc || (mat != MOE_MAT_GATE_UP && mat != MOE_MAT_DOWN)) return MOE_E_INVAL;
-    if (desc->dtype != MOE_BF16 && desc->dtype != MOE_FP8) return MOE_E_DTYPE;
+    if (!grouped_dtype(desc->dtype)) return MOE_E_DTYPE;
     const int rc = check_desc(desc, n, desc->dtype);
     if (rc != MOE_OK) return rc;
     return mat == MOE_MAT_GATE_UP ? square_gate_up(desc, n) : square_down(desc, n);
@@ -343,7 +364,7 @@ int moe_grouped_gate_up(const moe_layer_desc* desc, const moe_layer_weights* wei
     int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
     before_gate_up(desc, n, queue, stream_of(hip_stream));
-    run_gate_up<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr}, x, nullptr, n, offset,
+    run_gate_up<kBf16>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr}, x, nullptr, n, offset,
                        slot_by_expert, h, nullptr, nullptr, queue, stream_of(hip_stream));
     return launched();
 }
@@ -362,7 +383,7 @@ int moe_grouped_gate_up_fp8(const moe_layer_desc* desc, const moe_fp8_weights* w
     int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
     (void)hipGetLastError();
     before_gate_up(desc, n, queue, stream_of(hip_stream));
-    run_gate_up<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up}, xq, x_scale, n,
+    run_gate_up<kFp8>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up}, xq, x_scale, n,
                       offset, slot_by_expert, hq, h_scale, reinterpret_cast<char*>(ws) + p.hf, queue,
                       stream_of(hip_stream));
     return launched();
@@ -383,7 +404,7 @@ int moe_grouped_down(const moe_layer_desc* desc, const moe_layer_weights* weight
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
     before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
-    run_down<false>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
+    run_down<kBf16>(desc, Weights{weights->w_down, nullptr, nullptr, nullptr}, h, nullptr, ids, w, n, offset,
                     slot_by_expert, row_of, y, b + p.o, reinterpret_cast<uint8_t*>(b + p.os), queue, nullptr, nullptr,
                     stream_of(hip_stream));
     return launched();
@@ -405,7 +426,7 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
     int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
     int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
     before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
-    run_down<true>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
+    run_down<kFp8>(desc, Weights{weights->w_down, nullptr, weights->s_down, nullptr}, hq, h_scale, ids, w, n, offset,
                    slot_by_expert, row_of, y, b + p.o, reinterpret_cast<uint8_t*>(b + p.os), queue, nullptr, nullptr,
                    stream_of(hip_stream));
     return launched();
@@ -423,7 +444,7 @@ int moe_expert_grouped(const moe_layer_desc* desc, const moe_layer_weights* weig
         return MOE_E_INVAL;
     rc = check_ws(ws, ws_bytes, space_of(desc, n).total);
     if (rc != MOE_OK) return rc;
-    return run_pass<false>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr},
+    return run_pass<kBf16>(desc, Weights{weights->w_gate, weights->w_up, nullptr, nullptr},
                            Weights{weights->w_down, nullptr, nullptr, nullptr}, x, ids, w, n, y, info, ws,
                            stream_of(hip_stream));
 }
@@ -438,9 +459,86 @@ int moe_expert_grouped_fp8(const moe_layer_desc* desc, const moe_fp8_weights* we
         return MOE_E_INVAL;
     rc = check_ws(ws, ws_bytes, space_of(desc, n).total);
     if (rc != MOE_OK) return rc;
-    return run_pass<true>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up},
+    return run_pass<kFp8>(desc, Weights{weights->w_gate, weights->w_up, weights->s_gate, weights->s_up},
                           Weights{weights->w_down, nullptr, weights->s_down, nullptr}, x, ids, w, n, y, info, ws,
                           stream_of(hip_stream));
+}
+
+int moe_grouped_gate_up_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* xq,
+                             const float* x_scale, int32_t n, const int32_t* offset, const int32_t* slot_by_expert,
+                             void* hq, float* h_scale, void* ws, size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_INT8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !int8_ok(weights->w_gate, weights->s_gate) || !int8_ok(weights->w_up, weights->s_up) ||
+        !int8_ok(xq, x_scale) || !int8_ok(hq, h_scale) || !offset || !slot_by_expert)
+        return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    int32_t* queue = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(ws) + p.queue);
+    (void)hipGetLastError();
+    before_gate_up(desc, n, queue, stream_of(hip_stream));
+    run_gate_up<kInt8>(desc, int8_weights(weights->w_gate, weights->w_up, weights->s_gate, weights->s_up), xq,
+                       reinterpret_cast<const uint8_t*>(x_scale), n, offset, slot_by_expert, hq,
+                       reinterpret_cast<uint8_t*>(h_scale), reinterpret_cast<char*>(ws) + p.hf, queue,
+                       stream_of(hip_stream));
+    return launched();
+}
+
+int moe_grouped_down_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* hq,
+                          const float* h_scale, const int32_t* ids, const float* w, int32_t n, const int32_t* offset,
+                          const int32_t* slot_by_expert, void* y, void* ws, size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_INT8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !int8_ok(weights->w_down, weights->s_down) || !int8_ok(hq, h_scale) || !ids || !w || !offset ||
+        !slot_by_expert || !y || !aligned(y, 16))
+        return MOE_E_INVAL;
+    const Space p = space_of(desc, n);
+    rc = check_ws(ws, ws_bytes, p.total);
+    if (rc != MOE_OK) return rc;
+    (void)hipGetLastError();
+    char* b = reinterpret_cast<char*>(ws);
+    int32_t* row_of = reinterpret_cast<int32_t*>(b + p.row_of);
+    int32_t* queue = reinterpret_cast<int32_t*>(b + p.queue);
+    before_down(desc, n, slot_by_expert, offset, row_of, queue, stream_of(hip_stream));
+    run_down<kInt8>(desc, int8_weights(weights->w_down, nullptr, weights->s_down, nullptr), hq,
+                    reinterpret_cast<const uint8_t*>(h_scale), ids, w, n, offset, slot_by_expert, row_of, y, b + p.o,
+                    reinterpret_cast<uint8_t*>(b + p.os), queue, nullptr, nullptr, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_expert_grouped_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* x,
+                            const int32_t* ids, const float* w, int32_t n, void* y, int32_t* info, void* ws,
+                            size_t ws_bytes, void* hip_stream) {
+    int rc = check_desc(desc, n, MOE_INT8);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !int8_ok(weights->w_gate, weights->s_gate) || !int8_ok(weights->w_up, weights->s_up) ||
+        !int8_ok(weights->w_down, weights->s_down) || !x || !aligned(x, 16) || !ids || !w || !y || !aligned(y, 16))
+        return MOE_E_INVAL;
+    rc = check_ws(ws, ws_bytes, space_of(desc, n).total);
+    if (rc != MOE_OK) return rc;
+    return run_pass<kInt8>(desc, int8_weights(weights->w_gate, weights->w_up, weights->s_gate, weights->s_up),
+                           int8_weights(weights->w_down, nullptr, weights->s_down, nullptr), x, ids, w, n, y, info, ws,
+                           stream_of(hip_stream));
+}
+
+int moe_quant_rows_int8(const void* x, int64_t rows, int32_t K, void* q, float* scale, void* hip_stream) {
+    if (!x || !aligned(x, 16) || !int8_ok(q, scale)) return MOE_E_INVAL;
+    if (K < 16 || K % 16) return MOE_E_DTYPE;
+    if (rows < 1 || rows > MOE_MAX_QUANT_ROWS || K > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    (void)hipGetLastError();
+    launch_quant_i8(x, rows, K, nullptr, reinterpret_cast<uint8_t*>(q), scale, stream_of(hip_stream));
+    return launched();
+}
+
+int moe_dequant_rows_int8(const void* q, const float* scale, int64_t rows, int32_t K, void* x, void* hip_stream) {
+    if (!x || !aligned(x, 16) || !int8_ok(q, scale)) return MOE_E_INVAL;
+    if (K < 16 || K % 16) return MOE_E_DTYPE;
+    if (rows < 1 || rows > MOE_MAX_QUANT_ROWS || K > MOE_MAX_GROUP_WIDTH) return MOE_E_INVAL;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(k_dequant_rows_i8, dim3(rows_grid(rows, K)), dim3(256), 0, stream_of(hip_stream),
+                       reinterpret_cast<const uint8_t*>(q), scale, rows, K, reinterpret_cast<char*>(x));
+    return launched();
 }
 
 int moe_quant_rows(const void* x, int64_t rows, int32_t K, void* q, uint8_t* scale, void* hip_stream) {

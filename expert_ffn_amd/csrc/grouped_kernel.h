@@ -37,17 +37,26 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned int u32x4;
 typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
 
 constexpr int kUnit = 128;   // bytes of a contraction unit
 constexpr int kBlk = 128;    // elements of a quantisation block
 constexpr int kTile16 = 16;  // rows of a matrix operand
 
+// What the operands hold: bf16 values, e4m3 codes with a power of two for each block, or int8 codes
+// with a scale for each token and each weight row.
+constexpr int kBf16 = 0, kFp8 = 1, kInt8 = 2;
+constexpr int elem_size(int T) { return T == kBf16 ? 2 : 1; }
+// Sums of int8 products are whole numbers, at most 2^16 * 127^2 < 2^31 of them.
+template <int T>
+using Sum4 = std::conditional_t<T == kInt8, i32x4, f32x4>;
+
 struct Args {
     const char* x;        // x [n][K] (gate/up, gathered) or h [S][K] (down, in row order)
-    const uint8_t* xs;    // e4m3: scale bytes of x / h rows
+    const uint8_t* xs;    // e4m3: scale bytes of x / h rows; int8: their scales (float)
     const char* w0;       // W_gate or W_down
     const char* w1;       // W_up
-    const uint8_t* s0;    // e4m3: scale bytes of w0, w1  [N][ceil(R/128)][ceil(K/128)]
+    const uint8_t* s0;    // e4m3: scale bytes of w0, w1  [N][ceil(R/128)][ceil(K/128)]; int8: scales (float) [N][R]
     const uint8_t* s1;
     const int32_t* offset;
     const int32_t* slot;
@@ -63,9 +72,12 @@ __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlan
 
 // One unit's product.  e4m3: the operands' scale bytes, sa's lowest and byte `sel` of sb
 // (a constant once its loop is unrolled).
-template <bool FP8>
-__device__ __forceinline__ f32x4 mma_unit(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c, int sa, int sb, int sel = 0) {
-    if constexpr (FP8) {
+template <int T>
+__device__ __forceinline__ Sum4<T> mma_unit(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, Sum4<T> c, int sa, int sb, int sel = 0) {
+    if constexpr (T == kInt8) {
+        c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a0), __builtin_bit_cast(i32x4, b0), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a1), __builtin_bit_cast(i32x4, b1), c, 0, 0, 0);
+    } else if constexpr (T == kFp8) {
         struct Pair {
             u32x4 lo, hi;
         };
@@ -244,6 +256,126 @@ __global__ __launch_bounds__(256) void k_quant_weights(const char* __restrict__ 
     if (tid == 0) s[b] = (uint8_t)(k + 127);
 }
 
+// --- int8 codes with one scale a row ------------------------------------------------------
+// s = max|v| / 127 and the code is 127 v / max|v| to the nearest integer, ties to even, exactly: of bf16
+// values v = a 2^p and max = b 2^q (a, b < 256) the quotient is a half, or at least 2^-17 of itself away from one
+// (|254 a 2^p - (2 k + 1) b 2^q| is a multiple of 2^p), and the quotient below is right to 2^-23 and exact where
+// fp32 holds it.  So a quotient half way (v = max / 2 is one: 63.5) is met as such, which v / s would not do.
+struct RowScale {
+    float top, inv;  // max / 2^e in [1/2, 1) and about its reciprocal; top 0: a row of zeros
+    int e;
+};
+// `bits`: of the row's largest |v|, what is not finite above
+__device__ __forceinline__ RowScale row_scale(uint32_t bits) {
+    const float a = bits < 0x7f800000u ? __uint_as_float(bits) : 0.f;
+    const float top = __builtin_amdgcn_frexp_mantf(a);
+    return RowScale{top, a > 0.f ? __builtin_amdgcn_rcpf(top) : 0.f, __builtin_amdgcn_frexp_expf(a)};
+}
+// its scale, NaN for a row with what is not finite (whose codes are 0: it stands for NaN throughout)
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    return bits < 0x7f800000u ? __uint_as_float(bits) / 127.f : __uint_as_float(0x7fc00000u);
+}
+// the code in the lowest byte
+__device__ __forceinline__ uint32_t code_i8(float v, const RowScale& r) {
+    const float t = 127.f * __builtin_ldexpf(v, -r.e);  // exact: 8 bits times 7
+    float q = t * r.inv;
+    q = fmaf(fmaf(-r.top, q, t), r.inv, q);
+    return __float_as_uint(q + 12582912.f);  // 1.5 * 2^23: the sum's last place is 1
+}
+__device__ __forceinline__ uint32_t codes4_i8(float a, float b, float c, float d, const RowScale& r) {
+    const uint32_t lo = __builtin_amdgcn_perm(code_i8(b, r), code_i8(a, r), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code_i8(d, r), code_i8(c, r), 0x04000c0cu);
+    return r.inv != 0.f ? lo | hi : 0u;
+}
+
+// Rows of bf16 values to codes and scales; work group g of G.  L lanes a row (a power of two, from the row's
+// length: four vectors of eight values a lane, held between the maximum and the codes; longer rows than a work
+// group so holds are read again).
+constexpr int kRowVecs = 4;
+__host__ __device__ __forceinline__ int row_lanes(int K, int threads) {
+    int L = 16;
+    while (L < threads && L * kRowVecs * 8 < K) L *= 2;
+    return L;
+}
+__device__ __forceinline__ void quant_rows_i8(const char* __restrict__ x, int64_t rows, int K, uint8_t* __restrict__ q,
+                                              float* __restrict__ s, int64_t g, int64_t G) {
+    __shared__ uint32_t part[2][16];  // a wave's largest; two rounds in turn
+    const int L = row_lanes(K, blockDim.x), per = blockDim.x / L, l = threadIdx.x & (L - 1), span = L * 8;
+    const int V = (K + span - 1) / span;  // vectors a lane
+    int turn = 0;
+    for (int64_t b = g * per; b < rows; b += G * per, turn ^= 1) {
+        const int64_t row = b + threadIdx.x / L;
+        const bool in = row < rows;
+        const char* xr = x + (in ? row : 0) * K * 2;
+        u32x4 a[kRowVecs];
+        uint32_t m = 0;
+        auto load = [&](int v0) {
+#pragma unroll
+            for (int i = 0; i < kRowVecs; ++i) {
+                const int c = (v0 + i) * span + l * 8;
+                a[i] = in && c < K ? *reinterpret_cast<const u32x4*>(xr + (int64_t)c * 2) : u32x4{0u, 0u, 0u, 0u};
+            }
+        };
+        for (int v0 = 0; v0 < V; v0 += kRowVecs) {
+            load(v0);
+#pragma unroll
+            for (int i = 0; i < kRowVecs; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = max(m, max(a[i][j] << 16 & 0x7fffffffu, a[i][j] & 0x7fff0000u));
+        }
+        for (int o = min(L, 64) / 2; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        if (L > 64) {
+            if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = m;
+            __syncthreads();
+            const int w0 = threadIdx.x / L * (L / 64);
+            for (int w = 0; w < L / 64; ++w) m = max(m, part[turn][w0 + w]);
+        }
+        const RowScale r = row_scale(m);
+        if (in && l == 0) s[row] = scale_of(m);
+        for (int v0 = 0; v0 < V; v0 += kRowVecs) {
+            if (V > kRowVecs) load(v0);
+#pragma unroll
+            for (int i = 0; i < kRowVecs; ++i) {
+                const int c = (v0 + i) * span + l * 8;
+                if (in && c < K)
+                    *reinterpret_cast<u32x2*>(q + row * K + c) =
+                        u32x2{codes4_i8(bf16_lo(a[i][0]), bf16_hi(a[i][0]), bf16_lo(a[i][1]), bf16_hi(a[i][1]), r),
+                              codes4_i8(bf16_lo(a[i][2]), bf16_hi(a[i][2]), bf16_lo(a[i][3]), bf16_hi(a[i][3]), r)};
+            }
+        }
+    }
+}
+
+// `limit`: as above
+__global__ __launch_bounds__(256) void k_quant_rows_i8(const char* __restrict__ x, int64_t rows, int K,
+                                                      const int32_t* __restrict__ limit, uint8_t* __restrict__ q,
+                                                      float* __restrict__ s) {
+    if (limit) rows = min(rows, (int64_t)max(*limit, 0));
+    quant_rows_i8(x, rows, K, q, s, blockIdx.x, gridDim.x);
+}
+
+// Codes and scales back to bf16: code * scale, rounded.
+__global__ __launch_bounds__(256) void k_dequant_rows_i8(const uint8_t* __restrict__ q, const float* __restrict__ s,
+                                                        int64_t rows, int K, char* __restrict__ x) {
+    const int KB = (K + kBlk - 1) / kBlk, l = threadIdx.x & 15;
+    const int64_t blocks = rows * KB;
+    for (int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; b < blocks; b += (int64_t)gridDim.x * 16) {
+        const int64_t row = b / KB;
+        const int c = (int)(b - row * KB) * kBlk + l * 8;
+        if (c >= K) continue;
+        const float f = s[row];
+        const u32x2 v = *reinterpret_cast<const u32x2*>(q + row * K + c);
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            auto at = [&](int k) { return (float)((int)(v[i] << (24 - 8 * k)) >> 24) * f; };
+            o[2 * i] = bf16_pair(at(0), at(1));
+            o[2 * i + 1] = bf16_pair(at(2), at(3));
+        }
+        *reinterpret_cast<u32x4*>(x + (row * K + c) * 2) = o;
+    }
+}
+
 // --- grouping of any number of slots -------------------------------------------------
 // A stable counting sort over G chunks of slots, one work group of 16 waves each, the
 // waves on consecutive pieces of the chunk: first every chunk's histogram, then every
@@ -274,12 +406,16 @@ struct Group {
     int nq;
     const char* x;          // null, or rows to quantise (n rows of d)
     uint8_t *xq, *xs;
+    float* xs8;             // null: to e4m3; or the scales of int8 codes
     int n, d;
 };
 
 __device__ __forceinline__ bool group_quant(const Group& g) {
     if ((int)blockIdx.x < g.G) return false;
-    quant_rows<false>(g.x, g.n, g.d, g.xq, g.xs, blockIdx.x - g.G, gridDim.x - g.G);
+    if (g.xs8)
+        quant_rows_i8(g.x, g.n, g.d, g.xq, g.xs8, blockIdx.x - g.G, gridDim.x - g.G);
+    else
+        quant_rows<false>(g.x, g.n, g.d, g.xq, g.xs, blockIdx.x - g.G, gridDim.x - g.G);
     return true;
 }
 
@@ -525,10 +661,12 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float f) {
                                                __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true)}});
 }
 
-template <bool FP8, bool TILED, bool GU, bool SPLIT>
+template <int T, bool TILED, bool GU, bool SPLIT>
 __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
-    constexpr int ES = FP8 ? 1 : 2, NW = GU ? 2 : 1, AHEAD = !SPLIT ? 3 : GU ? 2 : 4;
-    __shared__ f32x4 red[SPLIT ? kThinWaves : 1][NW][64];
+    constexpr bool FP8 = T == kFp8;
+    constexpr int ES = elem_size(T), NW = GU ? 2 : 1, AHEAD = !SPLIT ? 3 : GU ? 2 : 4;
+    using Sum = Sum4<T>;
+    __shared__ Sum red[SPLIT ? kThinWaves : 1][NW][64];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int lr = lane & 15, q = lane >> 4;
     const int CB = (a.R + 15) / 16, CW = SPLIT ? CB : (CB + kThinWaves - 1) / kThinWaves;  // work groups a row tile
@@ -551,9 +689,9 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
     }
     const int RB = (a.R + kBlk - 1) / kBlk;
     const int64_t sw = FP8 ? ((int64_t)t.e * RB + cb * 16 / kBlk) * KB : 0;
-    f32x4 acc[NW];
+    Sum acc[NW];
 #pragma unroll
-    for (int i = 0; i < NW; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NW; ++i) acc[i] = Sum{0, 0, 0, 0};
     constexpr int STEP = SPLIT ? kThinWaves : 1;
     for (int u0 = SPLIT ? wave : 0; u0 < U; u0 += STEP * AHEAD) {
         u32x4 b[AHEAD][2], w[AHEAD][NW][2];
@@ -604,11 +742,11 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
             } else {
 #pragma unroll
                 for (int i = 0; i < NW; ++i)
-                    acc[i] = mma_unit<false>(w[p][i][0], w[p][i][1], b[p][0], b[p][1], acc[i], 0, 0);
+                    acc[i] = mma_unit<T>(w[p][i][0], w[p][i][1], b[p][0], b[p][1], acc[i], 0, 0);
             }
         }
     }
-    f32x4 v[NW];
+    Sum sum[NW];
     if constexpr (SPLIT) {
 #pragma unroll
         for (int i = 0; i < NW; ++i) red[wave][i][lane] = acc[i];
@@ -616,16 +754,28 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
         if (wave) return;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            v[i] = red[0][i][lane];
+            sum[i] = red[0][i][lane];
 #pragma unroll
-            for (int k = 1; k < kThinWaves; ++k) v[i] += red[k][i][lane];
+            for (int k = 1; k < kThinWaves; ++k) sum[i] += red[k][i][lane];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) v[i] = acc[i];
+        for (int i = 0; i < NW; ++i) sum[i] = acc[i];
     }
     const int c = cb * 16 + 4 * q;
     if (t.r0 + lr >= t.end || c >= a.R) return;
+    f32x4 v[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        if constexpr (T == kInt8) {  // (R is a multiple of 16: the scales of four columns are there)
+            const float sx = reinterpret_cast<const float*>(a.xs)[xrow];
+            const float* sw = reinterpret_cast<const float*>(i ? a.s1 : a.s0) + (int64_t)t.e * a.R + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] = (float)sum[i][k] * sx * sw[k];
+        } else {
+            v[i] = sum[i];
+        }
+    }
     if (GU) {
         float h[4];
 #pragma unroll
@@ -838,9 +988,10 @@ struct TileLds {
     int32_t offset[MOE_MAX_EXPERTS + 1];
 };
 
-template <bool FP8, bool TILED, bool GU>
+template <int T, bool TILED, bool GU>
 __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
-    constexpr int ES = FP8 ? 1 : 2;
+    constexpr bool FP8 = T == kFp8;
+    constexpr int ES = elem_size(T);
     __shared__ TileLds lds;
     // The arguments that are needed now and then are loaded again each time: kept, they would
     // push others out of the scalar registers.
@@ -1048,7 +1199,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 for (int i = F; i < E; ++i) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[i][j] = mma_unit<FP8>(b[j][0], b[j][1], x[i % H][0], x[i % H][1], acc[i][j],
+                        acc[i][j] = mma_unit<T>(b[j][0], b[j][1], x[i % H][0], x[i % H][1], acc[i][j],
                                                   GU && j >= 2 ? e1 : e0, (int)ex[i / 4], i);
                     __builtin_amdgcn_sched_barrier(0);
                     then(i);

@@ -710,7 +710,8 @@ int moe_pack_tiled(const moe_layer_desc* desc, const void* w, void* w_tiled, int
     moe_layer_desc dd = *desc;
     dd.flags = MOE_FLAG_TILED;
     dd.n_shared = 0;
-    if (desc->dtype == MOE_FP8) {  // e4m3 codes: steps of 64 elements, the bytes of bf16 rows half as wide
+    const bool codes = desc->dtype == MOE_FP8 || desc->dtype == MOE_INT8;
+    if (codes) {  // 8-bit codes: steps of 64 elements, the bytes of bf16 rows half as wide
         if (desc->d_model < 64 || desc->d_ff < 64 || desc->d_model % 64 || desc->d_ff % 64) return MOE_E_INVAL;
         dd.dtype = MOE_BF16;
         dd.d_model /= 2;
@@ -719,7 +720,7 @@ int moe_pack_tiled(const moe_layer_desc* desc, const void* w, void* w_tiled, int
     const int rc = check_desc(&dd, 1);
     if (rc != MOE_OK) return rc;
     if (!w || !w_tiled || !aligned16(w) || !aligned16(w_tiled)) return MOE_E_INVAL;
-    const int64_t es = desc->dtype == MOE_FP8 ? 1 : desc->dtype == MOE_BF16 ? 2 : 4;
+    const int64_t es = codes ? 1 : desc->dtype == MOE_BF16 ? 2 : 4;
     const int64_t bytes = (int64_t)desc->N * desc->d_model * desc->d_ff * es;
     const char* a0 = reinterpret_cast<const char*>(w);
     const char* b0 = reinterpret_cast<const char*>(w_tiled);

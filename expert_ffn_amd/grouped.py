@@ -1,5 +1,5 @@
 """The expert operation on grouped rows: passes of any length, in bf16 or with 8-bit
-weights (argument marshalling of the grouped calls of ``include/moe_expert.h``).
+weights, e4m3 or int8 (argument marshalling of the grouped calls of ``include/moe_expert.h``).
 
 Every call runs on ``stream`` (default: the current stream of its tensors' device), with
 that device current.  Outputs and workspaces that are not given are allocated for that
@@ -15,12 +15,15 @@ from . import _abi
 from ._abi import check, lib
 from .ops import Grouping, Layer, _check_dev
 
-# e4m3 codes [rows][K] and their scale bytes [rows][ceil(K/128)]: code * 2^(byte - 127)
+# e4m3 codes [rows][K] and their scale bytes [rows][ceil(K/128)]: code * 2^(byte - 127); or int8
+# codes [rows][K] and float32 scales [rows]: code * scale
 Quantized = namedtuple("Quantized", ["q", "scale"])
 
 _INT_MAX = (1 << 31) - 1
 _NO_GUARD = contextlib.nullcontext()
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_I8 = torch.int8
+_SUFFIX = {_BF16: "", _E4M3: "_fp8", _I8: "_int8"}  # of the calls on rows of this type
 
 
 def _blocks(v):
@@ -76,11 +79,26 @@ def _ws(ws, desc, n, dev, stream):
     return ws
 
 
-def _check_quantized(name, v, rows, K, dev):
+def _check_codes(codes):
+    if codes is not _E4M3 and codes is not _I8:
+        raise TypeError("codes are float8_e4m3fn or int8, not %s" % (codes,))
+
+
+def _scales(codes, rows, K):
+    """(type, shape) of the scales of rows of codes."""
+    return (_U8, (rows, _blocks(K))) if codes is _E4M3 else (_F32, (rows,))
+
+
+def _new_quantized(codes, rows, K, dev, stream):
+    typ, shape = _scales(codes, rows, K)
+    return Quantized(_empty((rows, K), codes, dev, stream), _empty(shape, typ, dev, stream))
+
+
+def _check_quantized(name, v, codes, rows, K, dev):
     if not isinstance(v, Quantized):
-        raise TypeError("%s must be Quantized (codes and scale bytes), got %s" % (name, type(v).__name__))
-    return (_check(name + ".q", v.q, _E4M3, (rows, K), dev),
-            _check(name + ".scale", v.scale, _U8, (rows, _blocks(K)), dev))
+        raise TypeError("%s must be Quantized (codes and scales), got %s" % (name, type(v).__name__))
+    typ, shape = _scales(codes, rows, K)
+    return _check(name + ".q", v.q, codes, (rows, K), dev), _check(name + ".scale", v.scale, typ, shape, dev)
 
 
 def _check_grouping(g, n, m, N, dev):
@@ -91,25 +109,22 @@ def _check_grouping(g, n, m, N, dev):
             _check("distinct", g.distinct, _I32, (N,), dev), _check("u_and_err", g.u_and_err, _I32, (2,), dev))
 
 
-class Fp8Layer:
-    """8-bit weights of one MoE layer: each matrix a pair (codes float8_e4m3fn, scale
-    bytes uint8), W_gate and W_up [N][d_ff][d] with [N][d_ff/128][d/128] scales, W_down
-    [N][d][d_ff] with [N][d/128][d_ff/128] (sizes rounded up), as ``Layer.fp8_copy``
-    makes them; with ``tiled`` the codes are in the layout of ``moe_pack_tiled``."""
+class _CodesLayer:
+    """8-bit weights of one MoE layer: each matrix a pair (codes, scales)."""
 
     def __init__(self, gate, up, down, m, tiled=False):
         for name, pair in (("gate", gate), ("up", up), ("down", down)):
             if len(pair) != 2:
-                raise ValueError("%s must be (codes, scale bytes)" % name)
+                raise ValueError("%s must be (codes, %s)" % (name, self._what))
         N, d_ff, d = gate[0].shape
         self.N, self.m, self.d, self.d_ff = N, int(m), d, d_ff
         self.tiled = bool(tiled)
         for name, (q, s), (R, K) in (("gate", gate, (d_ff, d)), ("up", up, (d_ff, d)), ("down", down, (d, d_ff))):
-            _check_dev("w_" + name, q, _E4M3)
-            _check("w_" + name, q, _E4M3, (N, R, K), gate[0].device)
-            _check("s_" + name, s, _U8, (N, _blocks(R), _blocks(K)), gate[0].device)
+            _check_dev("w_" + name, q, self.codes)
+            _check("w_" + name, q, self.codes, (N, R, K), gate[0].device)
+            _check("s_" + name, s, *self._scales(N, R, K), gate[0].device)
         self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
-        self._weights = _abi.Fp8Weights(*(m_[i].data_ptr() for i in (0, 1) for m_ in (self.gate, self.up, self.down)))
+        self._weights = self._struct(*(m_[i].data_ptr() for i in (0, 1) for m_ in (self.gate, self.up, self.down)))
 
     @property
     def device(self):
@@ -117,12 +132,12 @@ class Fp8Layer:
 
     @property
     def expert_bytes(self):
-        return 3 * self.d * self.d_ff + sum(p[1][0].numel() for p in (self.gate, self.up, self.down))
+        return 3 * self.d * self.d_ff + sum(p[1][0].numel() * p[1].element_size() for p in (self.gate, self.up, self.down))
 
     def desc(self, accumulate=False):
         """The layer's descriptor (``moe_layer_desc``)."""
         flags = (_abi.MOE_FLAG_ACCUMULATE if accumulate else 0) | (_abi.MOE_FLAG_TILED if self.tiled else 0)
-        return _abi.LayerDesc(self.N, self.m, self.d, self.d_ff, _abi.MOE_FP8, flags, 0)
+        return _abi.LayerDesc(self.N, self.m, self.d, self.d_ff, self._code, flags, 0)
 
     def tiled_copy(self, stream=None):
         """The same layer with the codes copied into the tiled layout by
@@ -132,28 +147,62 @@ class Fp8Layer:
         desc, dev = self.desc(), self.device
 
         def tl(pair, mat):
-            out = _empty(pair[0].shape, _E4M3, dev, stream)
+            out = _empty(pair[0].shape, self.codes, dev, stream)
             with _guard(dev):
                 check("moe_pack_tiled", lib().moe_pack_tiled(ctypes.byref(desc), pair[0].data_ptr(), out.data_ptr(),
                                                              mat, _on(dev, stream)))
             return out, pair[1]
         G, D = _abi.MOE_MAT_GATE_UP, _abi.MOE_MAT_DOWN
-        return Fp8Layer(tl(self.gate, G), tl(self.up, G), tl(self.down, D), self.m, tiled=True)
+        return type(self)(tl(self.gate, G), tl(self.up, G), tl(self.down, D), self.m, tiled=True)
 
     def grouped_workspace(self, n):
         """Workspace of the grouped calls on this layer for passes of up to n tokens."""
         return grouped_workspace(self, n)
 
 
-def quant_weights(w, stream=None):
-    """bf16 matrices [N][R][K] to (codes, scale bytes [N][R/128][K/128]), one power of
-    two for each block of 128 x 128 (``moe_quant_weights``)."""
+class Fp8Layer(_CodesLayer):
+    """8-bit weights of one MoE layer: each matrix a pair (codes float8_e4m3fn, scale
+    bytes uint8), W_gate and W_up [N][d_ff][d] with [N][d_ff/128][d/128] scales, W_down
+    [N][d][d_ff] with [N][d/128][d_ff/128] (sizes rounded up), as ``Layer.fp8_copy``
+    makes them; with ``tiled`` the codes are in the layout of ``moe_pack_tiled``."""
+
+    codes, _code, _what, _struct = _E4M3, _abi.MOE_FP8, "scale bytes", _abi.Fp8Weights
+
+    @staticmethod
+    def _scales(N, R, K):
+        return _U8, (N, _blocks(R), _blocks(K))
+
+
+class Int8Layer(_CodesLayer):
+    """8-bit integer weights of one MoE layer: each matrix a pair (codes int8, scales
+    float32 of its output channels), W_gate and W_up [N][d_ff][d] with [N][d_ff] scales,
+    W_down [N][d][d_ff] with [N][d], as ``Layer.int8_copy`` makes them; with ``tiled`` the
+    codes are in the layout of ``moe_pack_tiled``."""
+
+    codes, _code, _what, _struct = _I8, _abi.MOE_INT8, "scales", _abi.Int8Weights
+
+    @staticmethod
+    def _scales(N, R, K):
+        return _F32, (N, R)
+
+
+def quant_weights(w, stream=None, dtype=_E4M3):
+    """bf16 matrices [N][R][K] to (codes, scales): with float8_e4m3fn scale bytes
+    [N][R/128][K/128], one power of two for each block of 128 x 128 (``moe_quant_weights``);
+    with int8 float32 [N][R], one for each row (``moe_quant_rows_int8``)."""
+    _check_codes(dtype)
     _check_dev("w", w, _BF16)
     if w.dim() != 3:
         raise ValueError("w must be [N][R][K], got %s" % (tuple(w.shape),))
     N, R, K = w.shape
     dev = w.device
-    q = _empty((N, R, K), _E4M3, dev, stream)
+    q = _empty((N, R, K), dtype, dev, stream)
+    if dtype is _I8:
+        s = _empty((N, R), _F32, dev, stream)
+        with _guard(dev):
+            check("moe_quant_rows_int8", lib().moe_quant_rows_int8(w.data_ptr(), N * R, _int(K), q.data_ptr(),
+                                                                   s.data_ptr(), _on(dev, stream)))
+        return q, s
     s = _empty((N, _blocks(R), _blocks(K)), _U8, dev, stream)
     with _guard(dev):
         check("moe_quant_weights", lib().moe_quant_weights(w.data_ptr(), _int(N), _int(R), _int(K), q.data_ptr(),
@@ -161,44 +210,59 @@ def quant_weights(w, stream=None):
     return q, s
 
 
-def fp8_copy(layer, stream=None):
-    """``layer`` (plain bf16 weights) with 8-bit weights in plain layout."""
+def _codes_copy(cls, layer, stream):
     if layer.dtype != torch.bfloat16 or layer.packed or layer.tiled:
-        raise ValueError("fp8_copy takes plain bf16 weights (tile the copy)")
+        raise ValueError("%s takes plain bf16 weights (tile the copy)" % ("fp8_copy" if cls is Fp8Layer else "int8_copy"))
     if layer.shared is not None:
         raise ValueError("copy the routed and the shared experts as layers of their own (without_shared)")
-    return Fp8Layer(*(quant_weights(w, stream) for w in (layer.w_gate, layer.w_up, layer.w_down)), m=layer.m)
+    return cls(*(quant_weights(w, stream, cls.codes) for w in (layer.w_gate, layer.w_up, layer.w_down)), m=layer.m)
 
 
-def quant_rows(x, out=None, stream=None):
-    """Rows of bf16 values [rows][K] to ``Quantized``, one power of two for each block of
-    128 along a row (``moe_quant_rows``)."""
+def fp8_copy(layer, stream=None):
+    """``layer`` (plain bf16 weights) with 8-bit weights in plain layout."""
+    return _codes_copy(Fp8Layer, layer, stream)
+
+
+def int8_copy(layer, stream=None):
+    """``layer`` (plain bf16 weights) with int8 weights in plain layout."""
+    return _codes_copy(Int8Layer, layer, stream)
+
+
+def quant_rows(x, out=None, stream=None, dtype=_E4M3):
+    """Rows of bf16 values [rows][K] to ``Quantized``: with float8_e4m3fn one power of two
+    for each block of 128 along a row (``moe_quant_rows``), with int8 one scale for each
+    row (``moe_quant_rows_int8``)."""
+    _check_codes(dtype)
     _check_dev("x", x, _BF16)
     if x.dim() != 2:
         raise ValueError("x must be [rows][K], got %s" % (tuple(x.shape),))
     rows, K = x.shape
     dev = x.device
     if out is None:
-        out = Quantized(_empty((rows, K), _E4M3, dev, stream), _empty((rows, _blocks(K)), _U8, dev, stream))
-    q, s = _check_quantized("out", out, rows, K, dev)
+        out = _new_quantized(dtype, rows, K, dev, stream)
+    q, s = _check_quantized("out", out, dtype, rows, K, dev)
+    name = "moe_quant_rows" if dtype is _E4M3 else "moe_quant_rows_int8"
     with _guard(dev):
-        check("moe_quant_rows", lib().moe_quant_rows(x.data_ptr(), rows, _int(K), q, s, _on(dev, stream)))
+        check(name, getattr(lib(), name)(x.data_ptr(), rows, _int(K), q, s, _on(dev, stream)))
     return out
 
 
 def dequant_rows(v, out=None, stream=None):
-    """The bf16 values that ``Quantized`` rows stand for (``moe_dequant_rows``)."""
+    """The bf16 values that ``Quantized`` rows stand for (``moe_dequant_rows``,
+    ``moe_dequant_rows_int8``)."""
     if not isinstance(v, Quantized) or v.q.dim() != 2:
         raise TypeError("dequant_rows takes Quantized rows")
     rows, K = v.q.shape
-    dev = v.q.device
+    dev, codes = v.q.device, v.q.dtype
     _check_dev("v.q", v.q)
-    q, s = _check_quantized("v", v, rows, K, dev)
+    _check_codes(codes)
+    q, s = _check_quantized("v", v, codes, rows, K, dev)
     if out is None:
         out = _empty((rows, K), _BF16, dev, stream)
     x = _check("out", out, _BF16, (rows, K), dev)
+    name = "moe_dequant_rows" if codes is _E4M3 else "moe_dequant_rows_int8"
     with _guard(dev):
-        check("moe_dequant_rows", lib().moe_dequant_rows(q, s, rows, _int(K), x, _on(dev, stream)))
+        check(name, getattr(lib(), name)(q, s, rows, _int(K), x, _on(dev, stream)))
     return out
 
 
@@ -236,11 +300,12 @@ def group_slots(ids, N, out=None, ws=None, stream=None):
 
 
 def _kind(layer):
-    """(layer has 8-bit weights, its device); refuses what the grouped calls do not take."""
-    if isinstance(layer, Fp8Layer):
-        return True, layer.device
+    """(type of the layer's rows: bf16, or of its codes; its device); refuses what the
+    grouped calls do not take."""
+    if isinstance(layer, _CodesLayer):
+        return layer.codes, layer.device
     if not isinstance(layer, Layer):
-        raise TypeError("layer must be Layer or Fp8Layer, got %s" % type(layer).__name__)
+        raise TypeError("layer must be Layer, Fp8Layer or Int8Layer, got %s" % type(layer).__name__)
     if layer.dtype != _BF16:
         raise TypeError("grouped calls take bf16 or 8-bit weights, got %s" % layer.dtype)
     if layer.packed:
@@ -248,7 +313,7 @@ def _kind(layer):
     if layer.n_shared:
         raise ValueError("run the shared experts as a layer of their own with m = N and accumulate=True "
                          "(and the routed ones from without_shared())")
-    return False, layer.w_gate.device
+    return _BF16, layer.w_gate.device
 
 
 def grouped_workspace(layer, n):
@@ -269,31 +334,30 @@ def grouped_square(layer, n, mat):
 
 def grouped_gate_up(layer, x, grouping, out=None, ws=None, stream=None):
     """h [n*m][d_ff] in row order (``moe_grouped_gate_up``): bf16 from bf16 x [n][d], or
-    with 8-bit weights ``Quantized`` from ``Quantized`` x (``quant_rows``).  Rows from
-    offset[N] on are left as they were."""
-    fp8, dev = _kind(layer)
-    if isinstance(x, Quantized) != fp8:
-        raise TypeError("x must be %s for this layer" % ("Quantized (quant_rows)" if fp8 else "a bf16 tensor"))
-    n = (x.q if fp8 else x).shape[0]
+    with 8-bit weights ``Quantized`` from ``Quantized`` x (``quant_rows`` with the layer's
+    type of codes).  Rows from offset[N] on are left as they were."""
+    typ, dev = _kind(layer)
+    codes = typ is not _BF16
+    if isinstance(x, Quantized) != codes:
+        raise TypeError("x must be %s for this layer" % ("Quantized (quant_rows)" if codes else "a bf16 tensor"))
+    n = (x.q if codes else x).shape[0]
     S, d, f = n * layer.m, layer.d, layer.d_ff
     _, offset, slots, _, _ = _check_grouping(grouping, n, layer.m, layer.N, dev)
-    desc, L = layer.desc(), lib()
-    if fp8:
-        xs = _check_quantized("x", x, n, d, dev)
+    desc, name = layer.desc(), "moe_grouped_gate_up" + _SUFFIX[typ]
+    if codes:
+        xs = _check_quantized("x", x, typ, n, d, dev)
         if out is None:
-            out = Quantized(_empty((S, f), _E4M3, dev, stream), _empty((S, _blocks(f)), _U8, dev, stream))
-        hs = _check_quantized("out", out, S, f, dev)
-        name, call = "moe_grouped_gate_up_fp8", L.moe_grouped_gate_up_fp8
+            out = _new_quantized(typ, S, f, dev, stream)
+        hs = _check_quantized("out", out, typ, S, f, dev)
     else:
         xs = (_check("x", x, _BF16, (n, d), dev),)
         if out is None:
             out = _empty((S, f), _BF16, dev, stream)
         hs = (_check("out", out, _BF16, (S, f), dev),)
-        name, call = "moe_grouped_gate_up", L.moe_grouped_gate_up
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *xs, _int(n), offset, slots, *hs,
-                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check(name, getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(layer._weights), *xs, _int(n), offset, slots,
+                                         *hs, ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return out
 
 
@@ -308,40 +372,34 @@ def _check_y(layer, y, n, dev, accumulate, stream):
 def grouped_down(layer, h, ids, w, grouping, y=None, ws=None, accumulate=False, stream=None):
     """y [n][d] bf16: the down products of h's rows, summed over each token's slots with
     the routing weights w (``moe_grouped_down``); ``accumulate`` adds to y."""
-    fp8, dev = _kind(layer)
+    typ, dev = _kind(layer)
     n, m, f = ids.shape[0], layer.m, layer.d_ff
     idp, wp = _check("ids", ids, _I32, (n, m), dev), _check("w", w, _F32, (n, m), dev)
     _, offset, slots, _, _ = _check_grouping(grouping, n, m, layer.N, dev)
     y, yp = _check_y(layer, y, n, dev, accumulate, stream)
-    desc, L = layer.desc(accumulate), lib()
-    if fp8:
-        hs = _check_quantized("h", h, n * m, f, dev)
-        name, call = "moe_grouped_down_fp8", L.moe_grouped_down_fp8
-    else:
-        hs = (_check("h", h, _BF16, (n * m, f), dev),)
-        name, call = "moe_grouped_down", L.moe_grouped_down
+    desc, name = layer.desc(accumulate), "moe_grouped_down" + _SUFFIX[typ]
+    hs = (_check("h", h, _BF16, (n * m, f), dev),) if typ is _BF16 else _check_quantized("h", h, typ, n * m, f, dev)
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), *hs, idp, wp, _int(n), offset, slots, yp,
-                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check(name, getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(layer._weights), *hs, idp, wp, _int(n), offset, slots,
+                                         yp, ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return y
 
 
 def expert_grouped(layer, x, ids, w, y=None, ws=None, info=None, accumulate=False, stream=None):
     """A whole pass of any length: grouping, gate/up and down (``moe_expert_grouped``, or
-    ``moe_expert_grouped_fp8`` for an ``Fp8Layer``, which quantises x first).  x and y
+    ``moe_expert_grouped_fp8`` for an ``Fp8Layer`` and ``moe_expert_grouped_int8`` for an
+    ``Int8Layer``, which quantise x first).  x and y
     bf16 [n][d]; ids outside [0, N) add nothing; ``info`` int32 [3]: U, ids status, 0."""
-    fp8, dev = _kind(layer)
+    typ, dev = _kind(layer)
     n, m = x.shape[0], layer.m
     xp = _check("x", x, _BF16, (n, layer.d), dev)
     idp, wp = _check("ids", ids, _I32, (n, m), dev), _check("w", w, _F32, (n, m), dev)
     y, yp = _check_y(layer, y, n, dev, accumulate, stream)
     infop = None if info is None else _check("info", info, _I32, (3,), dev)
-    desc, L = layer.desc(accumulate), lib()
-    name, call = (("moe_expert_grouped_fp8", L.moe_expert_grouped_fp8) if fp8 else
-                  ("moe_expert_grouped", L.moe_expert_grouped))
+    desc, name = layer.desc(accumulate), "moe_expert_grouped" + _SUFFIX[typ]
     ws = _ws(ws, desc, n, dev, stream)
     with _guard(dev):
-        check(name, call(ctypes.byref(desc), ctypes.byref(layer._weights), xp, idp, wp, _int(n), yp, infop,
-                         ws.data_ptr(), ws.numel(), _on(dev, stream)))
+        check(name, getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(layer._weights), xp, idp, wp, _int(n), yp,
+                                         infop, ws.data_ptr(), ws.numel(), _on(dev, stream)))
     return y

@@ -146,6 +146,11 @@ class Layer:
         from .grouped import fp8_copy
         return fp8_copy(self, stream)
 
+    def int8_copy(self, stream=None):
+        """The same layer with int8 weights (``Int8Layer``), from plain bf16 weights."""
+        from .grouped import int8_copy
+        return int8_copy(self, stream)
+
 
 def pack_w_down(layer, w_down, out, stream=None):
     """Copy W_down [E][d][d_ff] (E experts: the layer's N, or its shared experts) into

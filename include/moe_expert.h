@@ -55,9 +55,10 @@ typedef enum {
     MOE_E_IDS = -5        /* an expert id out of [0, N), or repeated within a token */
 } moe_status;
 
-/* MOE_FP8 (e4m3 codes with a power of two for each block of 128): the grouped products
- * and moe_pack_tiled only; the calls on verification passes return MOE_E_DTYPE */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8 = 2 } moe_dtype;
+/* MOE_FP8 (e4m3 codes with a power of two for each block of 128) and MOE_INT8 (int8 codes with a
+ * scale for each row): the grouped products and moe_pack_tiled only; the calls on verification
+ * passes return MOE_E_DTYPE.  3 is no type. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8 = 2, MOE_INT8 = 4 } moe_dtype;
 
 enum { MOE_KIND_SLOT = 0, MOE_KIND_DEDUP = 1 };
 
@@ -323,7 +324,7 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  *
  * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=
  * MOE_MAX_GROUP_SLOTS, d_model and d_ff <= MOE_MAX_GROUP_WIDTH, multiples of 8 (bf16)
- * or 16 (MOE_FP8).  Descriptor flags: MOE_FLAG_TILED (whole 64-byte steps) and
+ * or 16 (MOE_FP8, MOE_INT8).  Descriptor flags: MOE_FLAG_TILED (whole 64-byte steps) and
  * MOE_FLAG_ACCUMULATE (y = round(y + sum)); n_shared must be 0: always-on experts run
  * as a layer of their own with m = N, every weight 1 and MOE_FLAG_ACCUMULATE.  fp32
  * layers get MOE_E_DTYPE.  Matrices, x, h, q and y are 16-byte aligned, other arrays aligned to their
@@ -376,6 +377,38 @@ typedef struct {
     const uint8_t* s_down; /* [N][ceil(d_model/128)][ceil(d_ff/128)] */
 } moe_fp8_weights;
 
+/*
+ * 8-bit integers.  A row of K values (a token's activations, a row of h, or one output channel of a
+ * matrix) shares a scale: with a = max|v| it is s = a / 127 in fp32, and the code of v is 127 v / a
+ * rounded to the nearest integer, ties to even, without any other rounding; it stands for code * s.  A row
+ * of zeros has s = 0.  A row that holds a value that is not finite has s = NaN and codes 0: all of it
+ * stands for NaN.  (Below a = 2^-119 s is subnormal and has fewer bits.)
+ *   moe_quant_rows_int8    x bf16 [rows][K] -> q int8 [rows][K], scale [rows] (for a matrix
+ *                          [N][R][K]: rows = N R, a weight-load-time step)
+ *   moe_dequant_rows_int8  bf16(code * s) [rows][K]
+ * K is a multiple of 16, at most MOE_MAX_GROUP_WIDTH, else MOE_E_DTYPE / MOE_E_INVAL;
+ * 1 <= rows <= MOE_MAX_QUANT_ROWS.  q and x 16-byte aligned.  One launch each.  moe_pack_tiled tiles codes with
+ * desc->dtype MOE_INT8 as those of MOE_FP8; scales keep their layout.
+ *
+ * The products add the codes' products in int32, exactly; a sum times the token's scale, times the
+ * channel's, is the fp32 value that the bf16 and e4m3 products have at that place.  h is rounded to
+ * bf16 and then quantised by row.
+ */
+#define MOE_MAX_QUANT_ROWS (1 << 26)
+int moe_quant_rows_int8(const void* x, int64_t rows, int32_t K, void* q, float* scale, void* hip_stream);
+int moe_dequant_rows_int8(const void* q, const float* scale, int64_t rows, int32_t K, void* x, void* hip_stream);
+
+/* Codes (plain or tiled) and scales of a layer's matrices, as moe_quant_rows_int8 gives them;
+ * device, caller-owned. */
+typedef struct {
+    const void* w_gate; /* [N][d_ff][d_model] */
+    const void* w_up;
+    const void* w_down; /* [N][d_model][d_ff] */
+    const float* s_gate; /* [N][d_ff] */
+    const float* s_up;
+    const float* s_down; /* [N][d_model] */
+} moe_int8_weights;
+
 /* Workspace bytes of the calls below for n tokens (0 for invalid arguments); it grows
  * with n, so a workspace for n serves fewer tokens too.  256-byte aligned; no zero-fill
  * needed, nothing kept between calls; calls that share one must not overlap in time.  The
@@ -389,8 +422,8 @@ int moe_grouped_square(const moe_layer_desc* desc, int32_t n, int32_t mat);
 /*
  * The two products by themselves.  offset and slot_by_expert come from moe_group_slots
  * (or moe_route_group) for the same n, m and N.  The other product's weights may be NULL.
- *   x    device [n][d_model] bf16, or codes with x_scale [n][ceil(d_model/128)]
- *   h    device [n*m][d_ff] bf16, or codes with h_scale [n*m][ceil(d_ff/128)], in row order
+ *   x    device [n][d_model] bf16, or codes with x_scale [n][ceil(d_model/128)] (int8: [n])
+ *   h    device [n*m][d_ff] bf16, or codes with h_scale [n*m][ceil(d_ff/128)] (int8: [n*m]), in row order
  *   y    device [n][d_model] bf16
  * Return MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE (nothing enqueued) or
  * MOE_E_HIP.
@@ -408,9 +441,16 @@ int moe_grouped_down_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weig
                          const uint8_t* h_scale, const int32_t* ids, const float* w, int32_t n, const int32_t* offset,
                          const int32_t* slot_by_expert, void* y, void* ws, size_t ws_bytes, void* hip_stream);
 
+int moe_grouped_gate_up_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* xq,
+                             const float* x_scale, int32_t n, const int32_t* offset, const int32_t* slot_by_expert,
+                             void* hq, float* h_scale, void* ws, size_t ws_bytes, void* hip_stream);
+int moe_grouped_down_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* hq,
+                          const float* h_scale, const int32_t* ids, const float* w, int32_t n, const int32_t* offset,
+                          const int32_t* slot_by_expert, void* y, void* ws, size_t ws_bytes, void* hip_stream);
+
 /*
- * moe_expert_grouped / moe_expert_grouped_fp8 -- a whole pass: grouping, (x quantised in
- * blocks of 128,) gate/up, down.  Arguments as for moe_expert_dedup, with x and y bf16
+ * moe_expert_grouped / moe_expert_grouped_fp8 / moe_expert_grouped_int8 -- a whole pass: grouping, (x
+ * quantised in blocks of 128, or by row,) gate/up, down.  Arguments as for moe_expert_dedup, with x and y bf16
  * (also with 8-bit weights).  info device [3] int32 or NULL: U, ids status, MOE_OK.
  */
 int moe_expert_grouped(const moe_layer_desc* desc, const moe_layer_weights* weights, const void* x, const int32_t* ids,
@@ -419,6 +459,9 @@ int moe_expert_grouped(const moe_layer_desc* desc, const moe_layer_weights* weig
 int moe_expert_grouped_fp8(const moe_layer_desc* desc, const moe_fp8_weights* weights, const void* x,
                            const int32_t* ids, const float* w, int32_t n, void* y, int32_t* info, void* ws,
                            size_t ws_bytes, void* hip_stream);
+int moe_expert_grouped_int8(const moe_layer_desc* desc, const moe_int8_weights* weights, const void* x,
+                            const int32_t* ids, const float* w, int32_t n, void* y, int32_t* info, void* ws,
+                            size_t ws_bytes, void* hip_stream);
 
 /* Number of kernel launches moe_expert_perslot / moe_expert_dedup enqueue per
  * call (moe_route_group is a separate, optional launch), or a negative status for
