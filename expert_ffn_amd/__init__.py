@@ -17,3 +17,4 @@ from .grouped import (  # noqa: F401
     Fp8Layer, Int8Layer, Quantized, dequant_rows, expert_grouped, group_slots, group_workspace, grouped_down, grouped_gate_up,
     grouped_square, quant_rows, quant_weights,
 )
+from .layer import Router, layer_pass, pass_workspace  # noqa: F401

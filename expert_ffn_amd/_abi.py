@@ -18,6 +18,7 @@ MOE_FLAG_ACCUMULATE = 1
 MOE_FLAG_WDOWN_PACKED = 2
 MOE_FLAG_TILED = 4
 MOE_MAT_GATE_UP, MOE_MAT_DOWN = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_STEP_NMAX, MOE_STEP_AMAX = 16, 64
 MOE_SCRATCH_BYTES = 16 << 20
 MOE_MAX_GROUP_SLOTS, MOE_MAX_GROUP_WIDTH = 1 << 22, 1 << 16
@@ -35,7 +36,8 @@ EXPORTS = ("moe_route_group", "moe_workspace_bytes", "moe_expert_perslot", "moe_
            "moe_quant_weights", "moe_grouped_workspace_bytes", "moe_grouped_gate_up",
            "moe_grouped_gate_up_fp8", "moe_grouped_down", "moe_grouped_down_fp8", "moe_expert_grouped",
            "moe_expert_grouped_fp8", "moe_grouped_square", "moe_quant_rows_int8", "moe_dequant_rows_int8",
-           "moe_grouped_gate_up_int8", "moe_grouped_down_int8", "moe_expert_grouped_int8")
+           "moe_grouped_gate_up_int8", "moe_grouped_down_int8", "moe_expert_grouped_int8",
+           "moe_pass_workspace_bytes", "moe_layer_pass")
 
 
 class MoeError(RuntimeError):
@@ -59,6 +61,11 @@ class LayerWeights(ctypes.Structure):
 class Fp8Weights(ctypes.Structure):
     _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
+
+
+class RouterDesc(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class Int8Weights(ctypes.Structure):
@@ -168,6 +175,10 @@ def lib():
             L.moe_grouped_down_fp8.argtypes = [pdesc, pw8, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
             L.moe_expert_grouped.argtypes = [pdesc, pw, vp, vp, vp, i32, vp, vp, vp, sz, vp]
             L.moe_expert_grouped_fp8.argtypes = [pdesc, pw8, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+            L.moe_pass_workspace_bytes.argtypes = [pdesc, i32]
+            L.moe_pass_workspace_bytes.restype = sz
+            L.moe_layer_pass.argtypes = [pdesc, pw, ctypes.POINTER(RouterDesc), vp, i32, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_layer_pass.restype = ctypes.c_int
             pwi = ctypes.POINTER(Int8Weights)
             L.moe_quant_rows_int8.argtypes = [vp, i64, i32, vp, vp, vp]
             L.moe_dequant_rows_int8.argtypes = [vp, vp, i64, i32, vp, vp]

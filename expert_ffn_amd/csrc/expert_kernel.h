@@ -246,7 +246,7 @@ struct Args {
     const char* x;       // [n][d]
     const int32_t* ids;  // [n*m]
     const float* w;      // [n*m]
-    float* y;            // [n][d]
+    char* y;             // [n][d], fp32, or bf16 (y16)
     char* h;             // bf16: hi [nslot][d_ff] then lo [nslot][d_ff]; fp32: [nslot][d_ff]
     float* O;            // [nslot][ks][d]: per slot and contraction part
     int32_t* sync;       // counters, see layout above
@@ -258,6 +258,7 @@ struct Args {
     int32_t n_shared;
     int32_t nslot;       // rows of h and O: routed slots t*m + j, then shared slots nm + s*n + t
     int32_t accumulate;
+    int32_t y16;
     int32_t gl;          // down items in register mode: tokens of h staged in LDS at a time
     int32_t g1;          // gate/up work groups (they take the first g1 block ids)
     int32_t S1;          // K steps of one gate/up row tile
@@ -974,9 +975,20 @@ __device__ __forceinline__ void down_work(const Args& a, Smem<NT * RB>& sm, int&
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[r] = fmaf(wv[jj], __uint_as_float(ov[jj][r]), acc[r]);
             }
-            f32x4* yp = reinterpret_cast<f32x4*>(a.y + (size_t)tok * a.d + i);
-            if (a.accumulate) acc += *yp;  // y is read only when the call accumulates
-            *yp = acc;
+            const size_t at = (size_t)tok * a.d + i;
+            if (a.y16) {
+                u32x2* yp = reinterpret_cast<u32x2*>(a.y + at * 2);
+                if (a.accumulate) {
+                    const u32x2 v = *yp;
+                    acc += f32x4{bf16_to_f32(v.x & 0xffffu), bf16_to_f32(v.x >> 16), bf16_to_f32(v.y & 0xffffu),
+                                 bf16_to_f32(v.y >> 16)};
+                }
+                *yp = u32x2{bf16_rne(acc[0]) | (bf16_rne(acc[1]) << 16), bf16_rne(acc[2]) | (bf16_rne(acc[3]) << 16)};
+            } else {
+                f32x4* yp = reinterpret_cast<f32x4*>(a.y + at * 4);
+                if (a.accumulate) acc += *yp;  // y is read only when the call accumulates
+                *yp = acc;
+            }
         }
     }
 }

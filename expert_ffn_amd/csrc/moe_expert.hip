@@ -12,6 +12,7 @@
 
 #include "expert_kernel.h"
 #include "moe_expert.h"
+#include "route_kernel.h"
 
 // Workspace of moe_expert_auto_noalloc: one copy per GPU, in the code object's
 // device memory.  In host code `scratch` names a host-side stand-in, not the
@@ -537,8 +538,8 @@ __global__ __launch_bounds__(256) void k_zero_words(int32_t* __restrict__ p, int
 
 template <int MODE>
 int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* x, const int32_t* ids,
-               const float* w, int32_t n, float* y, int32_t* info, void* ws, size_t ws_bytes, void* stream,
-               void* const* events, int32_t n_events, bool clear_counters = false) {
+               const float* w, int32_t n, void* y, int32_t* info, void* ws, size_t ws_bytes, void* stream,
+               void* const* events, int32_t n_events, bool clear_counters = false, bool y16 = false) {
     int rc = check_desc(d, n);
     if (rc != MOE_OK) return rc;
     if (!W || !W->w_gate || !W->w_up || !W->w_down || !x || !ids || !w || !y || !ws) return MOE_E_INVAL;
@@ -568,7 +569,8 @@ int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* 
     args.x = reinterpret_cast<const char*>(x);
     args.ids = ids;
     args.w = w;
-    args.y = y;
+    args.y = reinterpret_cast<char*>(y);
+    args.y16 = y16 ? 1 : 0;
     args.h = wsb + p.h_off;
     args.O = reinterpret_cast<float*>(wsb + p.o_off);
     args.sync = reinterpret_cast<int32_t*>(wsb + p.sync_off);
@@ -656,6 +658,41 @@ int router_check(const moe_layer_desc* desc, int32_t n) {
     if ((int64_t)desc->N * desc->d_model * es > (1ll << 31) - 4096) return MOE_E_INVAL;
     return MOE_OK;
 }
+
+// ---------------------------------------------------------------------------
+// moe_layer_pass
+// ---------------------------------------------------------------------------
+// parts of the contraction: a step a wave, at most kRouteParts and about a work group a compute unit for 16
+// tokens; of N, d and the type alone (see route_kernel.h)
+int route_parts(const moe_layer_desc* d) {
+    const int step = d->dtype == MOE_BF16 ? 32 : 16, steps = (d->d_model + step - 1) / step;
+    const int most = std::min(kRouteParts, std::max(1, kCUs / ((d->N + kTile - 1) / kTile)));
+    return std::max(1, std::min(most, steps / kRouteWaves));
+}
+
+int layer_check(const moe_layer_desc* d, int32_t n) {
+    const int rc = check_desc(d, n);
+    return rc != MOE_OK ? rc : router_check(d, n);
+}
+
+// Workspace of a pass: the router's counters and the experts' workspace first, whose counters are then at
+// the same place for every n.
+struct LayerSpace {
+    size_t expert, part, ids, w, total;
+};
+LayerSpace layer_space(const moe_layer_desc* d, int32_t n, size_t expert_bytes) {
+    LayerSpace p;
+    p.expert = align_up((size_t)(MOE_MAX_TOKENS / kTile) * kLine * 4);
+    p.part = p.expert + align_up(expert_bytes);
+    p.ids = p.part + align_up((size_t)route_parts(d) * n * d->N * 4);
+    p.w = p.ids + align_up((size_t)n * d->m * 4);
+    p.total = p.w + align_up((size_t)n * d->m * 4);
+    return p;
+}
+
+// Passes from this many tokens on run the deduplicating kernel.
+constexpr int kLayerDedup = 3;
+int layer_kind(int32_t n) { return n >= kLayerDedup ? MOE_KIND_DEDUP : MOE_KIND_SLOT; }
 
 }  // namespace
 
@@ -836,6 +873,67 @@ int moe_expert_dedup_ev(const moe_layer_desc* desc, const moe_layer_weights* wei
                         size_t ws_bytes, void* hip_stream, void* const* events, int32_t n_events) {
     if (!events) return MOE_E_INVAL;
     return run_expert<kDedup>(desc, weights, x, ids, w, n, y, info, ws, ws_bytes, hip_stream, events, n_events);
+}
+
+size_t moe_pass_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
+    if (layer_check(desc, n) != MOE_OK) return 0;
+    size_t total = 0;  // largest over 1..n tokens
+    for (int32_t k = 1; k <= n; ++k)
+        total = std::max(total, layer_space(desc, k, plan_for(desc, k, layer_kind(k)).total).total);
+    return total;
+}
+
+int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights, const moe_router* router, const void* x,
+                   int32_t n, void* y, int32_t* ids, float* w, int32_t* info, void* ws, size_t ws_bytes,
+                   void* hip_stream) {
+    int rc = layer_check(desc, n);
+    if (rc != MOE_OK) return rc;
+    if (!weights || !weights->w_gate || !weights->w_up || !weights->w_down || !router || !router->w || !x || !y || !ws)
+        return MOE_E_INVAL;
+    if (!aligned16(weights->w_gate) || !aligned16(weights->w_up) || !aligned16(weights->w_down) || !aligned16(router->w) ||
+        !aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) ||
+        ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(info) |
+          reinterpret_cast<uintptr_t>(router->bias)) & 3u))
+        return MOE_E_INVAL;
+    if (desc->n_shared > 0 && (!weights->w_gate_shared || !weights->w_up_shared || !weights->w_down_shared ||
+                               !aligned16(weights->w_gate_shared) || !aligned16(weights->w_up_shared) ||
+                               !aligned16(weights->w_down_shared)))
+        return MOE_E_INVAL;
+    if (router->score != MOE_SCORE_SOFTMAX && router->score != MOE_SCORE_SIGMOID) return MOE_E_INVAL;
+    const int kind = layer_kind(n);
+    const size_t expert_bytes = plan_for(desc, n, kind).total;
+    const LayerSpace p = layer_space(desc, n, expert_bytes);
+    if (ws_bytes < p.total) return MOE_E_WORKSPACE;
+    char* b = reinterpret_cast<char*>(ws);
+    RouteArgs a;
+    a.wr = reinterpret_cast<const char*>(router->w);
+    a.x = reinterpret_cast<const char*>(x);
+    a.bias = router->bias;
+    a.part = reinterpret_cast<float*>(b + p.part);
+    a.count = reinterpret_cast<int32_t*>(b);
+    a.ids = ids ? ids : reinterpret_cast<int32_t*>(b + p.ids);
+    a.w = w ? w : reinterpret_cast<float*>(b + p.w);
+    a.N = desc->N;
+    a.n = n;
+    a.m = desc->m;
+    a.d = desc->d_model;
+    a.KS = route_parts(desc);
+    a.sigmoid = router->score == MOE_SCORE_SIGMOID;
+    a.renorm = router->renorm != 0;
+    a.scale = router->scale;
+    const bool bf = desc->dtype == MOE_BF16;
+    const dim3 grid((desc->N + kTile - 1) / kTile, (n + kTile - 1) / kTile, a.KS);
+    hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+    (void)hipGetLastError();
+    const auto route = desc->N <= 128   ? (bf ? k_route<true, 2> : k_route<false, 2>)
+                       : desc->N <= 256 ? (bf ? k_route<true, 4> : k_route<false, 4>)
+                                        : (bf ? k_route<true, 16> : k_route<false, 16>);
+    hipLaunchKernelGGL(route, grid, dim3(kRouteThreads), 0, st, a);
+    if (hipGetLastError() != hipSuccess) return MOE_E_HIP;
+    return kind == MOE_KIND_DEDUP ? run_expert<kDedup>(desc, weights, x, a.ids, a.w, n, y, info, b + p.expert, expert_bytes,
+                                                       hip_stream, nullptr, 0, false, bf)
+                                  : run_expert<kPerSlot>(desc, weights, x, a.ids, a.w, n, y, info, b + p.expert,
+                                                         expert_bytes, hip_stream, nullptr, 0, false, bf);
 }
 
 }  // extern "C"

@@ -1,0 +1,225 @@
+// The router of a whole-layer pass in one launch: logits, selection and weights.
+//
+//   l_te = W_r[e] . x_t,   s_te = exp(l_te) / sum_e exp(l_te)  or  1 / (1 + exp(-l_te))
+//   selected: the m largest s_te + b_e (without b: l_te, which orders them alike), equal ones: lower id
+//   w_tj = scale * s_tj / (renorm ? sum over the selected : 1)
+//
+// One work group of 16 waves for 16 experts x 16 tokens x one of KS parts of the contraction; its waves split
+// the part, so that at d = 2048 in bf16 each has one step: one round of loads.  The parts go to memory, and the work
+// group that arrives last on a token tile adds them, in order, and selects: a wave a token, m rounds of a wave-wide
+// maximum.  How the contraction is cut depends on N, d and the type alone, so a token's routing does
+// not depend on the pass that it is in.
+#pragma once
+
+#include "expert_kernel.h"
+
+namespace moe_k {
+
+constexpr int kRouteWaves = 16, kRouteThreads = 64 * kRouteWaves;
+constexpr int kRouteParts = 8;  // most parts of the contraction
+static_assert(kRouteWaves == kTile, "a wave a token of the tile");
+
+struct RouteArgs {
+    const char* wr;     // [N][d]
+    const char* x;      // [n][d]
+    const float* bias;  // [N] or null
+    float* part;        // [KS][n][N]
+    int32_t* count;     // [token tiles][kLine], zero
+    int32_t* ids;       // [n][m]
+    float* w;
+    int32_t N, n, m, d, KS;
+    int32_t sigmoid, renorm;
+    float scale;
+};
+
+// The order of the values as unsigned numbers, NaN (which is never selected) below all.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+    return v == v ? ((int)b < 0 ? ~b : b | 0x80000000u) : 0u;
+}
+
+// The wave's largest, in every lane: rows of 16 by shifts, then across the rows.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOE_DPP_MAX(ctrl, rows) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, ctrl, rows, 0xf, false))
+    MOE_DPP_MAX(0x111, 0xf);  // row_shr:1
+    MOE_DPP_MAX(0x112, 0xf);
+    MOE_DPP_MAX(0x114, 0xf);
+    MOE_DPP_MAX(0x118, 0xf);
+    MOE_DPP_MAX(0x142, 0xa);  // row_bcast:15
+    MOE_DPP_MAX(0x143, 0xc);  // row_bcast:31
+#undef MOE_DPP_MAX
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {  // a fixed tree; lane 0's for all
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
+
+// Sigmoid times exp(-c), c <= 0: with c the largest of the selected logits, or 0, the quotients of
+// weights stay where all sigmoids are too small for fp32.
+__device__ __forceinline__ float sigmoid_from(float l, float c) {
+    return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - c) / (1.f + expf(l));
+}
+
+// CL: experts a lane holds, lane + 64 j
+template <bool BF16, int CL>
+__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
+    using F = Fmt<BF16>;
+    __shared__ f32x4 red[kRouteWaves][64];
+    __shared__ int sel_e[kRouteWaves][MOE_MAX_SLOTS];
+    __shared__ float sel_l[kRouteWaves][MOE_MAX_SLOTS];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int lr = lane & 15, q = lane >> 4;
+    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile, ks = blockIdx.z, KS = a.KS;
+    const int S = (a.d + F::kStep - 1) / F::kStep;
+    const int kb = ks * S / KS, kl = (ks + 1) * S / KS - kb;  // this part's steps
+    const int s0 = kb + wave * kl / kRouteWaves, s1 = kb + (wave + 1) * kl / kRouteWaves;
+    const auto rw = rsrc(a.wr, (uint32_t)a.N * a.d * F::kEsize);
+    const auto rx = rsrc(a.x, (uint32_t)a.n * a.d * F::kEsize);
+    const uint32_t la = e0 + lr < a.N ? (uint32_t)(e0 + lr) * a.d * F::kEsize : kOOB;
+    const uint32_t lb = t0 + lr < a.n ? (uint32_t)(t0 + lr) * a.d * F::kEsize : kOOB;
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kAhead = 4;
+    for (int s = s0; s < s1; s += kAhead) {
+        u32x4 wv[kAhead], xv[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = (s + j) * F::kStep + q * F::kPer;
+            const bool ok = s + j < s1 && k < a.d;  // (d % 8 == 0: whole chunks)
+            wv[j] = bload(rw, ok ? cat(la, (uint32_t)k * F::kEsize) : kOOB);
+            xv[j] = bload(rx, ok ? cat(lb, (uint32_t)k * F::kEsize) : kOOB);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) acc = F::mma(wv[j], xv[j], acc);
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    const auto rp = rsrc(a.part, (uint32_t)KS * a.n * a.N * 4);
+    if (wave == 0) {
+        f32x4 v = red[0][lane];
+#pragma unroll
+        for (int w = 1; w < kRouteWaves; ++w) v += red[w][lane];
+        // experts e0 + 4 q + i of token t0 + lr
+        const int t = t0 + lr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + 4 * q + i;
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), rp,
+                                                  e < a.N && t < a.n ? (((uint32_t)ks * a.n + t) * a.N + e) * 4u : kOOB, 0,
+                                                  kSc1);
+        }
+        stores_complete();
+        if (lane == 0) {
+            int32_t* count = a.count + kLine * blockIdx.y;
+            s_last = atomicAdd(count, 1) == (int)(gridDim.x * gridDim.z) - 1;
+            if (s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // all have arrived
+        }
+    }
+    __syncthreads();  // the loads (sc1) below go out after the last arrival was seen
+    const int t = t0 + wave;
+    if (!s_last || t >= a.n) return;  // (no barrier below)
+
+    float l[CL];
+    {
+        uint32_t pv[CL][kRouteParts];
+#pragma unroll
+        for (int j = 0; j < CL; ++j)
+#pragma unroll
+            for (int k = 0; k < kRouteParts; ++k) {
+                const int e = lane + 64 * j;
+                pv[j][k] = __builtin_amdgcn_raw_buffer_load_b32(
+                    rp, k < KS && e < a.N ? (((uint32_t)k * a.n + t) * a.N + e) * 4u : kOOB, 0, kSc1);
+            }
+#pragma unroll
+        for (int j = 0; j < CL; ++j) {
+            l[j] = __uint_as_float(pv[j][0]);
+#pragma unroll
+            for (int k = 1; k < kRouteParts; ++k) l[j] += __uint_as_float(pv[j][k]);  // (parts past KS: 0)
+        }
+    }
+    uint32_t key[CL];
+    float top = -INFINITY, Z = 1.f;  // the largest logit; sum of exp(l - top)
+#pragma unroll
+    for (int j = 0; j < CL; ++j) {
+        key[j] = lane + 64 * j < a.N ? order_of(l[j]) : 0u;
+        if (key[j]) top = fmaxf(top, l[j]);
+    }
+    if (!a.sigmoid && (a.bias || !a.renorm)) {
+        const uint32_t k = wave_max(order_of(top));
+        top = __uint_as_float((int)k < 0 ? k & 0x7fffffffu : ~k);
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < CL; ++j)
+            if (key[j]) z += expf(l[j] - top);
+        Z = wave_sum(z);
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < CL; ++j)
+            if (key[j]) {
+                const float s = a.sigmoid ? 1.f / (1.f + expf(-l[j])) : expf(l[j] - top) / Z;
+                key[j] = order_of(s + a.bias[lane + 64 * j]);
+            }
+    }
+    // rounds: the wave's largest key, of equal ones the lowest expert
+    int* se = sel_e[wave];
+    float* sl = sel_l[wave];
+    for (int r = 0; r < a.m; ++r) {
+        uint32_t best = key[0];
+        int bj = 0;
+        float bl = l[0];
+#pragma unroll
+        for (int j = 1; j < CL; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                bj = j;
+                bl = l[j];
+            }
+        const uint32_t most = wave_max(best);
+        int e = -1;
+        float v = 0.f;
+        if (most) {  // (0: nothing is left)
+            uint64_t who = __ballot(best == most);
+            if (who & (who - 1)) {  // several: the lowest 64 j + lane
+                const uint32_t least = wave_max(best == most ? ~(uint32_t)(bj * 64 + lane) : 0u);
+                who = 1ull << (~least & 63u);
+            }
+            const int at = __ffsll((unsigned long long)who) - 1;
+            const int j = __builtin_amdgcn_readlane(bj, at);
+            v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bl), at));
+            e = 64 * j + at;
+#pragma unroll
+            for (int i = 0; i < CL; ++i)
+                if (i == j && lane == at) key[i] = 0u;
+        }
+        if (lane == 0) {
+            se[r] = e;
+            sl[r] = v;
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // weights: s_j over their sum, or over Z; the first selected is the largest only without a bias
+    float c = -INFINITY;
+    for (int j = lane; j < a.m; j += 64)
+        if (se[j] >= 0) c = fmaxf(c, sl[j]);
+    const uint32_t ck = wave_max(order_of(c));
+    c = __uint_as_float((int)ck < 0 ? ck & 0x7fffffffu : ~ck);
+    if (a.sigmoid) c = a.renorm ? fminf(c, 0.f) : 0.f;
+    else if (!a.renorm) c = top;
+    auto value = [&](int j) { return se[j] < 0 ? 0.f : a.sigmoid ? sigmoid_from(sl[j], c) : expf(sl[j] - c); };
+    if (a.renorm) {
+        float z = 0.f;
+        for (int j = lane; j < a.m; j += 64) z += value(j);
+        Z = wave_sum(z);
+    }
+    for (int j = lane; j < a.m; j += 64) {
+        a.ids[(size_t)t * a.m + j] = se[j];
+        a.w[(size_t)t * a.m + j] = se[j] < 0 ? 0.f : value(j) / Z * a.scale;
+    }
+}
+
+}  // namespace moe_k

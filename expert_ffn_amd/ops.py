@@ -141,6 +141,11 @@ class Layer:
         from .grouped import grouped_workspace
         return grouped_workspace(self, n)
 
+    def pass_workspace(self, n):
+        """Zero-filled workspace of ``layer_pass`` for passes of up to n tokens."""
+        from .layer import pass_workspace
+        return pass_workspace(self, n)
+
     def fp8_copy(self, stream=None):
         """The same layer with 8-bit weights (``Fp8Layer``), from plain bf16 weights."""
         from .grouped import fp8_copy

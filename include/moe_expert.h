@@ -298,6 +298,42 @@ int moe_router_topk(const moe_layer_desc* desc, const void* w_router, const void
  * 1..n), or 0 for invalid arguments. */
 size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
 
+/*
+ * moe_layer_pass -- a whole MoE layer on the tokens of a verification pass: router, selection, the routed
+ * experts and the always-on ones, in two kernel launches.  For every token t
+ *   l_te = W_r[e] . x_t                      (fp32 accumulation)
+ *   s_te = exp(l_te) / sum_e exp(l_te)       (MOE_SCORE_SOFTMAX)   or
+ *          1 / (1 + exp(-l_te))              (MOE_SCORE_SIGMOID)
+ *   the m experts with the largest s_te + b_e, in descending order, equal ones: lower id
+ *   first (without b the order is that of l_te)
+ *   w_tj = scale * s_tj / (renorm ? sum_j s_tj : 1)
+ *   y_t  = sum_j w_tj FFN_tj(x_t) + sum over the shared experts of FFN(x_t)
+ * with the expert calls' FFN and order of the sums: y is what moe_expert_dedup gives for the ids and weights
+ * that the call hands back, rounded once more where the layer is bf16.  A token's ids and weights do not
+ * depend on the other tokens of the pass.
+ *   desc     as for the expert calls (fp32 or bf16; every weight layout; n_shared; accumulate: y = round(y + result));
+ *            N * d_model * element size < 2^31
+ *   x, y     device [n][d_model], both of desc's type
+ *   ids, w   device [n][m] int32 / fp32, written; either may be NULL
+ *   info     device [3] int32 or NULL, as for moe_expert_perslot
+ *   ws       device workspace of at least moe_pass_workspace_bytes(desc, n), 256-byte aligned, zero-filled before
+ *            first use, as for the expert calls; one sized for n serves fewer tokens too
+ * A logit that is NaN takes no part: its expert is never selected, and not in the softmax's sum; a slot left
+ * without a candidate gets id -1 and weight 0 (info[1] is then MOE_E_IDS).
+ * Returns MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE (nothing enqueued), or MOE_E_HIP.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+    const void* w;     /* device W_r [N][d_model], dtype of the layer, 16-byte aligned */
+    const float* bias; /* device [N], added to the scores for the selection alone; or NULL */
+    int32_t score;     /* MOE_SCORE_* */
+    int32_t renorm;    /* not 0: the selected experts' weights are divided by their sum */
+    float scale;       /* factor of the weights */
+} moe_router;
+size_t moe_pass_workspace_bytes(const moe_layer_desc* desc, int32_t n);
+int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights, const moe_router* router, const void* x,
+                   int32_t n, void* y, int32_t* ids, float* w, int32_t* info, void* ws, size_t ws_bytes, void* hip_stream);
+
 /* ---------------------------------------------------------------------------
  * The expert operation on grouped rows: the same layers on passes of any length (a
  * prompt, a padded batch, one token), in bf16 or with 8-bit weights and activations.
