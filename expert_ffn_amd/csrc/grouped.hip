@@ -83,8 +83,7 @@ void run_group(Group g, hipStream_t st) {
 // units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
 // tile has beyond it); thin tiles address all of memory.
 bool square(const Args& a, int type, bool gu) {
-    const bool fp8 = type == kFp8;
-    if (type == kInt8) return false;
+    const bool fp8 = type != kBf16;
     const int64_t kby = (int64_t)a.K * elem_size(type), most = (1ll << 31) - 4096;
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
     return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? (fp8 ? 12 : 8) : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
@@ -159,7 +158,6 @@ void before_down(const moe_layer_desc* d, int n, const int32_t* sbe, const int32
 
 template <int T, bool GU>
 void launch_product(const Args& a, bool tiled, hipStream_t st) {
-    if constexpr (T != kInt8) {
     if (square(a, T, GU)) {
         const int64_t tiles = (int64_t)a.S / kTM + std::min(a.N, a.S), tc = GU ? kTN / 2 : kTN;
         const int grid = (int)std::min<int64_t>(kCUs, (tiles * ((a.R + tc - 1) / tc) + 7) / 8 * 8);
@@ -168,7 +166,6 @@ void launch_product(const Args& a, bool tiled, hipStream_t st) {
         else
             hipLaunchKernelGGL((k_tile<T, false, GU>), dim3(grid), dim3(kTileThreads), 0, st, a);
         return;
-    }
     }
     // A launch holds 2^32 threads at most: as many row tiles at once as keep below that.
     const int64_t cols = (a.R + 15) / 16, units = ((int64_t)a.K * elem_size(T) + kUnit - 1) / kUnit;

@@ -979,7 +979,10 @@ constexpr int kMaxKB = MOE_MAX_GROUP_WIDTH / kBlk;
 
 struct TileLds {
     char stage[2][kStage];  // rows, then weight rows
-    uint8_t xs[2][4][kTM];  // e4m3: scale bytes of four units' rows, [wm][row % 16][i]
+    union {
+        uint8_t xs[2][4][kTM];  // e4m3: scale bytes of four units' rows, [wm][row % 16][i]
+        float scale[2][kTM];    // int8: scales of a tile's rows and weight rows (gate/up: 128 of each matrix)
+    };
     uint32_t red[4][kTM];   // e4m3 gate/up: |h| maxima (their bits) of a row's four column groups
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
     uint8_t ws[2][2][kMaxKB];  // e4m3: a tile's weight scale bytes: of both matrices, or of 128 rows each
@@ -990,8 +993,8 @@ struct TileLds {
 
 template <int T, bool TILED, bool GU>
 __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
-    constexpr bool FP8 = T == kFp8;
-    constexpr int ES = elem_size(T);
+    constexpr bool FP8 = T == kFp8, I8 = T == kInt8;
+    constexpr int ES = elem_size(T), HS = FP8 ? 1 : 2;  // bytes of an operand's element, of h's in gate/up's output
     __shared__ TileLds lds;
     // The arguments that are needed now and then are loaded again each time: kept, they would
     // push others out of the scalar registers.
@@ -1123,6 +1126,16 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     auto keep_weight_scale = [&](int par, int i, uint8_t v) {
         if (i < 2 * KB) lds.ws[par][i >= KB][i >= KB ? i - KB : i] = v;
     };
+    // int8: a scale a thread, those of the tile's rows, then of its weight rows.  (At a tile's first unit
+    // lds.token still has its own tokens.)
+    auto tile_scale = [&](const Place& t) {
+        const int c = tid & (kTM - 1), half = GU ? c >> 7 : 0;
+        const float* rows = reinterpret_cast<const float*>(arg()->xs);
+        const float *s0 = reinterpret_cast<const float*>(arg()->s0), *s1 = GU ? reinterpret_cast<const float*>(arg()->s1) : s0;
+        const float* at = tid < kTM ? rows + (GU ? lds.token[c] : row_of(t))
+                                    : (half ? s1 : s0) + ((int64_t)t.e * a.R + min(t.ct * TC + (GU ? c & 127 : c), a.R - 1));
+        return *at;
+    };
     const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
     auto keep_rows = [&](int par) {
         const uint32_t v = nx >> nx_shift;
@@ -1175,11 +1188,12 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         uint8_t wsn[2] = {0, 0};  // its weight scale bytes
         Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
         Weights wr = weights_of(p);
-        f32x4 acc[NB][4];
+        Sum4<T> acc[NB][4];
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < 4; ++j) acc[i][j] = Sum4<T>{0, 0, 0, 0};
+        float scale = 0.f;  // int8: one of the tile's, on its way to shared memory
         for (int u = 0; u < U; ++u) {
             char* here = lds.stage[par];
             char* there = lds.stage[par ^ 1];
@@ -1256,11 +1270,13 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     wsn[0] = weight_scale(pn, tid);
                     if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
                 }
+                if (I8) scale = tile_scale(p);
             } else if (u == 1) {
                 if (FP8) {
                     keep_weight_scale(spar ^ 1, tid, wsn[0]);
                     if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
                 }
+                if (I8) lds.scale[tid / kTM][tid & (kTM - 1)] = scale;  // (read at the tile's end, long before the next's)
                 if (GU) keep(slot_n);
                 if (tid == 0) lds.after = got + 2 * step;
             } else if (ub == U) {
@@ -1310,8 +1326,34 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         asm volatile("" : "+v"(el));  // addresses below are formed here, not kept through the products
         const int er = el & 15, eq = el >> 4;
         if constexpr (GU) {
-            const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * ES, (uint32_t)p.rows * a.R * ES);
+            const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * HS, (uint32_t)p.rows * a.R * HS);
             const int c0 = p.ct * TC + wn * 32;  // this wave's 32 columns of h
+            // bf16 h of row block i, turned: whole pieces of rows
+            auto store_h = [&](int i, f32x4 h0, f32x4 h1) {
+                *reinterpret_cast<u32x2*>(turn + er * 80 + 8 * eq) = u32x2{bf16_pair(h0[0], h0[1]), bf16_pair(h0[2], h0[3])};
+                *reinterpret_cast<u32x2*>(turn + er * 80 + 32 + 8 * eq) =
+                    u32x2{bf16_pair(h1[0], h1[1]), bf16_pair(h1[2], h1[3])};
+                const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 2) * 80 + (el & 3) * 16);
+                const int rr = (i * 2 + wm) * 16 + (el >> 2), c = c0 + (el & 3) * 8;
+                __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
+            };
+            if constexpr (I8) {
+                f32x4 sw[4];  // of the lane's columns: two blocks of gate's, two of up's
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sw[j] = *reinterpret_cast<const f32x4*>(&lds.scale[1][(j >> 1) * 128 + wn * 32 + (j & 1) * 16 + 4 * eq]);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const float sx = lds.scale[0][(i * 2 + wm) * 16 + er];
+                    f32x4 h[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            h[j][k] = silu((float)acc[i][j][k] * sx * sw[j][k]) * ((float)acc[i][j + 2][k] * sx * sw[j + 2][k]);
+                    store_h(i, h[0], h[1]);
+                }
+            } else {
             uint32_t m[NB];  // |h|'s largest bits: the order of the values, with what is not finite above
             bool odd = false;
 #pragma unroll
@@ -1375,31 +1417,30 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                                                      el < 32 && i < NB ? rr * CT + p.ct : kOOB, 0, 0);
             } else {
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const f32x4 h = acc[i][j];
-                        *reinterpret_cast<u32x2*>(turn + er * 80 + j * 32 + 8 * eq) =
-                            u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
-                    }
-                    const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 2) * 80 + (el & 3) * 16);
-                    const int rr = (i * 2 + wm) * 16 + (el >> 2), c = c0 + (el & 3) * 8;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
-                }
+                for (int i = 0; i < NB; ++i) store_h(i, acc[i][0], acc[i][1]);
+            }
             }
         } else {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
             const int c0 = p.ct * TC + wn * 64;  // this wave's 64 columns, a block of O
             int byte[NB];
+            f32x4 sw[4];
+            if constexpr (I8) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sw[j] = *reinterpret_cast<const f32x4*>(&lds.scale[1][wn * 64 + j * 16 + 4 * eq]);
+            }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 float v[4][4];  // read once from the accumulators
                 uint32_t m = 0;
+                float sx = 0.f;
+                if constexpr (I8) sx = lds.scale[0][(i * 2 + wm) * 16 + er];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        v[j][k] = acc[i][j][k];
+                        if constexpr (I8) v[j][k] = (float)acc[i][j][k] * sx * sw[j][k];
+                        else v[j][k] = acc[i][j][k];
                         asm volatile("" : "+v"(v[j][k]));
                         m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
                     }
