@@ -8,6 +8,7 @@
 
 #include "grouped_kernel.h"
 #include "moe_expert.h"
+#include "small_kernel.h"
 
 namespace {
 
@@ -251,6 +252,43 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 
+// The two-launch pass of few slots in 8-bit integers, where its codes fit shared memory.
+bool small_pass(const moe_layer_desc* d, int32_t n) {
+    const int64_t S = (int64_t)n * d->m;
+    return d->dtype == MOE_INT8 && S <= kSmallSlots && std::min<int64_t>(S, kTile16) * (d->d_model + 16) <= kSmallLds &&
+           S * (d->d_ff + 16) <= kSmallLds;
+}
+
+void run_small(const moe_layer_desc* d, const Weights& gu, const Weights& dn, const void* x, const int32_t* ids,
+               const float* w, int32_t n, void* y, int32_t* info, char* h, hipStream_t st) {
+    Small a{};
+    a.x = reinterpret_cast<const char*>(x);
+    a.ids = ids;
+    a.rw = w;
+    a.w0 = reinterpret_cast<const char*>(gu.w0);
+    a.w1 = reinterpret_cast<const char*>(gu.w1);
+    a.wd = reinterpret_cast<const char*>(dn.w0);
+    a.s0 = reinterpret_cast<const float*>(gu.s0);
+    a.s1 = reinterpret_cast<const float*>(gu.s1);
+    a.sd = reinterpret_cast<const float*>(dn.s0);
+    a.h = h;
+    a.y = reinterpret_cast<char*>(y);
+    a.info = info;
+    a.N = d->N;
+    a.n = n;
+    a.m = d->m;
+    a.S = n * d->m;
+    a.d = d->d_model;
+    a.f = d->d_ff;
+    a.accumulate = (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0;
+    const int tiles = std::min(a.N, a.S) + a.S / kTile16;  // most there can be
+    const bool tiled = d->flags & MOE_FLAG_TILED;
+    hipLaunchKernelGGL(tiled ? k_small_gate_up<true> : k_small_gate_up<false>, dim3(tiles * (a.f / 16)), dim3(256),
+                       std::min(a.S, kTile16) * (a.d + 16), st, a);
+    hipLaunchKernelGGL(tiled ? k_small_down<true> : k_small_down<false>, dim3(a.d / 16), dim3(kSmallDownThreads),
+                       a.S * (a.f + 16), st, a);
+}
+
 template <int T>
 int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, const void* x, const int32_t* ids,
              const float* w, int32_t n, void* y, int32_t* info, void* ws, hipStream_t st) {
@@ -259,6 +297,10 @@ int run_pass(const moe_layer_desc* d, const Weights& gu, const Weights& dn, cons
     auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(b + at); };
     auto u8 = [&](size_t at) { return reinterpret_cast<uint8_t*>(b + at); };
     (void)hipGetLastError();
+    if (T == kInt8 && small_pass(d, n)) {
+        run_small(d, gu, dn, x, ids, w, n, y, info, b + p.hf, st);
+        return launched();
+    }
     Group g{};
     g.ids = ids;
     g.S = (int64_t)n * d->m;

@@ -288,6 +288,17 @@ __device__ __forceinline__ uint32_t codes4_i8(float a, float b, float c, float d
     return r.inv != 0.f ? lo | hi : 0u;
 }
 
+__device__ __forceinline__ u32x2 codes8_i8(u32x4 a, const RowScale& r) {  // of eight bf16 values
+    return u32x2{codes4_i8(bf16_lo(a[0]), bf16_hi(a[0]), bf16_lo(a[1]), bf16_hi(a[1]), r),
+                 codes4_i8(bf16_lo(a[2]), bf16_hi(a[2]), bf16_lo(a[3]), bf16_hi(a[3]), r)};
+}
+__device__ __forceinline__ uint32_t largest(u32x4 a) {  // bits of the largest |v| of eight
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(a[j] << 16 & 0x7fffffffu, a[j] & 0x7fff0000u));
+    return m;
+}
+
 // Rows of bf16 values to codes and scales; work group g of G.  L lanes a row (a power of two, from the row's
 // length: four vectors of eight values a lane, held between the maximum and the codes; longer rows than a work
 // group so holds are read again).
@@ -319,9 +330,7 @@ __device__ __forceinline__ void quant_rows_i8(const char* __restrict__ x, int64_
         for (int v0 = 0; v0 < V; v0 += kRowVecs) {
             load(v0);
 #pragma unroll
-            for (int i = 0; i < kRowVecs; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = max(m, max(a[i][j] << 16 & 0x7fffffffu, a[i][j] & 0x7fff0000u));
+            for (int i = 0; i < kRowVecs; ++i) m = max(m, largest(a[i]));
         }
         for (int o = min(L, 64) / 2; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
         if (L > 64) {
@@ -337,10 +346,7 @@ __device__ __forceinline__ void quant_rows_i8(const char* __restrict__ x, int64_
 #pragma unroll
             for (int i = 0; i < kRowVecs; ++i) {
                 const int c = (v0 + i) * span + l * 8;
-                if (in && c < K)
-                    *reinterpret_cast<u32x2*>(q + row * K + c) =
-                        u32x2{codes4_i8(bf16_lo(a[i][0]), bf16_hi(a[i][0]), bf16_lo(a[i][1]), bf16_hi(a[i][1]), r),
-                              codes4_i8(bf16_lo(a[i][2]), bf16_hi(a[i][2]), bf16_lo(a[i][3]), bf16_hi(a[i][3]), r)};
+                if (in && c < K) *reinterpret_cast<u32x2*>(q + row * K + c) = codes8_i8(a[i], r);
             }
         }
     }
