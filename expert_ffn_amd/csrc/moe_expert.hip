@@ -925,7 +925,8 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
     const dim3 grid((desc->N + kTile - 1) / kTile, (n + kTile - 1) / kTile, a.KS);
     hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
     (void)hipGetLastError();
-    const auto route = desc->N <= 128   ? (bf ? k_route<true, 2> : k_route<false, 2>)
+    const auto route = desc->N <= 64    ? (bf ? k_route<true, 1> : k_route<false, 1>)
+                       : desc->N <= 128 ? (bf ? k_route<true, 2> : k_route<false, 2>)
                        : desc->N <= 256 ? (bf ? k_route<true, 4> : k_route<false, 4>)
                                         : (bf ? k_route<true, 16> : k_route<false, 16>);
     hipLaunchKernelGGL(route, grid, dim3(kRouteThreads), 0, st, a);

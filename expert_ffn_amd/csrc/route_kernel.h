@@ -6,9 +6,10 @@
 //
 // One work group of 16 waves for 16 experts x 16 tokens x one of KS parts of the contraction; its waves split
 // the part, so that at d = 2048 in bf16 each has one step: one round of loads.  The parts go to memory, and the work
-// group that arrives last on a token tile adds them, in order, and selects: a wave a token, m rounds of a wave-wide
-// maximum.  How the contraction is cut depends on N, d and the type alone, so a token's routing does
-// not depend on the pass that it is in.
+// group that arrives last on a token tile adds them, in order, and selects: a wave a token, m rounds of a
+// wave-wide maximum; or, of one or two tokens, by rank (an expert's place is the number of those before it), all
+// threads together.  How the contraction is cut depends on N, d and the type alone, so a token's routing does not
+// depend on the pass that it is in.
 #pragma once
 
 #include "expert_kernel.h"
@@ -17,6 +18,10 @@ namespace moe_k {
 
 constexpr int kRouteWaves = 16, kRouteThreads = 64 * kRouteWaves;
 constexpr int kRouteParts = 8;  // most parts of the contraction
+// Selection by rank for tiles of up to so many (token, expert) pairs: its work grows with tokens N^2 and all of the work
+// group shares it.  The launch by rank and by rounds, N = 128: one token 6.9 / 7.6 us, 16 tokens 18.2 / 11.4; N = 64,
+// 5 tokens 11.1 / 8.9 (as 128).
+constexpr int kRankMost = 256;
 static_assert(kRouteWaves == kTile, "a wave a token of the tile");
 
 struct RouteArgs {
@@ -37,6 +42,8 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
     return v == v ? ((int)b < 0 ? ~b : b | 0x80000000u) : 0u;
 }
+
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((int)k < 0 ? k & 0x7fffffffu : ~k); }
 
 // The wave's largest, in every lane: rows of 16 by shifts, then across the rows.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -71,6 +78,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     __shared__ int sel_e[kRouteWaves][MOE_MAX_SLOTS];
     __shared__ float sel_l[kRouteWaves][MOE_MAX_SLOTS];
     __shared__ int s_last;
+    constexpr int NK = 64 * CL;
+    __shared__ __align__(16) uint32_t s_key[kRankMost];
+    __shared__ float s_l[kRankMost];
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int lr = lane & 15, q = lane >> 4;
     const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile, ks = blockIdx.z, KS = a.KS;
@@ -119,11 +129,16 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         }
     }
     __syncthreads();  // the loads (sc1) below go out after the last arrival was seen
-    const int t = t0 + wave;
-    if (!s_last || t >= a.n) return;  // (no barrier below)
-
-    float l[CL];
-    {
+    if (!s_last) return;
+    const int t = t0 + wave, nt = min(kTile, a.n - t0);  // this wave's token, tokens of the tile
+    const bool live = wave < nt;
+    const bool rank = nt * NK <= kRankMost;
+    if (!rank && !live) return;  // (by rounds there is no barrier)
+    int* se = sel_e[wave];
+    float* sl = sel_l[wave];
+    float l[CL], top = -INFINITY, Z = 1.f;  // logits; the largest; sum of exp(l - top)
+    uint32_t key[CL];
+    if (live) {
         uint32_t pv[CL][kRouteParts];
 #pragma unroll
         for (int j = 0; j < CL; ++j)
@@ -138,87 +153,116 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
             l[j] = __uint_as_float(pv[j][0]);
 #pragma unroll
             for (int k = 1; k < kRouteParts; ++k) l[j] += __uint_as_float(pv[j][k]);  // (parts past KS: 0)
+            key[j] = lane + 64 * j < a.N ? order_of(l[j]) : 0u;
+            if (key[j]) top = fmaxf(top, l[j]);
+        }
+        if (!a.sigmoid && (a.bias || !a.renorm)) {
+            top = value_of(wave_max(order_of(top)));
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < CL; ++j)
+                if (key[j]) z += expf(l[j] - top);
+            Z = wave_sum(z);
+        }
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < CL; ++j)
+                if (key[j]) {
+                    const float s = a.sigmoid ? 1.f / (1.f + expf(-l[j])) : expf(l[j] - top) / Z;
+                    key[j] = order_of(s + a.bias[lane + 64 * j]);
+                }
         }
     }
-    uint32_t key[CL];
-    float top = -INFINITY, Z = 1.f;  // the largest logit; sum of exp(l - top)
+    if (rank) {
+        if (live) {
 #pragma unroll
-    for (int j = 0; j < CL; ++j) {
-        key[j] = lane + 64 * j < a.N ? order_of(l[j]) : 0u;
-        if (key[j]) top = fmaxf(top, l[j]);
-    }
-    if (!a.sigmoid && (a.bias || !a.renorm)) {
-        const uint32_t k = wave_max(order_of(top));
-        top = __uint_as_float((int)k < 0 ? k & 0x7fffffffu : ~k);
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < CL; ++j)
-            if (key[j]) z += expf(l[j] - top);
-        Z = wave_sum(z);
-    }
-    if (a.bias) {
-#pragma unroll
-        for (int j = 0; j < CL; ++j)
-            if (key[j]) {
-                const float s = a.sigmoid ? 1.f / (1.f + expf(-l[j])) : expf(l[j] - top) / Z;
-                key[j] = order_of(s + a.bias[lane + 64 * j]);
+            for (int j = 0; j < CL; ++j) {
+                s_key[wave * NK + lane + 64 * j] = key[j];
+                s_l[wave * NK + lane + 64 * j] = l[j];
             }
-    }
-    // rounds: the wave's largest key, of equal ones the lowest expert
-    int* se = sel_e[wave];
-    float* sl = sel_l[wave];
-    for (int r = 0; r < a.m; ++r) {
-        uint32_t best = key[0];
-        int bj = 0;
-        float bl = l[0];
-#pragma unroll
-        for (int j = 1; j < CL; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                bj = j;
-                bl = l[j];
-            }
-        const uint32_t most = wave_max(best);
-        int e = -1;
-        float v = 0.f;
-        if (most) {  // (0: nothing is left)
-            uint64_t who = __ballot(best == most);
-            if (who & (who - 1)) {  // several: the lowest 64 j + lane
-                const uint32_t least = wave_max(best == most ? ~(uint32_t)(bj * 64 + lane) : 0u);
-                who = 1ull << (~least & 63u);
-            }
-            const int at = __ffsll((unsigned long long)who) - 1;
-            const int j = __builtin_amdgcn_readlane(bj, at);
-            v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bl), at));
-            e = 64 * j + at;
-#pragma unroll
-            for (int i = 0; i < CL; ++i)
-                if (i == j && lane == at) key[i] = 0u;
+            for (int j = lane; j < a.m; j += 64) se[j] = -1;
         }
-        if (lane == 0) {
-            se[r] = e;
-            sl[r] = v;
+        __syncthreads();
+        // G threads an expert, each a part of the others; what is no expert has key 0, behind all
+        int G = 1;
+        while (G < 8 && 2 * G * nt * NK <= kRouteThreads) G *= 2;
+        const int g = tid & (G - 1), part = NK / G;
+        for (int i = tid / G; i < nt * NK; i += kRouteThreads / G) {
+            const int u = i / NK, e = i & (NK - 1);
+            const uint32_t mine = s_key[i];
+            const u32x4* others = reinterpret_cast<const u32x4*>(&s_key[u * NK + g * part]);
+            int before = 0;
+#pragma unroll 4
+            for (int k = 0; k < part / 4; ++k) {
+                const u32x4 v = others[k];
+                const int at = g * part + 4 * k;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) before += v[c] + (at + c < e ? 1u : 0u) > mine;  // (no key is 2^32 - 1)
+            }
+            for (int o = G / 2; o > 0; o >>= 1) before += __shfl_xor(before, o, 64);
+            if (g == 0 && mine && before < a.m) {
+                sel_e[u][before] = e;
+                sel_l[u][before] = s_l[i];
+            }
         }
+        __syncthreads();
+        if (!live) return;
+    } else {
+        // rounds: the wave's largest key, of equal ones the lowest expert
+        for (int r = 0; r < a.m; ++r) {
+            uint32_t best = key[0];
+            int bj = 0;
+            float bl = l[0];
+#pragma unroll
+            for (int j = 1; j < CL; ++j)
+                if (key[j] > best) {
+                    best = key[j];
+                    bj = j;
+                    bl = l[j];
+                }
+            const uint32_t most = wave_max(best);
+            int e = -1;
+            float v = 0.f;
+            if (most) {  // (0: nothing is left)
+                uint64_t who = __ballot(best == most);
+                if (who & (who - 1)) {  // several: the lowest 64 j + lane
+                    const uint32_t least = wave_max(best == most ? ~(uint32_t)(bj * 64 + lane) : 0u);
+                    who = 1ull << (~least & 63u);
+                }
+                const int at = __ffsll((unsigned long long)who) - 1;
+                const int j = __builtin_amdgcn_readlane(bj, at);
+                v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bl), at));
+                e = 64 * j + at;
+#pragma unroll
+                for (int i = 0; i < CL; ++i)
+                    if (i == j && lane == at) key[i] = 0u;
+            }
+            if (lane == 0) {
+                se[r] = e;
+                sl[r] = v;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    // weights: s_j over their sum, or over Z; the first selected is the largest only without a bias
+    // weights: s_j over the sum of the selected, or over Z (with a bias the first selected need not be the largest)
     float c = -INFINITY;
     for (int j = lane; j < a.m; j += 64)
         if (se[j] >= 0) c = fmaxf(c, sl[j]);
-    const uint32_t ck = wave_max(order_of(c));
-    c = __uint_as_float((int)ck < 0 ? ck & 0x7fffffffu : ~ck);
+    c = value_of(wave_max(order_of(c)));
     if (a.sigmoid) c = a.renorm ? fminf(c, 0.f) : 0.f;
     else if (!a.renorm) c = top;
-    auto value = [&](int j) { return se[j] < 0 ? 0.f : a.sigmoid ? sigmoid_from(sl[j], c) : expf(sl[j] - c); };
-    if (a.renorm) {
-        float z = 0.f;
-        for (int j = lane; j < a.m; j += 64) z += value(j);
-        Z = wave_sum(z);
+    float z = 0.f;
+    for (int j = lane; j < a.m; j += 64) {
+        const float v = se[j] < 0 ? 0.f : a.sigmoid ? sigmoid_from(sl[j], c) : expf(sl[j] - c);
+        sl[j] = v;  // (a lane's own places)
+        z += v;
     }
+    if (a.renorm) Z = wave_sum(z);
+    const float f = a.scale / Z;
     for (int j = lane; j < a.m; j += 64) {
         a.ids[(size_t)t * a.m + j] = se[j];
-        a.w[(size_t)t * a.m + j] = se[j] < 0 ? 0.f : value(j) / Z * a.scale;
+        a.w[(size_t)t * a.m + j] = se[j] < 0 ? 0.f : sl[j] * f;
     }
 }
 
