@@ -77,6 +77,12 @@ void run_group(Group g, hipStream_t st) {
 // bf16 230 / 229 / 235 / 248 against 227 / 228 / 229 / 230, e4m3 129 / 134 / 139 / 148 against 144 / 146 / 147 / 148;
 // with popularity falling as 1 / rank^1.1, bf16 147 / 173 / 191 / 213 against 146 / 160 / 159 / 165, e4m3
 // 93 / 107 / 118 / 130 against 100 / 113 / 112 / 117.
+// int8 runs thin tiles without e4m3's widening: whole passes at a mean of 12 / 14 / 16 / 20 rows, thin against square:
+//     128 of 2048 x 768, ids uniform   134 / 142 / 153 / 174   145 / 146 / 147 / 150
+//       popularity 1 / rank^1.1        120 / 130 / 135 / 161   111 / 124 / 120 / 142
+//     64 of 2048 x 1408, uniform       120 / 129 / 139 / 155   130 / 130 / 131 / 134
+//       1 / rank^1.1                   117 / 123 / 138 / 147   113 / 119 / 131 / 135
+//     8 of 4096 x 14336, uniform       270 / 308 / 346 / 376   298 / 300 / 301 / 303
 // The mean counts padding, as only the device knows the groups.  4096 tokens of 8 slots of which 32 tokens are
 // live, thin against square, whole passes of the first layer: bf16 296 / 214, e4m3 232 / 151 (a thin tile's work
 // groups are launched for every row there could be).  900 of 1000 rows on one of the 128 experts: 179 / 166 and 103 / 107.
@@ -84,10 +90,10 @@ void run_group(Group g, hipStream_t st) {
 // units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
 // tile has beyond it); thin tiles address all of memory.
 bool square(const Args& a, int type, bool gu) {
-    const bool fp8 = type != kBf16;
+    const int least = type == kBf16 ? 8 : type == kFp8 ? 12 : 14;
     const int64_t kby = (int64_t)a.K * elem_size(type), most = (1ll << 31) - 4096;
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
-    return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? (fp8 ? 12 : 8) : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
+    return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? least : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
            (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
 }
 

@@ -777,7 +777,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
             const float sx = reinterpret_cast<const float*>(a.xs)[xrow];
             const float* sw = reinterpret_cast<const float*>(i ? a.s1 : a.s0) + (int64_t)t.e * a.R + c;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] = (float)sum[i][k] * sx * sw[k];
+            for (int k = 0; k < 4; ++k) v[i][k] = (float)sum[i][k] * sw[k] * sx;
         } else {
             v[i] = sum[i];
         }
@@ -1356,7 +1356,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            h[j][k] = silu((float)acc[i][j][k] * sx * sw[j][k]) * ((float)acc[i][j + 2][k] * sx * sw[j + 2][k]);
+                            h[j][k] = silu((float)acc[i][j][k] * sw[j][k] * sx) * ((float)acc[i][j + 2][k] * sw[j + 2][k] * sx);
                     store_h(i, h[0], h[1]);
                 }
             } else {
@@ -1445,7 +1445,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if constexpr (I8) v[j][k] = (float)acc[i][j][k] * sx * sw[j][k];
+                        if constexpr (I8) v[j][k] = (float)acc[i][j][k] * sw[j][k];  // (times sx below)
                         else v[j][k] = acc[i][j][k];
                         asm volatile("" : "+v"(v[j][k]));
                         m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
@@ -1457,8 +1457,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(v[j][k])));
                 }
-                byte[i] = term_byte(quad_max(m));
-                const float inv = __uint_as_float((uint32_t)(268 - byte[i]) << 23);  // 2^(141 - byte)
+                m = quad_max(m);
+                if constexpr (I8) m = __float_as_uint(mag(__uint_as_float(m) * sx));
+                byte[i] = term_byte(m);
+                float inv = __uint_as_float((uint32_t)(268 - byte[i]) << 23);  // 2^(141 - byte)
+                if constexpr (I8) inv *= sx;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float* o = v[j];

@@ -690,9 +690,20 @@ LayerSpace layer_space(const moe_layer_desc* d, int32_t n, size_t expert_bytes) 
     return p;
 }
 
-// Passes from this many tokens on run the deduplicating kernel.
-constexpr int kLayerDedup = 3;
-int layer_kind(int32_t n) { return n >= kLayerDedup ? MOE_KIND_DEDUP : MOE_KIND_SLOT; }
+// The kernel of a pass: per-slot for one token without always-on experts, else deduplicating.  bf16, tiled, three
+// layers in turn, ids even, us per-slot / deduplicating:
+//                                              n = 1          2            3            4
+//     128 experts of 2048 x 768, 8 a token     22.4 / 23.2    33.5 / 35.3  42.7 / 43.6  52.7 / 53.2
+//     64 of 2048 x 1408, 6                     31.1 / 31.1    42.7 / 41.9  53.8 / 53.9  70.2 / 70.0
+//       and two always on                      41.1 / 39.5    47.0 / 45.9  61.3 / 60.5  75.8 / 71.7
+//     16 of 2048 x 2816, 4                     47.9 / 51.7    59.7 / 59.0  66.4 / 58.7  86.0 / 74.4
+//     16 of 4096 x 4096, 2                     63.3 / 66.4    89.7 / 83.6  98.7 / 92.2   133 / 123
+//     64 of 4096 x 1536, 8, and one always on  80.9 / 68.2     114 / 115    165 / 160    196 / 175
+//     8 of 4096 x 14336, 2                      132 / 128      249 / 231    374 / 318    472 / 335
+// Skewed routing, where tokens share more experts, gains more by reading each once.
+int layer_kind(const moe_layer_desc* d, int32_t n) {
+    return n >= 2 || d->n_shared > 0 ? MOE_KIND_DEDUP : MOE_KIND_SLOT;
+}
 
 }  // namespace
 
@@ -879,7 +890,7 @@ size_t moe_pass_workspace_bytes(const moe_layer_desc* desc, int32_t n) {
     if (layer_check(desc, n) != MOE_OK) return 0;
     size_t total = 0;  // largest over 1..n tokens
     for (int32_t k = 1; k <= n; ++k)
-        total = std::max(total, layer_space(desc, k, plan_for(desc, k, layer_kind(k)).total).total);
+        total = std::max(total, layer_space(desc, k, plan_for(desc, k, layer_kind(desc, k)).total).total);
     return total;
 }
 
@@ -900,7 +911,7 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
                                !aligned16(weights->w_down_shared)))
         return MOE_E_INVAL;
     if (router->score != MOE_SCORE_SOFTMAX && router->score != MOE_SCORE_SIGMOID) return MOE_E_INVAL;
-    const int kind = layer_kind(n);
+    const int kind = layer_kind(desc, n);
     const size_t expert_bytes = plan_for(desc, n, kind).total;
     const LayerSpace p = layer_space(desc, n, expert_bytes);
     if (ws_bytes < p.total) return MOE_E_WORKSPACE;

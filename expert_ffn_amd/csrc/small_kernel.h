@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void k_small_gate_up(Small a) {
         const i32x4 sum = red[0][i][lane] + red[1][i][lane] + red[2][i][lane] + red[3][i][lane];
         const float* sw = (i ? a.s1 : a.s0) + (int64_t)tile.e * a.f + c;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = (float)sum[k] * sx[lr] * sw[k];
+        for (int k = 0; k < 4; ++k) v[i][k] = (float)sum[k] * sw[k] * sx[lr];
     }
     float h[4];
 #pragma unroll
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(kSmallDownThreads) void k_small_down(Small a) {
     __syncthreads();
     // a slot's term w O, in fp32; in place of the sums
     float term = 0.f;
-    if (live) term = (float)sum[s][c] * sh[s] * sd;
+    if (live) term = (float)sum[s][c] * sd * sh[s];
     float* O = reinterpret_cast<float*>(&sum[0][0]);
     if (s < S) O[s * 17 + c] = term;
     float* wt = sh;  // the slots' weights, 0 for what is not valid, in place of the scales

@@ -426,8 +426,8 @@ typedef struct {
  * 1 <= rows <= MOE_MAX_QUANT_ROWS.  q and x 16-byte aligned.  One launch each.  moe_pack_tiled tiles codes with
  * desc->dtype MOE_INT8 as those of MOE_FP8; scales keep their layout.
  *
- * The products add the codes' products in int32, exactly; a sum times the token's scale, times the
- * channel's, is the fp32 value that the bf16 and e4m3 products have at that place.  h is rounded to
+ * The products add the codes' products in int32, exactly; a sum times the channel's scale, times the
+ * token's, is the fp32 value that the bf16 and e4m3 products have at that place.  h is rounded to
  * bf16 and then quantised by row.
  */
 #define MOE_MAX_QUANT_ROWS (1 << 26)
