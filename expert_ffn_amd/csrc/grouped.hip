@@ -258,10 +258,14 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 
-// The two-launch pass of few slots in 8-bit integers, where its codes fit shared memory.
+// The two-launch pass of few slots in 8-bit integers, where its codes fit shared memory and there are columns enough
+// for its down product, a work group 16 of them.  Two launches and five, us: 128 experts of 2048 x 768, 8 / 16 / 32 / 64
+// slots 15.6 / 21.3 / 35.1 / 58.4 and 25.3 / 31.4 / 41.2 / 60.4; 64 of 2048 x 1408, 6 / 24 / 48 slots 18.7 / 46.2 / 73.3
+// and 26.7 / 48.5 / 72.9; 8 of 4096 x 14336, 2 slots 79 and 84; 8 of 64 x 64, 21 slots 12.9 and 21.4; but 32 of
+// 192 x 1536, 35 slots 26.9 and 23.2.
 bool small_pass(const moe_layer_desc* d, int32_t n) {
     const int64_t S = (int64_t)n * d->m;
-    return d->dtype == MOE_INT8 && S <= kSmallSlots && std::min<int64_t>(S, kTile16) * (d->d_model + 16) <= kSmallLds &&
+    return d->dtype == MOE_INT8 && S <= kSmallSlots && (d->d_model >= 256 || S * d->d_ff <= (1 << 14)) && std::min<int64_t>(S, kTile16) * (d->d_model + 16) <= kSmallLds &&
            S * (d->d_ff + 16) <= kSmallLds;
 }
 

@@ -13,7 +13,7 @@
 namespace moe_g {
 
 constexpr int kSmallSlots = 64;             // a lane a slot
-constexpr int kSmallLds = 56 * 1024;        // bytes of codes in shared memory, at most
+constexpr int kSmallLds = 54 * 1024;        // bytes of codes in shared memory, at most (with the kernels' own 64 KB)
 constexpr int kSmallDownThreads = 1024;
 
 struct Small {

@@ -224,6 +224,18 @@ def test_pass(N, m, d, f, n):
         assert (y[n - n // 4:] == 0).all()
 
 
+@pytest.mark.parametrize("N,m,d,f,n", [
+    (8, 1, 3440, 32, 16), (8, 1, 3456, 32, 16), (2, 1, 64, 18416, 3), (2, 1, 64, 18432, 3), (4, 2, 128, 192, 32),
+    (4, 2, 128, 192, 33), (64, 8, 256, 192, 8), (1024, 4, 64, 48, 16), (4, 1, 16400, 32, 70), (2, 1, 32, 65536, 2),
+    (2, 1, 32, 65536, 70), (3, 1, 65536, 32, 70)])
+def test_where_the_form_of_a_pass_changes(N, m, d, f, n):
+    """Passes of 64 slots and one more, codes that just fit shared memory and just do not, rows of many rounds."""
+    say("int8 pass", N, m, d, f, n)
+    case = Case(N, m, d, f, layout="tiled" if d % 64 == 0 and f % 64 == 0 else "plain")
+    ids, w = _ids(n, n, m, N)
+    _check_pass(case, _randn(n, n, d).to(BF).cuda(), ids, w, "pass %s" % ((N, m, d, f, n),))
+
+
 @pytest.mark.parametrize("counts", [[300, 0, 1, 257, 64, 0, 192, 33], [0, 0, 700, 0, 0, 0, 0, 0]])
 @pytest.mark.parametrize("layout", ["plain", "tiled"])
 def test_many_rows(counts, layout):
