@@ -265,8 +265,8 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
 // 192 x 1536, 35 slots 26.9 and 23.2.
 bool small_pass(const moe_layer_desc* d, int32_t n) {
     const int64_t S = (int64_t)n * d->m;
-    return d->dtype == MOE_INT8 && S <= kSmallSlots && (d->d_model >= 256 || S * d->d_ff <= (1 << 14)) && std::min<int64_t>(S, kTile16) * (d->d_model + 16) <= kSmallLds &&
-           S * (d->d_ff + 16) <= kSmallLds;
+    return d->dtype == MOE_INT8 && S <= kSmallSlots && (d->d_model >= 256 || S * d->d_ff <= (1 << 14)) &&
+           std::min<int64_t>(S, kTile16) * (d->d_model + 16) <= kSmallLds && S * (d->d_ff + 16) <= kSmallLds;
 }
 
 void run_small(const moe_layer_desc* d, const Weights& gu, const Weights& dn, const void* x, const int32_t* ids,

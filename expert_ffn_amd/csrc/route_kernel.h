@@ -58,19 +58,29 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {  // a fixed tree; lane 0's for all
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+__device__ __forceinline__ float wave_sum(float v) {  // a fixed tree, the same in every lane
+#define MOE_DPP_ADD(ctrl, rows) \
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, rows, 0xf, true))
+    MOE_DPP_ADD(0x111, 0xf);
+    MOE_DPP_ADD(0x112, 0xf);
+    MOE_DPP_ADD(0x114, 0xf);
+    MOE_DPP_ADD(0x118, 0xf);
+    MOE_DPP_ADD(0x142, 0xa);
+    MOE_DPP_ADD(0x143, 0xc);
+#undef MOE_DPP_ADD
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// Sigmoid times exp(-c), c <= 0: with c the largest of the selected logits, or 0, the quotients of
-// weights stay where all sigmoids are too small for fp32.
+// Sigmoid times exp(-c), c <= 0, the same in every lane: with c the largest of the selected logits, or 0, the
+// quotients of weights stay where all sigmoids are too small for fp32.
 __device__ __forceinline__ float sigmoid_from(float l, float c) {
-    return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - c) / (1.f + expf(l));
+    const float t = expf(-fabsf(l));
+    float up = t;
+    if (c < 0.f) up = expf(l - c);
+    return (l > 0.f ? 1.f : up) * __builtin_amdgcn_rcpf(1.f + t);
 }
 
-// CL: experts a lane holds, lane + 64 j
+// CL: experts a lane holds, CL lane + j
 template <bool BF16, int CL>
 __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     using F = Fmt<BF16>;
@@ -144,7 +154,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         for (int j = 0; j < CL; ++j)
 #pragma unroll
             for (int k = 0; k < kRouteParts; ++k) {
-                const int e = lane + 64 * j;
+                const int e = CL * lane + j;
                 pv[j][k] = __builtin_amdgcn_raw_buffer_load_b32(
                     rp, k < KS && e < a.N ? (((uint32_t)k * a.n + t) * a.N + e) * 4u : kOOB, 0, kSc1);
             }
@@ -153,7 +163,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
             l[j] = __uint_as_float(pv[j][0]);
 #pragma unroll
             for (int k = 1; k < kRouteParts; ++k) l[j] += __uint_as_float(pv[j][k]);  // (parts past KS: 0)
-            key[j] = lane + 64 * j < a.N ? order_of(l[j]) : 0u;
+            key[j] = CL * lane + j < a.N ? order_of(l[j]) : 0u;
             if (key[j]) top = fmaxf(top, l[j]);
         }
         if (!a.sigmoid && (a.bias || !a.renorm)) {
@@ -168,8 +178,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
 #pragma unroll
             for (int j = 0; j < CL; ++j)
                 if (key[j]) {
-                    const float s = a.sigmoid ? 1.f / (1.f + expf(-l[j])) : expf(l[j] - top) / Z;
-                    key[j] = order_of(s + a.bias[lane + 64 * j]);
+                    const float s = a.sigmoid ? sigmoid_from(l[j], 0.f) : expf(l[j] - top) / Z;
+                    key[j] = order_of(s + a.bias[CL * lane + j]);
                 }
         }
     }
@@ -177,8 +187,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         if (live) {
 #pragma unroll
             for (int j = 0; j < CL; ++j) {
-                s_key[wave * NK + lane + 64 * j] = key[j];
-                s_l[wave * NK + lane + 64 * j] = l[j];
+                s_key[wave * NK + CL * lane + j] = key[j];
+                s_l[wave * NK + CL * lane + j] = l[j];
             }
             for (int j = lane; j < a.m; j += 64) se[j] = -1;
         }
@@ -208,38 +218,35 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         __syncthreads();
         if (!live) return;
     } else {
-        // rounds: the wave's largest key, of equal ones the lowest expert
-        for (int r = 0; r < a.m; ++r) {
-            uint32_t best = key[0];
-            int bj = 0;
-            float bl = l[0];
+        // rounds: the wave's largest key, of equal ones the lowest lane's (and a lane's first), which is the lowest
+        // expert; the lanes keep 64 rounds' results, then hand them over
+        for (int r0 = 0; r0 < a.m; r0 += 64) {
+            int mine_e = -1;
+            float mine_l = 0.f;
+            const int rounds = min(64, a.m - r0);
+            for (int r = 0; r < rounds; ++r) {
+                uint32_t best = key[0];
+                int bj = 0;
+                float bl = l[0];
 #pragma unroll
-            for (int j = 1; j < CL; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    bj = j;
-                    bl = l[j];
+                for (int j = 1; j < CL; ++j) {
+                    const bool more = key[j] > best;
+                    best = more ? key[j] : best;
+                    bj = more ? j : bj;
+                    bl = more ? l[j] : bl;
                 }
-            const uint32_t most = wave_max(best);
-            int e = -1;
-            float v = 0.f;
-            if (most) {  // (0: nothing is left)
-                uint64_t who = __ballot(best == most);
-                if (who & (who - 1)) {  // several: the lowest 64 j + lane
-                    const uint32_t least = wave_max(best == most ? ~(uint32_t)(bj * 64 + lane) : 0u);
-                    who = 1ull << (~least & 63u);
-                }
-                const int at = __ffsll((unsigned long long)who) - 1;
-                const int j = __builtin_amdgcn_readlane(bj, at);
-                v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bl), at));
-                e = 64 * j + at;
+                const uint32_t most = wave_max(best);
+                const int at = __ffsll((unsigned long long)__ballot(best == most)) - 1;
+                const int j = __builtin_amdgcn_readlane(bj, at), e = most ? CL * at + j : -1;  // (0: nothing is left)
+                const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(bl), at));
+                mine_e = lane == r ? e : mine_e;
+                mine_l = lane == r ? v : mine_l;
 #pragma unroll
-                for (int i = 0; i < CL; ++i)
-                    if (i == j && lane == at) key[i] = 0u;
+                for (int i = 0; i < CL; ++i) key[i] = i == j && lane == at ? 0u : key[i];
             }
-            if (lane == 0) {
-                se[r] = e;
-                sl[r] = v;
+            if (lane < rounds) {
+                se[r0 + lane] = mine_e;
+                sl[r0 + lane] = mine_l;
             }
         }
         __builtin_amdgcn_wave_barrier();
