@@ -684,7 +684,7 @@ LayerSpace layer_space(const moe_layer_desc* d, int32_t n, size_t expert_bytes) 
     LayerSpace p;
     p.expert = align_up((size_t)(MOE_MAX_TOKENS / kTile) * kLine * 4);
     p.part = p.expert + align_up(expert_bytes);
-    p.ids = p.part + align_up((size_t)route_parts(d) * n * d->N * 4);
+    p.ids = p.part + align_up((size_t)route_parts(d) * n * route_row(d->N) * 4);
     p.w = p.ids + align_up((size_t)n * d->m * 4);
     p.total = p.w + align_up((size_t)n * d->m * 4);
     return p;

@@ -28,7 +28,7 @@ struct RouteArgs {
     const char* wr;     // [N][d]
     const char* x;      // [n][d]
     const float* bias;  // [N] or null
-    float* part;        // [KS][n][N]
+    float* part;        // [KS][n][row of N, whole fours]
     int32_t* count;     // [token tiles][kLine], zero
     int32_t* ids;       // [n][m]
     float* w;
@@ -80,6 +80,23 @@ __device__ __forceinline__ float sigmoid_from(float l, float c) {
     return (l > 0.f ? 1.f : up) * __builtin_amdgcn_rcpf(1.f + t);
 }
 
+__host__ __device__ __forceinline__ uint32_t route_row(int N) { return (uint32_t)(N + 3) & ~3u; }
+
+template <int V>
+__device__ __forceinline__ void route_load(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so, uint32_t* v) {
+    if constexpr (V == 1) {
+        v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, vo, so, kSc1);
+    } else if constexpr (V == 2) {
+        const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, vo, so, kSc1));
+        v[0] = w.x;
+        v[1] = w.y;
+    } else {
+        const u32x4 w = bload2<kSc1>(r, vo, so);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
+    }
+}
+
 // CL: experts a lane holds, CL lane + j
 template <bool BF16, int CL>
 __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
@@ -117,20 +134,20 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     }
     red[wave][lane] = acc;
     __syncthreads();
-    const auto rp = rsrc(a.part, (uint32_t)KS * a.n * a.N * 4);
+    const uint32_t NP = route_row(a.N);
+    const auto rp = rsrc(a.part, (uint32_t)KS * a.n * NP * 4);
     if (wave == 0) {
-        f32x4 v = red[0][lane];
+        f32x4 r[kRouteWaves];  // (read together)
 #pragma unroll
-        for (int w = 1; w < kRouteWaves; ++w) v += red[w][lane];
-        // experts e0 + 4 q + i of token t0 + lr
-        const int t = t0 + lr;
+        for (int w = 0; w < kRouteWaves; ++w) r[w] = red[w][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 v = r[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = e0 + 4 * q + i;
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), rp,
-                                                  e < a.N && t < a.n ? (((uint32_t)ks * a.n + t) * a.N + e) * 4u : kOOB, 0,
-                                                  kSc1);
-        }
+        for (int w = 1; w < kRouteWaves; ++w) v += r[w];
+        // experts e0 + 4 q .. + 3 of token t0 + lr (past N: zeros)
+        const uint32_t t = t0 + lr, e = e0 + 4 * q;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rp,
+                                               e < NP && (int)t < a.n ? ((ks * a.n + t) * NP + e) * 4u : kOOB, 0, kSc1);
         stores_complete();
         if (lane == 0) {
             int32_t* count = a.count + kLine * blockIdx.y;
@@ -149,20 +166,23 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     float l[CL], top = -INFINITY, Z = 1.f;  // logits; the largest; sum of exp(l - top)
     uint32_t key[CL];
     if (live) {
-        uint32_t pv[CL][kRouteParts];
+        constexpr int V = CL < 4 ? CL : 4, W = CL / V;  // a lane's experts as W vectors
+        uint32_t pv[kRouteParts][CL], bias[CL];
 #pragma unroll
-        for (int j = 0; j < CL; ++j)
+        for (int w = 0; w < W; ++w) {
+            const uint32_t e = CL * lane + V * w, vo = e < NP ? (t * NP + e) * 4u : kOOB;
 #pragma unroll
-            for (int k = 0; k < kRouteParts; ++k) {
-                const int e = CL * lane + j;
-                pv[j][k] = __builtin_amdgcn_raw_buffer_load_b32(
-                    rp, k < KS && e < a.N ? (((uint32_t)k * a.n + t) * a.N + e) * 4u : kOOB, 0, kSc1);
-            }
+            for (int k = 0; k < kRouteParts; ++k)
+                route_load<V>(rp, k < KS ? vo : kOOB, k * a.n * NP * 4u, &pv[k][V * w]);
+        }
+        const auto rb = rsrc(a.bias, a.bias ? a.N * 4u : 0u);
+#pragma unroll
+        for (int j = 0; j < CL; ++j) bias[j] = __builtin_amdgcn_raw_buffer_load_b32(rb, (CL * lane + j) * 4u, 0, 0);
 #pragma unroll
         for (int j = 0; j < CL; ++j) {
-            l[j] = __uint_as_float(pv[j][0]);
+            l[j] = __uint_as_float(pv[0][j]);
 #pragma unroll
-            for (int k = 1; k < kRouteParts; ++k) l[j] += __uint_as_float(pv[j][k]);  // (parts past KS: 0)
+            for (int k = 1; k < kRouteParts; ++k) l[j] += __uint_as_float(pv[k][j]);  // (parts past KS: 0)
             key[j] = CL * lane + j < a.N ? order_of(l[j]) : 0u;
             if (key[j]) top = fmaxf(top, l[j]);
         }
@@ -179,7 +199,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
             for (int j = 0; j < CL; ++j)
                 if (key[j]) {
                     const float s = a.sigmoid ? sigmoid_from(l[j], 0.f) : expf(l[j] - top) / Z;
-                    key[j] = order_of(s + a.bias[CL * lane + j]);
+                    key[j] = order_of(s + __uint_as_float(bias[j]));
                 }
         }
     }
