@@ -70,13 +70,16 @@ struct Args {
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+__device__ __forceinline__ i32x4 mma_i8(u32x4 a, u32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
 // One unit's product.  e4m3: the operands' scale bytes, sa's lowest and byte `sel` of sb
 // (a constant once its loop is unrolled).
 template <int T>
 __device__ __forceinline__ Sum4<T> mma_unit(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, Sum4<T> c, int sa, int sb, int sel = 0) {
     if constexpr (T == kInt8) {
-        c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a0), __builtin_bit_cast(i32x4, b0), c, 0, 0, 0);
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a1), __builtin_bit_cast(i32x4, b1), c, 0, 0, 0);
+        return mma_i8(a1, b1, mma_i8(a0, b0, c));
     } else if constexpr (T == kFp8) {
         struct Pair {
             u32x4 lo, hi;
@@ -1217,10 +1220,17 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = F; i < E; ++i) {
+                    if constexpr (I8) {  // a sum's two products apart
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[i][j] = mma_i8(b[j][kk], x[i % H][kk], acc[i][j]);
+                    } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         acc[i][j] = mma_unit<T>(b[j][0], b[j][1], x[i % H][0], x[i % H][1], acc[i][j],
                                                   GU && j >= 2 ? e1 : e0, (int)ex[i / 4], i);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                     then(i);
                     __builtin_amdgcn_sched_barrier(0);
