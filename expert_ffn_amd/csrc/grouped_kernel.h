@@ -7,16 +7,17 @@
 //   gate/up  h_r = silu(W_gate[e] x_t) * (W_up[e] x_t)
 //   down     O_s = W_down[e] h_r,   y_t = sum_j w_tj O_tj  in increasing j
 //
-// Both weight types are read in units of 128 bytes along the contraction: 64 bf16 or
-// 128 e4m3 elements.  A lane's operands of a unit are two 16-byte chunks, kk = 0, 1, at
-// byte 64 kk + 16 (lane / 16) of row lane % 16: two bf16 16x16x32 products, or one e4m3
-// 16x16x128 product (any order of k that both operands share gives the same sum).  The
+// All weight types are read in units of 128 bytes along the contraction: 64 bf16 or
+// 128 8-bit elements.  A lane's operands of a unit are two 16-byte chunks, kk = 0, 1, at
+// byte 64 kk + 16 (lane / 16) of row lane % 16: two bf16 16x16x32 or int8 16x16x64 products, or one
+// e4m3 16x16x128 product (any order of k that both operands share gives the same sum).  The
 // weights are the product's first operand, so that lane l of the result holds four
 // consecutive weight rows, 4 (l / 16) + i, of token l % 16.
 //
 // e4m3 operands carry a power of two for each block of 128 along the contraction (and
 // 128 weight rows), as the byte k + 127 that the scaled matrix instruction takes for
-// each row's 32 elements: all four get the block's.
+// each row's 32 elements: all four get the block's.  int8 operands carry one fp32 scale a row,
+// which meets the sums behind the contraction, so that these are whole numbers and exact.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -302,6 +303,9 @@ __device__ __forceinline__ uint32_t largest(u32x4 a) {  // bits of the largest |
     return m;
 }
 
+// Bound by memory: 16384 x 2048 in 19.8 us, 101 MB at 5.1 TB/s (a large copy here: 4.9); of 129 x 1408 4.1 us are
+// a launch, one load, five exchanges and the division.
+//
 // Rows of bf16 values to codes and scales; work group g of G.  L lanes a row (a power of two, from the row's
 // length: four vectors of eight values a lane, held between the maximum and the codes; longer rows than a work
 // group so holds are read again).
@@ -363,7 +367,7 @@ __global__ __launch_bounds__(256) void k_quant_rows_i8(const char* __restrict__ 
     quant_rows_i8(x, rows, K, q, s, blockIdx.x, gridDim.x);
 }
 
-// Codes and scales back to bf16: code * scale, rounded.
+// Codes and scales back to bf16: code * scale, rounded.  16384 x 2048 in 16.7 us: 101 MB at 6.0 TB/s.
 __global__ __launch_bounds__(256) void k_dequant_rows_i8(const uint8_t* __restrict__ q, const float* __restrict__ s,
                                                         int64_t rows, int K, char* __restrict__ x) {
     const int KB = (K + kBlk - 1) / kBlk, l = threadIdx.x & 15;
@@ -652,6 +656,8 @@ __device__ __forceinline__ TileAt find_tile(const int32_t* __restrict__ offset, 
 // flight leave registers for more waves: of 2 / 3 / 4 / 6 / 8 without SPLIT that e4m3 down took
 // 36 / 37 / 40 / 43 / 51 us, one of 1408 columns 36 / 33 / 34 / 36 / 44; e4m3 gate/up with SPLIT at 1 / 2 / 3 / 4
 // 72 / 70 / 76 / 79; bf16 differs by 1-3 %.
+// int8 products need no widening, and their sums no rounding: gate/up of the 32 tokens below in 24.3 us (113 MB at
+// 4.7 TB/s), down in 14.4 (57 MB at 3.9), in e4m3 25.7 and 16.3.
 // Memory bounds them: gate/up and down of 32 tokens (skewed over 128 bf16 experts of 2048 x 768) 49 + 27 us;
 // of one token on 8 e4m3 experts (25 + 13 MB in all) 9.4 + 6.9 us, where the latency of a launch and its first
 // loads is most.  Quantising h inside e4m3 down tiles, which spares a launch, made each of
@@ -826,7 +832,11 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 //
 // What they reach, PFLOP/s: gate/up of one expert's 4096 rows of 2048 x 8192 in bf16 1.03 (a library
 // product of that size 1.15), of 2048 rows of 4096 x 4096 1.19 (1.47); of 8 experts' 2048 rows each of
-// 2048 x 4096 1.18, in e4m3 2.1.  128 experts of 2048 x 768 with 32768 skewed rows reach 0.75: 43 % of
+// 2048 x 4096 1.18, in e4m3 2.1.  int8, PO/s: one expert's 16384 rows of 8192 x 2048 2.60, 4096 rows of 32768 x 2048
+// 2.71, 8192 of 4096 x 4096 2.41, 65536 of 1024 x 512 1.59 (8 units a tile; a library product of 8192^3: 2.1), with the matrix
+// units busy up to two thirds of the time at 2.0 GHz; operands that are all zero are 15 % faster, so power has a part.  What
+// a unit's reads, turns and wave priorities are changed to makes no difference that shows (int8 gate/up of 4096 tokens
+// 194-201 us).  128 experts of 2048 x 768 with 32768 skewed rows reach 0.75: 43 % of
 // their tiles' rows are missing (a unit costs the same), each compute unit has 5 or 6 tiles, and a
 // tile's change and results, 2 of its 32 units' time at this width, are not hidden.  Tiles of 128 rows
 // instead: 366 us for 297, and 165 for 134 in 8-bit down.

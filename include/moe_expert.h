@@ -305,20 +305,21 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  *   s_te = exp(l_te) / sum_e exp(l_te)       (MOE_SCORE_SOFTMAX)   or
  *          1 / (1 + exp(-l_te))              (MOE_SCORE_SIGMOID)
  *   the m experts with the largest s_te + b_e, in descending order, equal ones: lower id
- *   first (without b the order is that of l_te)
+ *   first (without b the order is that of l_te; an expert with b_e = -infinity is taken only where no other is left)
  *   w_tj = scale * s_tj / (renorm ? sum_j s_tj : 1)
  *   y_t  = sum_j w_tj FFN_tj(x_t) + sum over the shared experts of FFN(x_t)
- * with the expert calls' FFN and order of the sums: y is what moe_expert_dedup gives for the ids and weights
- * that the call hands back, rounded once more where the layer is bf16.  A token's ids and weights do not
- * depend on the other tokens of the pass.
+ * with the expert calls' FFN and order of the sums: y is what moe_expert_dedup (or, for one token without
+ * shared experts, moe_expert_perslot) gives for the ids and weights that the call hands back, rounded once more where
+ * the layer is bf16.  A token's ids and weights do not depend on the other tokens of the pass.  (moe_router_topk sums
+ * its logits in another order: two experts within its fp32 error of each other may change places.)
  *   desc     as for the expert calls (fp32 or bf16; every weight layout; n_shared; accumulate: y = round(y + result));
  *            N * d_model * element size < 2^31
- *   x, y     device [n][d_model], both of desc's type
+ *   x, y     device [n][d_model], both of desc's type; outputs overlap no input
  *   ids, w   device [n][m] int32 / fp32, written; either may be NULL
  *   info     device [3] int32 or NULL, as for moe_expert_perslot
  *   ws       device workspace of at least moe_pass_workspace_bytes(desc, n), 256-byte aligned, zero-filled before
  *            first use, as for the expert calls; one sized for n serves fewer tokens too
- * A logit that is NaN takes no part: its expert is never selected, and not in the softmax's sum; a slot left
+ * Logits should be finite.  One that is NaN takes no part: its expert is never selected, and not in the softmax's sum; a slot left
  * without a candidate gets id -1 and weight 0 (info[1] is then MOE_E_IDS).
  * Returns MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE (nothing enqueued), or MOE_E_HIP.
  */
@@ -353,10 +354,10 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
  * run on differ in their arithmetic.  Thin tiles (passes of few rows an expert) keep the terms
  * W_down h in fp32, so that y is rounded once.  Square tiles (from 8 to 16 rows an expert on average,
  * by type and size: moe_grouped_square) hand them on in 11 bits: each term is off by up to 2^-11 |w_tj W_down h|
- * (and 2^-39 of the largest of its 64 columns), whatever is left of their sum.  8-bit products on square tiles
+ * (and 2^-39 of the largest of its 64 columns), whatever is left of their sum.  e4m3 products on square tiles
  * go through a matrix instruction that cuts each product to 2^-13 of the largest of its 8 neighbours along the
- * contraction (which is small beside the 2^-4 of an operand's own quantisation); thin tiles do not cut.
- * Results are deterministic.
+ * contraction (which is small beside the 2^-4 of an operand's own quantisation); thin tiles do not cut,
+ * and int8 products add whole numbers.  Results are deterministic.
  *
  * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=
  * MOE_MAX_GROUP_SLOTS, d_model and d_ff <= MOE_MAX_GROUP_WIDTH, multiples of 8 (bf16)
