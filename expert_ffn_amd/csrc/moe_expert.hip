@@ -662,8 +662,8 @@ int router_check(const moe_layer_desc* desc, int32_t n) {
 // ---------------------------------------------------------------------------
 // moe_layer_pass
 // ---------------------------------------------------------------------------
-// parts of the contraction: a step a wave, at most kRouteParts and about a work group a compute unit for 16
-// tokens; of N, d and the type alone (see route_kernel.h)
+// parts of the contraction: a step a wave, at most kRouteParts and about a work group a compute unit for a
+// tile of tokens; of N, d and the type alone (see route_kernel.h)
 int route_parts(const moe_layer_desc* d) {
     const int step = d->dtype == MOE_BF16 ? 32 : 16, steps = (d->d_model + step - 1) / step;
     const int most = std::min(kRouteParts, std::max(1, kCUs / ((d->N + kTile - 1) / kTile)));
@@ -682,7 +682,7 @@ struct LayerSpace {
 };
 LayerSpace layer_space(const moe_layer_desc* d, int32_t n, size_t expert_bytes) {
     LayerSpace p;
-    p.expert = align_up((size_t)(MOE_MAX_TOKENS / kTile) * kLine * 4);
+    p.expert = align_up((size_t)(MOE_MAX_TOKENS / kRouteTokens) * kLine * 4);
     p.part = p.expert + align_up(expert_bytes);
     p.ids = p.part + align_up((size_t)route_parts(d) * n * route_row(d->N) * 4);
     p.w = p.ids + align_up((size_t)n * d->m * 4);
@@ -933,7 +933,7 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
     a.renorm = router->renorm != 0;
     a.scale = router->scale;
     const bool bf = desc->dtype == MOE_BF16;
-    const dim3 grid((desc->N + kTile - 1) / kTile, (n + kTile - 1) / kTile, a.KS);
+    const dim3 grid((desc->N + kTile - 1) / kTile, (n + kRouteTokens - 1) / kRouteTokens, a.KS);
     hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
     (void)hipGetLastError();
     const auto route = desc->N <= 64    ? (bf ? k_route<true, 1> : k_route<false, 1>)

@@ -4,17 +4,17 @@
 //   selected: the m largest s_te + b_e (without b: l_te, which orders them alike), equal ones: lower id
 //   w_tj = scale * s_tj / (renorm ? sum over the selected : 1)
 //
-// One work group of 16 waves for 16 experts x 16 tokens x one of KS parts of the contraction; its waves split
+// One work group of 16 waves for 16 experts x 4 tokens x one of KS parts of the contraction; its waves split
 // the part, so that at d = 2048 in bf16 each has one step: one round of loads.  The parts go to memory, and the work
 // group that arrives last on a token tile adds them, in order, and selects: a wave a token, m rounds of a
-// wave-wide maximum; or, of one or two tokens, by rank (an expert's place is the number of those before it), all
+// wave-wide maximum; or, of few tokens, by rank (an expert's place is the number of those before it), all
 // threads together.  How the contraction is cut depends on N, d and the type alone, so a token's routing does not
 // depend on the pass that it is in.
 //
-// Latency is the time: one token on 128 experts of d = 2048 takes 6.6 us, of which logits and arrival are 4.5 (a launch,
-// a round of loads, a store, an atomic); 16 tokens a work group 10.2, where four waves a SIMD select.  The two launches
-// of moe_router_topk are 7.3 for one token.  Half or a quarter of the parts: no difference for one token, 0.9 and 2.2 us
-// more for 32.
+// Latency is the time: one token on 128 experts of d = 2048 takes 6.3 us, of which logits and arrival are 4.5 (a launch,
+// a round of loads, a store, an atomic); 32 tokens 9.0, with 16 tokens a work group, where four waves a SIMD select,
+// 10.2.  The two launches of moe_router_topk are 7.3 for one token.  Half or a quarter of the parts: no difference for one
+// token, 0.9 and 2.2 us more for 32.
 #pragma once
 
 #include "expert_kernel.h"
@@ -24,10 +24,11 @@ namespace moe_k {
 constexpr int kRouteWaves = 16, kRouteThreads = 64 * kRouteWaves;
 constexpr int kRouteParts = 8;  // most parts of the contraction
 // Selection by rank for tiles of up to so many (token, expert) pairs: its work grows with tokens N^2 and all of the work
-// group shares it.  The launch by rank and by rounds, N = 128: one token 6.9 / 7.6 us, 16 tokens 18.2 / 11.4; N = 64,
-// 5 tokens 11.1 / 8.9 (as 128).
+// group shares it.  The launch by rank and by rounds at N = 128: one token 6.9 / 7.6 us, 5 tokens 11.1 / 8.9, 16 18.2 / 11.4
+// (with rounds slower than now).
 constexpr int kRankMost = 256;
-static_assert(kRouteWaves == kTile, "a wave a token of the tile");
+// Tokens of a work group: a quarter of the matrix operand's columns, so that the waves that select have a SIMD each.
+constexpr int kRouteTokens = 4;
 
 struct RouteArgs {
     const char* wr;     // [N][d]
@@ -107,22 +108,23 @@ template <bool BF16, int CL>
 __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     using F = Fmt<BF16>;
     __shared__ f32x4 red[kRouteWaves][64];
-    __shared__ int sel_e[kRouteWaves][MOE_MAX_SLOTS];
-    __shared__ float sel_l[kRouteWaves][MOE_MAX_SLOTS];
+    __shared__ int sel_e[kRouteTokens][MOE_MAX_SLOTS];
+    __shared__ float sel_l[kRouteTokens][MOE_MAX_SLOTS];
     __shared__ int s_last;
     constexpr int NK = 64 * CL;
     __shared__ __align__(16) uint32_t s_key[kRankMost];
     __shared__ float s_l[kRankMost];
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int lr = lane & 15, q = lane >> 4;
-    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile, ks = blockIdx.z, KS = a.KS;
+    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kRouteTokens, ks = blockIdx.z, KS = a.KS;
+    const int nt = min(kRouteTokens, a.n - t0);  // tokens of this tile
     const int S = (a.d + F::kStep - 1) / F::kStep;
     const int kb = ks * S / KS, kl = (ks + 1) * S / KS - kb;  // this part's steps
     const int s0 = kb + wave * kl / kRouteWaves, s1 = kb + (wave + 1) * kl / kRouteWaves;
     const auto rw = rsrc(a.wr, (uint32_t)a.N * a.d * F::kEsize);
     const auto rx = rsrc(a.x, (uint32_t)a.n * a.d * F::kEsize);
     const uint32_t la = e0 + lr < a.N ? (uint32_t)(e0 + lr) * a.d * F::kEsize : kOOB;
-    const uint32_t lb = t0 + lr < a.n ? (uint32_t)(t0 + lr) * a.d * F::kEsize : kOOB;
+    const uint32_t lb = lr < nt ? (uint32_t)(t0 + lr) * a.d * F::kEsize : kOOB;
     f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int kAhead = 4;
     for (int s = s0; s < s1; s += kAhead) {
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
         // experts e0 + 4 q .. + 3 of token t0 + lr (past N: zeros)
         const uint32_t t = t0 + lr, e = e0 + 4 * q;
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rp,
-                                               e < NP && (int)t < a.n ? ((ks * a.n + t) * NP + e) * 4u : kOOB, 0, kSc1);
+                                               e < NP && lr < nt ? ((ks * a.n + t) * NP + e) * 4u : kOOB, 0, kSc1);
         stores_complete();
         if (lane == 0) {
             int32_t* count = a.count + kLine * blockIdx.y;
@@ -162,12 +164,12 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     }
     __syncthreads();  // the loads (sc1) below go out after the last arrival was seen
     if (!s_last) return;
-    const int t = t0 + wave, nt = min(kTile, a.n - t0);  // this wave's token, tokens of the tile
+    const int t = t0 + wave;  // this wave's token
     const bool live = wave < nt;
     const bool rank = nt * NK <= kRankMost;
     if (!rank && !live) return;  // (by rounds there is no barrier)
-    int* se = sel_e[wave];
-    float* sl = sel_l[wave];
+    int* se = sel_e[live ? wave : 0];
+    float* sl = sel_l[live ? wave : 0];
     float l[CL], top = -INFINITY, Z = 1.f;  // logits; the largest; sum of exp(l - top)
     uint32_t key[CL];
     if (live) {
