@@ -77,23 +77,39 @@ void run_group(Group g, hipStream_t st) {
 // bf16 230 / 229 / 235 / 248 against 227 / 228 / 229 / 230, e4m3 129 / 134 / 139 / 148 against 144 / 146 / 147 / 148;
 // with popularity falling as 1 / rank^1.1, bf16 147 / 173 / 191 / 213 against 146 / 160 / 159 / 165, e4m3
 // 93 / 107 / 118 / 130 against 100 / 113 / 112 / 117.
-// int8 runs thin tiles without e4m3's widening: whole passes at a mean of 12 / 14 / 16 / 20 rows, thin against square:
-//     128 of 2048 x 768, ids uniform   134 / 142 / 153 / 174   145 / 146 / 147 / 150
-//       popularity 1 / rank^1.1        120 / 130 / 135 / 161   111 / 124 / 120 / 142
-//     64 of 2048 x 1408, uniform       120 / 129 / 139 / 155   130 / 130 / 131 / 134
-//       1 / rank^1.1                   117 / 123 / 138 / 147   113 / 119 / 131 / 135
-//     8 of 4096 x 14336, uniform       270 / 308 / 346 / 376   298 / 300 / 301 / 303
+// int8 runs thin tiles without e4m3's widening: whole passes at a mean of 10 / 12 / 14 / 16 / 20 rows, thin against square:
+//     128 of 2048 x 768, ids uniform   128 / 134 / 142 / 153 / 174   144 / 145 / 146 / 147 / 150
+//       popularity 1 / rank^1.1        105 / 120 / 130 / 135 / 161   108 / 111 / 124 / 120 / 142
+//     64 of 2048 x 1408, uniform       118 / 120 / 129 / 139 / 155   129 / 130 / 130 / 131 / 134
+//       1 / rank^1.1                   112 / 117 / 123 / 138 / 147   110 / 113 / 119 / 131 / 135
+//     8 of 4096 x 14336, uniform       263 / 270 / 308 / 346 / 376   297 / 298 / 300 / 301 / 303
+//     105 of 2400 x 1504, one a token, 1 / rank^1.23, 13.5 rows      166 against 98
+// so from 12, where even routing loses what skewed gains.  Small layers leave most compute units without a square tile: one takes about 1.1 us a unit and 5, while
+// thin tiles share the products out, 256 rows x columns a unit at 6000 a us (of one matrix; gate/up, down with twice the
+// columns a tile a third less).  Gate/up at a mean of 32 / 64 / 128 / 256 / 512 rows, ids uniform, thin against square:
+//     16 of 1024 x 512    15 / 15 / 22 / 34 /  59   21 / 23 / 25 / 29 / 31
+//     8 of 512 x 512      14 / 14 / 14 / 16 /  24   18 / 19 / 21 / 23 / 24
+//     32 of 1024 x 1024   24 / 35 / 60 / 110 / 210  24 / 38 / 39 / 50 / 72
+//     4 of 2048 x 512     14 / 14 / 15 / 20 /  31   28 / 30 / 33 / 37 / 38
+//     8 of 2560 x 1536    21 / 32 / 52 / 93 / 176   32 / 35 / 39 / 44 / 48
+// and down: 16 of 1024 x 512 15 / 15 / 21 / 30 / 52 and 17 / 19 / 22 / 28 / 33; 8 of 2560 x 1536 18 / 27 / 45 / 80 / 151 and
+// 25 / 28 / 32 / 37 / 40.
 // The mean counts padding, as only the device knows the groups.  4096 tokens of 8 slots of which 32 tokens are
 // live, thin against square, whole passes of the first layer: bf16 296 / 214, e4m3 232 / 151 (a thin tile's work
 // groups are launched for every row there could be).  900 of 1000 rows on one of the 128 experts: 179 / 166 and 103 / 107.
 // Square tiles' loads run up to two units ahead into the next tile, which takes four
 // units a tile, and have buffer offsets of 31 bits (x, or a matrix and the rows that its last
 // tile has beyond it); thin tiles address all of memory.
-bool square(const Args& a, int type, bool gu) {
-    const int least = type == kBf16 ? 8 : type == kFp8 ? 12 : 14;
-    const int64_t kby = (int64_t)a.K * elem_size(type), most = (1ll << 31) - 4096;
+// Fewest slots of square tiles.
+int64_t square_from(const Args& a, int type, bool gu) {
     const int64_t tc = gu ? kTN / 2 : kTN, tiles = std::min(a.N, a.S) * ((a.R + tc - 1) / tc);
-    return kby > 3 * kUnit && a.S >= (tiles >= 2 * kCUs ? least : 16) * (int64_t)a.N && (a.R + kTN) * kby <= most &&
+    if (type != kInt8) return (tiles >= 2 * kCUs ? (type == kFp8 ? 12 : 8) : 16) * (int64_t)a.N;
+    const int64_t U = (a.K + kUnit - 1) / kUnit, work = gu ? 768000 : 1000000;  // rows x columns: work (1.1 + 5 / U)
+    return std::max((int64_t)12 * a.N, work * (11 * U + 50) / (10 * U * a.R) + 1);
+}
+bool square(const Args& a, int type, bool gu) {
+    const int64_t kby = (int64_t)a.K * elem_size(type), most = (1ll << 31) - 4096;
+    return kby > 3 * kUnit && a.S >= square_from(a, type, gu) && (a.R + kTN) * kby <= most &&
            (gu ? (int64_t)(a.S / a.m) * kby : kTM * kby) <= most;
 }
 
@@ -129,9 +145,13 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
         return a;
     };
     p.queue = take(2 * kQueue * 4);  // gate/up's, then down's
-    // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert), fp16 from square ones
+    // O: fp32 from thin tiles (of shapes that square tiles take, only below 16 rows an expert, or, int8, where those
+    // begin), fp16 from square ones
     size_t o = S * d->d_model * 4;
-    if (square_down(d, n)) o = std::max(o / 2, (size_t)16 * d->N * d->d_model * 4);
+    if (square_down(d, n)) {
+        const size_t thin = i8 ? square_from(shape_of(d->N, d->m, n, d->d_model, d->d_ff), kInt8, false) : (size_t)16 * d->N;
+        o = std::max(o / 2, thin * d->d_model * 4);
+    }
     // gate/up's fp32 h (int8: bf16; quantised before down begins), then O
     p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : i8 ? S * d->d_ff * 2 : 0));
     p.os = take(S * ((d->d_model + 63) / 64));

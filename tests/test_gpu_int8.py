@@ -236,7 +236,8 @@ def test_where_the_form_of_a_pass_changes(N, m, d, f, n):
     _check_pass(case, _randn(n, n, d).to(BF).cuda(), ids, w, "pass %s" % ((N, m, d, f, n),))
 
 
-@pytest.mark.parametrize("counts", [[300, 0, 1, 257, 64, 0, 192, 33], [0, 0, 700, 0, 0, 0, 0, 0]])
+@pytest.mark.parametrize("counts", [[300, 0, 1, 257, 64, 0, 192, 33], [1200, 0, 1, 1030, 300, 64, 897, 257],
+                                    [0, 0, 4000, 0, 0, 0, 0, 0]])
 @pytest.mark.parametrize("layout", ["plain", "tiled"])
 def test_many_rows(counts, layout):
     say("int8 many rows", counts, layout)
@@ -245,18 +246,32 @@ def test_many_rows(counts, layout):
     n = ids.numel()
     ids = ids[torch.randperm(n, generator=torch.Generator().manual_seed(4))].to(torch.int32)[:, None].cuda().contiguous()
     case = Case(N, 1, d, f, layout=layout)
+    assert case.square(n, efa.MOE_MAT_GATE_UP) == case.square(n, efa.MOE_MAT_DOWN) == (n > 1000)
     _check_pass(case, _randn(9, n, d).to(BF).cuda(), ids, _randn(2, n, 1).cuda(), "rows")
 
 
-@pytest.mark.parametrize("n", [3, 300])
-def test_largest_codes_do_not_overflow(n):
+def test_square_tiles_of_odd_sizes():
+    """Contractions of a few units and part of one, columns that end inside a tile, skewed rows, several slots a token."""
+    say("int8 square odd sizes")
+    for N, m, d, f, n, layout in ((6, 3, 400, 1040, 3000, "plain"), (12, 5, 1104, 432, 2100, "plain"),
+                                  (5, 2, 448, 3200, 1500, "tiled"), (24, 8, 2064, 1008, 300, "plain")):
+        case = Case(N, m, d, f, layout=layout, seed=N)
+        x = (_randn(n, n, d) * torch.exp(_randn(3, 1, d))).to(BF).cuda()
+        ids, w = _ids(n + 1, n, m, N, zipf=1.0, pad=n // 10)
+        assert case.square(n, efa.MOE_MAT_GATE_UP) and case.square(n, efa.MOE_MAT_DOWN)
+        _check_pass(case, x, ids, w, "square %s" % ((N, m, d, f, n),))
+
+
+@pytest.mark.parametrize("n,f,square", [(3, 16, False), (300, 16, False), (4000, 256, True)])
+def test_largest_codes_do_not_overflow(n, f, square):
     """Every code 127 over the longest contraction: sums of 65536 * 127^2, above 2^24 by far."""
     say("int8 longest", n)
-    N, d, f = 2, 65536, 16
+    N, d = 2, 65536
     q = torch.full((N, f, d), 127, dtype=I8, device="cuda")
     s = torch.full((N, f), 2.0 ** -20, device="cuda")
     dn = (torch.full((N, d, f), -127, dtype=I8, device="cuda"), torch.full((N, d), 2.0 ** -7, device="cuda"))
     layer = efa.Int8Layer((q, s), (q, s), dn, m=1)
+    assert efa.grouped_square(layer, n, efa.MOE_MAT_GATE_UP) == square
     x = torch.full((n, d), 127.0, dtype=BF, device="cuda")
     ids = (torch.arange(n, dtype=torch.int32, device="cuda") % 2)[:, None].contiguous()
     g = efa.group_slots(ids, N)
@@ -266,15 +281,16 @@ def test_largest_codes_do_not_overflow(n):
     assert (h.q == 127).all()
     assert ((h.scale.double() * 127 - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want).all()
     y = efa.grouped_down(layer, h, ids, torch.ones(n, 1, device="cuda"), g)
-    o = -16.0 * 127 * 127 * 2.0 ** -7 * h.scale.double()[:, None].expand(n, d)
+    o = -float(f) * 127 * 127 * 2.0 ** -7 * h.scale.double()[:, None].expand(n, d)
     o = o[torch.argsort(g.slot_by_expert.long())]
     assert ((y.double() - o).abs() <= (2.0 ** -8 + 2.0 ** -10) * o.abs()).all()
 
 
 def test_rows_that_are_not_finite_stay_their_own():
     say("int8 nan rows")
-    for n in (6, 400):
+    for n in (6, 400, 2500):
         case = Case(4, 2, 576, 640)
+        assert case.square(n, efa.MOE_MAT_DOWN) == (n == 2500)
         x = _randn(1, n, 576).to(BF).cuda()
         ids, w = _ids(2, n, 2, 4)
         want = efa.expert_grouped(case.layer, x, ids, w)
@@ -306,7 +322,7 @@ def test_no_valid_id_and_ids_twice():
     _check_pass(case, x, ids, torch.rand(4, 3, device="cuda"), "ids twice")
 
 
-@pytest.mark.parametrize("n", [9, 600])
+@pytest.mark.parametrize("n", [9, 600, 2500])
 def test_accumulate_and_rows_behind_the_last(n):
     say("int8 accumulate", n)
     case = Case(8, 2, 576, 640)
@@ -336,7 +352,7 @@ def test_a_layer_of_always_on_experts():
 def test_other_stream_and_captured():
     say("int8 streams and graphs")
     case = Case(16, 4, 576, 640, layout="plain")
-    for n in (7, 300):
+    for n in (7, 300, 1200):
         x = _randn(1, n, 576).to(BF).cuda()
         ids, w = _ids(3, n, 4, 16)
         want = efa.expert_grouped(case.layer, x, ids, w)

@@ -80,12 +80,25 @@ def test_pointers_and_workspace():
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
 
 
-@pytest.mark.parametrize("N,m,d,f", [(8, 2, 576, 640), (128, 8, 2048, 768), (1024, 1, 16, 16), (8, 2, 4096, 14336)])
+@pytest.mark.parametrize("N,m,d,f", [(1, 1, 4096, 1024), (4, 2, 2048, 512), (8, 2, 576, 640), (128, 8, 2048, 768), (1024, 1, 16, 16), (8, 2, 4096, 14336)])
 def test_a_longer_pass_needs_no_less(N, m, d, f):
     L = _abi.lib()
     desc = _desc(N=N, m=m, d_model=d, d_ff=f)
     sizes = [L.moe_grouped_workspace_bytes(ctypes.byref(desc), n) for n in list(range(1, 200)) + list(range(200, 9000, 61))]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_where_square_tiles_begin():
+    """From 12 slots an expert, and in small layers from the rows x columns that make up for the compute units
+    without a tile."""
+    L = _abi.lib()
+    for N, m, d, f, mat, first in ((128, 8, 2048, 768, 0, 12 * 128), (128, 8, 2048, 768, 1, 12 * 128),
+                                   (16, 2, 1024, 512, 0, 2588), (16, 2, 1024, 512, 1, 2295), (1, 1, 4096, 1024, 0, 943)):
+        desc = _desc(N=N, m=m, d_model=d, d_ff=f)
+        n = -(-first // m)
+        assert [L.moe_grouped_square(ctypes.byref(desc), k, mat) for k in (n - 1, n)] == [0, 1], (N, d, f, mat)
+    # contractions of up to three units never
+    assert L.moe_grouped_square(ctypes.byref(_desc(N=1, m=1, d_model=384, d_ff=4096)), 1 << 20, 0) == 0
 
 
 def test_rows():
