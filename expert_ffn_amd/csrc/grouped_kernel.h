@@ -825,6 +825,9 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 // (each read has ended before the barrier of Ra or Rb, and wm = 1 reads one phase later, before
 // these).  They are waited for at the end of Mb (the last 128 rows of the next unit) and of Rb
 // (the rest of it), one phase before wm = 0 reads them: the counts are of what was issued since.
+// (In a tile's first unit they include the stores of the tile before, which are so waited for too: counts for
+// that unit alone, chosen by branches, cost more, int8 down of 2777 tokens 112 us for 109, e4m3 gate/up of 2048 wide
+// ones 523 for 502, bf16 630 for 619 in down.)
 // (Figures of 8-bit down in comparisons here and below are from when it handed its terms on in bf16, about
 // 12 us less.)  With the last 128 rows read in Rb alone and loaded in Ma, gate/up of 4096 tokens (128 bf16 experts of
 // 2048 x 768) took 298 us for 292, 8-bit down 133 for 128; with the first 128 rows also read a phase ahead
@@ -1185,18 +1188,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     block_barrier();
     if (wm) block_barrier();
 
-    // a wave's stores of a tile: the same number whatever its rows, those of no row are dropped by their bounds
-    constexpr auto stores_of = [](int nb) { return GU ? (FP8 ? nb / 2 + 1 : nb) : 2 * nb + (nb + 3) / 4; };
-    int par = 0;      // the stage of the unit at hand
-    int before = 0;   // row blocks of a wave in the tile before, whose stores may still be on their way
-    auto wait_past = [&](auto n, int nb) {
-        constexpr int N = decltype(n)::value;
-        if (nb == 0) wait_vm<N>();
-        else if (nb == 2) wait_vm<N + stores_of(2)>();
-        else if (nb == 4) wait_vm<N + stores_of(4)>();
-        else if (nb == 6) wait_vm<N + stores_of(6)>();
-        else wait_vm<N + stores_of(8)>();
-    };
+    int par = 0;  // the stage of the unit at hand
     int xpar = 0, spar = 0;  // where the scale bytes of the rows and weights at hand are
     auto tile = [&](auto nb) {
         constexpr int NB = decltype(nb)::value, H = NB < 4 ? NB : 4;  // row blocks of a wave; of Ra and Ma
@@ -1329,7 +1321,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             load_weights(wr, ub, here, 1);
             load_rows(xa, gather, ub, here, 0);
             wait_lds();
-            wait_past(std::integral_constant<int, 5>(), u == 0 ? before : 0);
+            wait_vm<5>();
             block_barrier();
             // Mb
             auto last = [&] {
@@ -1509,7 +1501,6 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                                                      0, 0);
             }
         }
-        before = NB;
         spar ^= 1;
         return pn;
     };
@@ -1523,7 +1514,6 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         p = Place{uni(pn.e), uni(pn.r0), uni(pn.rows), uni(pn.ct)};
         after = uni(after);
         par = uni(par);
-        before = uni(before);
         xpar = uni(xpar);
         spar = uni(spar);
     }
