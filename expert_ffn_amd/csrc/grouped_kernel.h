@@ -1197,7 +1197,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         int got = 0;
         int slot_n = 0;           // the next tile's, as asked for
         uint8_t wsn[2] = {0, 0};  // its weight scale bytes
-        Rows xa = rows_of(p), xb = xa;  // the first and the last 128 rows
+        Rows xa = rows_of(p);
         Weights wr = weights_of(p);
         Sum4<T> acc[NB][4];
 #pragma unroll
@@ -1244,12 +1244,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));  // they stay in this phase
             };
             // Ra
-            int ua = u + 1, ub = u + 2;  // past the last unit: the next tile's first
-            if (ua >= U) {
-                xb = rows_of(pn);
-                if (GU) address(2, 4);
-                ua = 0;
-            }
+            const int ua = u + 1 < U ? u + 1 : 0;  // past the last unit: the next tile's first
+            int ub = u + 2;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -1259,8 +1255,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         (TILED ? (wn * 4 + j) * 2048 + kk * 1024 + lane * 16 : swz(wn * 64 + j * 16 + lr, kk * 4 + q)));
 #pragma unroll
             for (int i = 0; i < H; ++i) read_rows(i);
-            load_rows(xb, gather, ua, there, 2);
-            load_rows(xb, gather, ua, there, 3);
+            load_rows(xa, gather, ua, there, 2);
+            load_rows(xa, gather, ua, there, 3);
             if (FP8) {
                 const u32x2 v = *reinterpret_cast<const u32x2*>(&lds.xs[xpar][u & 3][wm * 128 + lr * 8]);
                 ex[0] = v[0];
@@ -1276,33 +1272,35 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             });
             block_barrier();
             // Rb
-            if (u == 0) {
-                pn = take(after);
-                if (GU) slot_n = ask(pn);
-                if (tid == 0) {
-                    int at = xcd * kLine;
-                    asm volatile("" : "+v"(at));  // a lane's address: a wave's would be waited for at once
-                    got = atomicAdd(&arg()->queue[at], 1);
+            if (__builtin_expect(u < 2 || ub == U, 0)) {  // (one branch for most units)
+                if (u == 0) {
+                    pn = take(after);
+                    if (GU) slot_n = ask(pn);
+                    if (tid == 0) {
+                        int at = xcd * kLine;
+                        asm volatile("" : "+v"(at));  // a lane's address: a wave's would be waited for at once
+                        got = atomicAdd(&arg()->queue[at], 1);
+                    }
+                    if (FP8) {
+                        wsn[0] = weight_scale(pn, tid);
+                        if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
+                    }
+                    if (I8) scale = tile_scale(p);
+                } else if (u == 1) {
+                    if (FP8) {
+                        keep_weight_scale(spar ^ 1, tid, wsn[0]);
+                        if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
+                    }
+                    if (I8) lds.scale[tid / kTM][tid & (kTM - 1)] = scale;  // (read at the tile's end, long before the next's)
+                    if (GU) keep(slot_n);
+                    if (tid == 0) lds.after = got + 2 * step;
+                } else if (ub == U) {
+                    wr = weights_of(pn);
+                    xa = rows_of(pn);
+                    if (GU) address(0, 4);
+                    row_address(pn);
+                    after = uni(lds.after);
                 }
-                if (FP8) {
-                    wsn[0] = weight_scale(pn, tid);
-                    if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
-                }
-                if (I8) scale = tile_scale(p);
-            } else if (u == 1) {
-                if (FP8) {
-                    keep_weight_scale(spar ^ 1, tid, wsn[0]);
-                    if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
-                }
-                if (I8) lds.scale[tid / kTM][tid & (kTM - 1)] = scale;  // (read at the tile's end, long before the next's)
-                if (GU) keep(slot_n);
-                if (tid == 0) lds.after = got + 2 * step;
-            } else if (ub == U) {
-                wr = weights_of(pn);
-                xa = rows_of(pn);
-                if (GU) address(0, 2);
-                row_address(pn);
-                after = uni(lds.after);
             }
             if (ub >= U) ub -= U;
 #pragma unroll
