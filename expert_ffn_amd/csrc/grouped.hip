@@ -272,9 +272,9 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     if (!u_err) a.row_of = row_of;  // (a pass's grouping has left them)
     launch_product<T, false>(a, d->flags & MOE_FLAG_TILED, st);
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
-    hipLaunchKernelGGL(square_down(d, n) ? k_combine<false> : k_combine<true>,
+    hipLaunchKernelGGL((square_down(d, n) ? k_combine<false, T == kInt8> : k_combine<true>),
                        dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
-                       reinterpret_cast<const char*>(o), os, row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       reinterpret_cast<const char*>(o), os, reinterpret_cast<const float*>(hs), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 

@@ -890,6 +890,17 @@ __device__ __forceinline__ void block_barrier() {
 // largest into [2^14, 2^15).  `byte` is its exponent's byte in fp32, 14 at least so that 2^127 scales it.
 __device__ __forceinline__ int term_byte(uint32_t largest) { return max((int)(largest >> 23), 14); }
 
+// int8: by what the largest scale of the 64 columns could make of K codes, which needs no look at the sums, and without
+// the row's scale, which k_combine multiplies by.  |sum| <= 127^2 K < 2^b, so |sum| times the scale comes below 2^15 (at
+// byte 254 below 2^16 where it is finite in fp32); sums are whole, so a column whose scale is 2^(b - 28) of the largest or more
+// keeps 11 bits of every term, and all are right to 2^-39 of 2^b times the largest scale (2^-126 at least).  With the
+// largest term of each row as above int8 down of 4096 x 8 tokens took 142 us for 134, of 8191 x 8 236 for 220, of 2777 x 6
+// 110 for 108.
+__device__ __forceinline__ int term_byte_i8(uint32_t largest_scale, int K) {
+    const int b = 32 - __builtin_clz(127u * 127u * (uint32_t)K);
+    return min(max((int)(largest_scale >> 23) + b, 14), 254);
+}
+
 // The largest of the four lanes l % 16 + 16 k.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     const u32x2 a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
@@ -1148,14 +1159,13 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     auto keep_weight_scale = [&](int par, int i, uint8_t v) {
         if (i < 2 * KB) lds.ws[par][i >= KB][i >= KB ? i - KB : i] = v;
     };
-    // int8: a scale a thread, those of the tile's rows, then of its weight rows.  (At a tile's first unit
-    // lds.token still has its own tokens.)
+    // int8: a scale a thread, gate/up those of the tile's rows, then of its weight rows, down of its weight rows.  (At a
+    // tile's first unit lds.token still has its own tokens.)
     auto tile_scale = [&](const Place& t) {
         const int c = tid & (kTM - 1), half = GU ? c >> 7 : 0;
-        const float* rows = reinterpret_cast<const float*>(arg()->xs);
         const float *s0 = reinterpret_cast<const float*>(arg()->s0), *s1 = GU ? reinterpret_cast<const float*>(arg()->s1) : s0;
-        const float* at = tid < kTM ? rows + (GU ? lds.token[c] : row_of(t))
-                                    : (half ? s1 : s0) + ((int64_t)t.e * a.R + min(t.ct * TC + (GU ? c & 127 : c), a.R - 1));
+        const float* at = (half ? s1 : s0) + ((int64_t)t.e * a.R + min(t.ct * TC + (GU ? c & 127 : c), a.R - 1));
+        if (GU && tid < kTM) at = reinterpret_cast<const float*>(arg()->xs) + lds.token[c];
         return *at;
     };
     const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
@@ -1440,43 +1450,60 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
             const int c0 = p.ct * TC + wn * 64;  // this wave's 64 columns, a block of O
             int byte[NB];
-            f32x4 sw[4];
+            f32x4 sw[4];  // int8: the columns' scales times the terms' power of two
+            int byte_i8 = 0;
             if constexpr (I8) {
+                uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sw[j] = *reinterpret_cast<const f32x4*>(&lds.scale[1][wn * 64 + j * 16 + 4 * eq]);
+                for (int j = 0; j < 4; ++j) {
+                    sw[j] = *reinterpret_cast<const f32x4*>(&lds.scale[1][wn * 64 + j * 16 + 4 * eq]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(sw[j][k])));
+                }
+                byte_i8 = term_byte_i8(quad_max(m), a.K);
+                const float inv = __uint_as_float((uint32_t)(268 - byte_i8) << 23);  // 2^(141 - byte)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sw[j] *= inv;
             }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                float v[4][4];  // read once from the accumulators
-                uint32_t m = 0;
-                float sx = 0.f;
-                if constexpr (I8) sx = lds.scale[0][(i * 2 + wm) * 16 + er];
+                auto keep16 = [&](int j, const float (&o)[4]) {
+                    *reinterpret_cast<u32x2*>(turn + er * 144 + j * 32 + 8 * eq) = u32x2{f16_pair(o[0], o[1]), f16_pair(o[2], o[3])};
+                };
+                if constexpr (I8) {
+                    byte[i] = byte_i8;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j) {
+                        float o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (I8) v[j][k] = (float)acc[i][j][k] * sw[j][k];  // (times sx below)
-                        else v[j][k] = acc[i][j][k];
-                        asm volatile("" : "+v"(v[j][k]));
-                        m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
+                        for (int k = 0; k < 4; ++k) o[k] = (float)acc[i][j][k] * sw[j][k];
+                        keep16(j, o);
                     }
-                if (__any(m >= 0x7f800000u)) {  // rare: what is not finite takes no part
-                    m = 0;
+                } else {
+                    float v[4][4];  // read once from the accumulators
+                    uint32_t m = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(v[j][k])));
-                }
-                m = quad_max(m);
-                if constexpr (I8) m = __float_as_uint(mag(__uint_as_float(m) * sx));
-                byte[i] = term_byte(m);
-                float inv = __uint_as_float((uint32_t)(268 - byte[i]) << 23);  // 2^(141 - byte)
-                if constexpr (I8) inv *= sx;
+                        for (int k = 0; k < 4; ++k) {
+                            v[j][k] = acc[i][j][k];
+                            asm volatile("" : "+v"(v[j][k]));
+                            m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
+                        }
+                    if (__any(m >= 0x7f800000u)) {  // rare: what is not finite takes no part
+                        m = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float* o = v[j];
-                    *reinterpret_cast<u32x2*>(turn + er * 144 + j * 32 + 8 * eq) =
-                        u32x2{f16_pair(o[0] * inv, o[1] * inv), f16_pair(o[2] * inv, o[3] * inv)};
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(v[j][k])));
+                    }
+                    byte[i] = term_byte(quad_max(m));
+                    const float inv = __uint_as_float((uint32_t)(268 - byte[i]) << 23);  // 2^(141 - byte)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float o[4] = {v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv};
+                        keep16(j, o);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -1546,10 +1573,11 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 // The error of y in that bf16 down is 0.0023 (norm) with bf16 terms and 0.0017 here, that of rounding y.
 // (Long passes whose contraction is too short for square tiles pay for fp32: down of 4096 x 8 tokens of 16
 // experts, 1024 x 176 in bf16, 128 -> 136 us, 1024 x 368 in e4m3 142 -> 153.)
-// What is not finite is itself in fp16 and takes no part in a block's largest.
+// What is not finite is itself in fp16 and takes no part in a block's largest.  ROWS (int8): O still lacks its row's `scale`.
 // info (may be null): U, ids status, MOE_OK.
-template <bool F32>
+template <bool F32, bool ROWS = false>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const uint8_t* __restrict__ os,
+                                                const float* __restrict__ scale,
                                                 const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
                                                 int m, int N, int d,
@@ -1567,17 +1595,18 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
         for (int j0 = 0; j0 < m; j0 += 64) {
             // this lane's slot: its row (-1: none) and weight
             int row = -1;
-            float wj = 0.f;
+            float wj = 0.f, sj = 0.f;
             if (j0 + lane < m) {
                 const int64_t slot = t * m + j0 + lane;
                 const int id = ids[slot], r = min(max(row_of[slot], 0), last);
                 wj = w[slot];
                 row = id >= 0 && id < N ? r : -1;
+                if (ROWS) sj = scale[r];
             }
             uint64_t live = __ballot(row >= 0);
             while (live) {
                 u32x4 o[8][F32 ? 2 : 1];
-                float wt[8];
+                float wt[8], sx[8];
                 int rows8 = 0;  // of lane 8 k + b: row k of the eight
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -1585,10 +1614,11 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                     live &= live - 1;
 #pragma unroll
                     for (auto& p : o[k]) p = u32x4{0u, 0u, 0u, 0u};
-                    wt[k] = 0.f;
+                    wt[k] = sx[k] = 0.f;
                     if (l < 64) {
                         const int64_t r = __builtin_amdgcn_readlane(row, l);
                         wt[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(wj), l));
+                        if (ROWS) sx[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(sj), l));
                         const u32x4* at = reinterpret_cast<const u32x4*>(O + (r * d + c) * (F32 ? 4 : 2));
                         if (in) o[k][0] = at[0];
                         if constexpr (F32) {
@@ -1610,8 +1640,9 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                             s[4 + v] += wt[k] * __uint_as_float(o[k][1][v]);
                         } else {
                             const f32x2 t2 = f16_values(o[k][0][v]);
-                            s[2 * v] += wt[k] * (t2[0] * f);
-                            s[2 * v + 1] += wt[k] * (t2[1] * f);
+                            const float o0 = t2[0] * f, o1 = t2[1] * f;
+                            s[2 * v] += wt[k] * (ROWS ? o0 * sx[k] : o0);
+                            s[2 * v + 1] += wt[k] * (ROWS ? o1 * sx[k] : o1);
                         }
                     }
                 }

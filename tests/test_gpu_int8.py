@@ -401,3 +401,47 @@ def test_near_the_bf16_layer():
     # (largest about 6), of W_down 0.8 %: 2.3 % together; half as much again for the spread of the maxima.
     assert (a - b).norm() <= 0.035 * a.norm()
     assert _abi.MOE_INT8 == 4
+
+
+@pytest.mark.parametrize("layout", ["plain", "tiled"])
+@pytest.mark.parametrize("top,sx", [(1.0, 2.0 ** -10), (2.0 ** 106, 2.0 ** -118), (2.0 ** -126, 2.0 ** 118)])
+def test_terms_of_square_tiles_beside_columns_of_any_scale(top, sx, layout):
+    """Columns whose scales are far below their neighbours', zero or NaN, and scales near the ends of fp32.  With
+    127^2 K < 2^b and S the largest scale of a term's 64 columns (2^-126 at least) the term is rounded to fp16 in steps of at most
+    2^-10 of itself, or of 2^-24 (2^b S) 2^-14 where fp16 is subnormal: half of either, and fp32's roundings before
+    and behind (three, 2^-24 each), then bf16's."""
+    say("int8 scales", top, layout)
+    N, d, K, n = 2, 576, 512, 9000
+    b = 23  # 127^2 * 512 < 2^23
+    g = torch.Generator().manual_seed(5)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, dtype=torch.int32).to(I8).cuda()
+    ratio = torch.tensor([1.0, 2.0 ** -3 * 1.3, 2.0 ** -9 * 1.7, 2.0 ** -15 * 1.1, 2.0 ** -19, 2.0 ** -24 * 1.9, 2.0 ** -40, 0.0])
+    sd = (top * ratio.double().repeat(d // 8)[None] * torch.tensor([[1.0], [0.77]])).float()
+    sd[1, 64:128] *= 2.0 ** -12  # another largest in one block
+    sd[0, 70] = float("nan")
+    sd = sd.cuda()
+    any_q = (codes(N, K, d), torch.ones(N, K, device="cuda"))
+    wd = codes(N, d, K)
+    wd[:, :, 1:] = torch.where(torch.arange(d, device="cuda")[None, :, None] % 5 == 0, 0, wd[:, :, 1:])  # sums of one product
+    layer = efa.Int8Layer(any_q, any_q, (wd, sd), m=1)
+    assert efa.grouped_square(layer, n, efa.MOE_MAT_DOWN)
+    if layout == "tiled":
+        layer = layer.tiled_copy()
+    ids = (torch.arange(n, dtype=torch.int32, device="cuda") % 2)[:, None].contiguous()
+    gr = efa.group_slots(ids, N)
+    h = efa.Quantized(codes(n, K), torch.full((n,), sx, device="cuda") * (1 + 0.9 * torch.rand(n, generator=g).cuda()))
+    y = efa.grouped_down(layer, h, ids, torch.ones(n, 1, device="cuda"), gr).double()
+    row = torch.empty(n, dtype=torch.long, device="cuda")
+    row[gr.slot_by_expert.long()] = torch.arange(n, device="cuda")
+    for e in range(N):
+        t = torch.arange(e, n, 2, device="cuda")
+        sums = h.q[row[t]].double() @ wd[e].double().T
+        s = h.scale[row[t]].double()[:, None]
+        want = sums * sd[e].double() * s
+        most = torch.nan_to_num(sd[e]).double().view(-1, 64).amax(1).clamp(min=2.0 ** -126).repeat_interleave(64)
+        tol = (2.0 ** -11 + 3 * 2.0 ** -24) * want.abs() + 2.0 ** -39 * 2.0 ** b * most * s
+        tol = tol + 2.0 ** -8 * (want.abs() + tol) + 1e-40
+        bad = torch.isnan(sd[e])
+        assert torch.isnan(y[t][:, bad]).all()
+        _within(y[t][:, ~bad], want[:, ~bad], tol[:, ~bad], "scales %g expert %d" % (top, e))
+        assert (y[t][:, sd[e] == 0] == 0).all()
