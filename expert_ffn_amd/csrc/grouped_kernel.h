@@ -1354,13 +1354,12 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         if constexpr (GU) {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * HS, (uint32_t)p.rows * a.R * HS);
             const int c0 = p.ct * TC + wn * 32;  // this wave's 32 columns of h
-            // bf16 h of row block i, turned: whole pieces of rows
+            // bf16 h of row block i: lanes exchange halves, so that each stores eight columns of a row
             auto store_h = [&](int i, f32x4 h0, f32x4 h1) {
-                *reinterpret_cast<u32x2*>(turn + er * 80 + 8 * eq) = u32x2{bf16_pair(h0[0], h0[1]), bf16_pair(h0[2], h0[3])};
-                *reinterpret_cast<u32x2*>(turn + er * 80 + 32 + 8 * eq) =
-                    u32x2{bf16_pair(h1[0], h1[1]), bf16_pair(h1[2], h1[3])};
-                const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 2) * 80 + (el & 3) * 16);
-                const int rr = (i * 2 + wm) * 16 + (el >> 2), c = c0 + (el & 3) * 8;
+                const auto lo = __builtin_amdgcn_permlane16_swap(bf16_pair(h0[0], h0[1]), bf16_pair(h1[0], h1[1]), false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(bf16_pair(h0[2], h0[3]), bf16_pair(h1[2], h1[3]), false, false);
+                const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+                const int rr = (i * 2 + wm) * 16 + er, c = c0 + (eq & 1) * 16 + (eq >> 1) * 8;
                 __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
             };
             if constexpr (I8) {
