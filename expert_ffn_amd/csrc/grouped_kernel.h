@@ -1355,12 +1355,13 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * HS, (uint32_t)p.rows * a.R * HS);
             const int c0 = p.ct * TC + wn * 32;  // this wave's 32 columns of h
             // bf16 h of row block i: lanes exchange halves, so that each stores eight columns of a row
+            const int ch = c0 + (eq & 1) * 16 + (eq >> 1) * 8;
+            const uint32_t oh = ch < a.R ? ((uint32_t)(wm * 16 + er) * a.R + ch) * 2 : kOOB;
             auto store_h = [&](int i, f32x4 h0, f32x4 h1) {
                 const auto lo = __builtin_amdgcn_permlane16_swap(bf16_pair(h0[0], h0[1]), bf16_pair(h1[0], h1[1]), false, false);
                 const auto hi = __builtin_amdgcn_permlane16_swap(bf16_pair(h0[2], h0[3]), bf16_pair(h1[2], h1[3]), false, false);
                 const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
-                const int rr = (i * 2 + wm) * 16 + er, c = c0 + (eq & 1) * 16 + (eq >> 1) * 8;
-                __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(v, ro, oh + (uint32_t)(i * 32) * a.R * 2, 0, 0);
             };
             if constexpr (I8) {
                 f32x4 sw[4];  // of the lane's columns: two blocks of gate's, two of up's
@@ -1419,6 +1420,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         max(max(lds.red[0][rr], lds.red[1][rr]), max(lds.red[2][rr], lds.red[3][rr]))));
                 };
                 // codes, two blocks of rows at a time: 32 rows of 32 bytes
+                const int cc = c0 + (el & 1) * 16;
+                const uint32_t oc = cc < a.R ? (uint32_t)(((el >> 5) * 2 + wm) * 16 + ((el >> 1) & 15)) * a.R + cc : kOOB;
 #pragma unroll
                 for (int i = 0; i < NB; i += 2) {
 #pragma unroll
@@ -1432,8 +1435,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         }
                     }
                     const u32x4 v = *reinterpret_cast<const u32x4*>(turn + (el >> 1) * 48 + (el & 1) * 16);
-                    const int rr = ((i + (el >> 5)) * 2 + wm) * 16 + ((el >> 1) & 15), c = c0 + (el & 1) * 16;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, c < a.R ? (uint32_t)rr * a.R + c : kOOB, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(v, ro, oc + (uint32_t)(i * 32) * a.R, 0, 0);
                 }
                 // scale bytes: wave column wn those of two blocks
                 const int i = wn * 2 + (el >> 4), rr = (i * 2 + wm) * 16 + er;
@@ -1449,6 +1451,8 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             const auto ro = rsrc(arg()->out + (int64_t)p.r0 * a.R * 2, (uint32_t)p.rows * a.R * 2);
             const int c0 = p.ct * TC + wn * 64;  // this wave's 64 columns, a block of O
             int byte[NB];
+            const int cd = c0 + (el & 7) * 8;
+            const uint32_t od = cd < a.R ? ((uint32_t)(wm * 16 + (el >> 3)) * a.R + cd) * 2 : kOOB;
             f32x4 sw[4];  // int8: the columns' scales times the terms' power of two
             int byte_i8 = 0;
             if constexpr (I8) {
@@ -1508,21 +1512,19 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                 for (int k = 0; k < 2; ++k) {
                     const int r = k * 8 + (el >> 3);
                     const u32x4 row = *reinterpret_cast<const u32x4*>(turn + r * 144 + (el & 7) * 16);
-                    const int rr = (i * 2 + wm) * 16 + r, c = c0 + (el & 7) * 8;
-                    __builtin_amdgcn_raw_buffer_store_b128(row, ro, c < a.R ? ((uint32_t)rr * a.R + c) * 2 : kOOB, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(row, ro, od + (uint32_t)(i * 32 + k * 8) * a.R * 2, 0, 0);
                 }
             }
             // the bytes of four row blocks at a time, a lane a row
             const int OB = (a.R + 63) / 64, ob = p.ct * (TC / 64) + wn;
             const auto rso = rsrc(arg()->outs + (int64_t)p.r0 * OB, (uint32_t)p.rows * OB);
+            const uint32_t oo = ob < OB ? (uint32_t)((eq * 2 + wm) * 16 + er) * OB + ob : kOOB;
 #pragma unroll
             for (int i = 0; i < NB; i += 4) {
                 int v = byte[i];
 #pragma unroll
                 for (int k = 1; k < 4; ++k) v = i + k < NB && eq == k ? byte[min(i + k, NB - 1)] : v;
-                const int rr = ((i + eq) * 2 + wm) * 16 + er;
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, rso, i + eq < NB && ob < OB ? (uint32_t)rr * OB + ob : kOOB,
-                                                     0, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, rso, i + eq < NB ? oo + (uint32_t)(i * 32) * OB : kOOB, 0, 0);
             }
         }
         spar ^= 1;
