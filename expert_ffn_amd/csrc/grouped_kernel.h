@@ -835,11 +835,11 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_thin(Args a) {
 //
 // What they reach, PFLOP/s: gate/up of one expert's 4096 rows of 2048 x 8192 in bf16 1.03 (a library
 // product of that size 1.15), of 2048 rows of 4096 x 4096 1.19 (1.47); of 8 experts' 2048 rows each of
-// 2048 x 4096 1.18, in e4m3 2.1.  int8, PO/s: one expert's 16384 rows of 8192 x 2048 2.60, 4096 rows of 32768 x 2048
-// 2.71, 8192 of 4096 x 4096 2.41, 65536 of 1024 x 512 1.59 (8 units a tile; a library product of 8192^3: 2.1), with the matrix
+// 2048 x 4096 1.18, in e4m3 2.1.  int8, PO/s: one expert's 16384 rows of 8192 x 2048 2.69, 4096 rows of 32768 x 2048
+// 2.79, 8192 of 4096 x 4096 2.50, 65536 of 1024 x 512 1.71 (8 units a tile; a library product of 8192^3: 2.1), with the matrix
 // units busy up to two thirds of the time at 2.0 GHz; operands that are all zero are 15 % faster, so power has a part.  What
-// a unit's reads, turns and wave priorities are changed to makes no difference that shows (int8 gate/up of 4096 tokens
-// 194-201 us).  128 experts of 2048 x 768 with 32768 skewed rows reach 0.75: 43 % of
+// a unit's reads, turns and wave priorities are changed to made no difference that showed (int8 gate/up of 4096 tokens
+// 194-201 us, now 177); branches in it do: one for most units, and one count a wait, are 3 to 5 % of e4m3 gate/up.  128 experts of 2048 x 768 with 32768 skewed rows reach 0.75: 43 % of
 // their tiles' rows are missing (a unit costs the same), each compute unit has 5 or 6 tiles, and a
 // tile's change and results, 2 of its 32 units' time at this width, are not hidden.  Tiles of 128 rows
 // instead: 366 us for 297, and 165 for 134 in 8-bit down.
