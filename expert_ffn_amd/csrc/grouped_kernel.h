@@ -657,7 +657,8 @@ __device__ __forceinline__ TileAt find_tile(const int32_t* __restrict__ offset, 
 // 36 / 37 / 40 / 43 / 51 us, one of 1408 columns 36 / 33 / 34 / 36 / 44; e4m3 gate/up with SPLIT at 1 / 2 / 3 / 4
 // 72 / 70 / 76 / 79; bf16 differs by 1-3 %.
 // int8 products need no widening, and their sums no rounding: gate/up of the 32 tokens below in 24.3 us (113 MB at
-// 4.7 TB/s), down in 14.4 (57 MB at 3.9), in e4m3 25.7 and 16.3.
+// 4.7 TB/s), down in 14.4 (57 MB at 3.9), in e4m3 25.7 and 16.3.  Units ahead: gate/up of 32 skewed tokens with 1 / 2 / 3 /
+// 4 32.1 / 32.1 / 34.4 / 34.0 us (a call), down with 2 / 3 / 4 / 6 18.8 / 18.8 / 19.2 / 20.7.
 // Memory bounds them: gate/up and down of 32 tokens (skewed over 128 bf16 experts of 2048 x 768) 49 + 27 us;
 // of one token on 8 e4m3 experts (25 + 13 MB in all) 9.4 + 6.9 us, where the latency of a launch and its first
 // loads is most.  Quantising h inside e4m3 down tiles, which spares a launch, made each of
