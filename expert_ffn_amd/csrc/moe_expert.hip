@@ -570,7 +570,6 @@ int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* 
     args.ids = ids;
     args.w = w;
     args.y = reinterpret_cast<char*>(y);
-    args.y16 = y16 ? 1 : 0;
     args.h = wsb + p.h_off;
     args.O = reinterpret_cast<float*>(wsb + p.o_off);
     args.sync = reinterpret_cast<int32_t*>(wsb + p.sync_off);
@@ -587,7 +586,7 @@ int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* 
     args.T1 = p.T1;
     args.T2 = p.T2;
     args.ks = p.ks;
-    args.accumulate = (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0;
+    args.out = ((d->flags & MOE_FLAG_ACCUMULATE) ? kYAdd : 0) | (y16 ? kYBf16 : 0);
     args.gl = p.gl;
     args.g1 = p.g1;
     args.S1 = p.S1;
