@@ -154,7 +154,7 @@ Space space_of(const moe_layer_desc* d, int32_t n) {
     }
     // gate/up's fp32 h (int8: bf16; quantised before down begins), then O
     p.hf = p.o = take(std::max(o, fp8 ? S * d->d_ff * 4 : i8 ? S * d->d_ff * 2 : 0));
-    p.os = take(S * ((d->d_model + 63) / 64));
+    p.os = take(i8 ? 0 : S * ((d->d_model + 63) / 64));
     p.h = take(S * d->d_ff * elem_size(type_of(d)));
     p.hs = take(fp8 ? S * blocks_of(d->d_ff) : i8 ? S * 4 : 0);
     p.xq = take(fp8 || i8 ? (size_t)n * d->d_model : 0);
@@ -274,7 +274,8 @@ void run_down(const moe_layer_desc* d, const Weights& w, const void* h, const ui
     const int64_t work = (int64_t)n * ((d->d_model + 511) / 512);  // waves
     hipLaunchKernelGGL((square_down(d, n) ? k_combine<false, T == kInt8> : k_combine<true>),
                        dim3((int)std::min<int64_t>((work + 3) / 4, 1 << 20)), dim3(256), 0, st,
-                       reinterpret_cast<const char*>(o), os, reinterpret_cast<const float*>(hs), row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
+                       reinterpret_cast<const char*>(o), os, reinterpret_cast<const float*>(hs), reinterpret_cast<const float*>(w.s0),
+                       T == kInt8 ? ldexpf(1.f, term_bits(d->d_ff) - 15) : 0.f, row_of, ids, rw, (int64_t)n, d->m, d->N, d->d_model,
                        (d->flags & MOE_FLAG_ACCUMULATE) ? 1 : 0, reinterpret_cast<char*>(y), u_err, info);
 }
 

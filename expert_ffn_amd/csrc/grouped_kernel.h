@@ -887,20 +887,14 @@ __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// O of square tiles: blocks of 64 columns of a row as fp16 times a power of two, which puts the block's
+// O of square tiles, bf16 and e4m3: blocks of 64 columns of a row as fp16 times a power of two, which puts the block's
 // largest into [2^14, 2^15).  `byte` is its exponent's byte in fp32, 14 at least so that 2^127 scales it.
 __device__ __forceinline__ int term_byte(uint32_t largest) { return max((int)(largest >> 23), 14); }
 
-// int8: by what the largest scale of the 64 columns could make of K codes, which needs no look at the sums, and without
-// the row's scale, which k_combine multiplies by.  |sum| <= 127^2 K < 2^b, so |sum| times the scale comes below 2^15 (at
-// byte 254 below 2^16 where it is finite in fp32); sums are whole, so a column whose scale is 2^(b - 28) of the largest or more
-// keeps 11 bits of every term, and all are right to 2^-39 of 2^b times the largest scale (2^-126 at least).  With the
-// largest term of each row as above int8 down of 4096 x 8 tokens took 142 us for 134, of 8191 x 8 236 for 220, of 2777 x 6
-// 110 for 108.
-__device__ __forceinline__ int term_byte_i8(uint32_t largest_scale, int K) {
-    const int b = 32 - __builtin_clz(127u * 127u * (uint32_t)K);
-    return min(max((int)(largest_scale >> 23) + b, 14), 254);
-}
+// int8 terms go on as whole sums times 2^(15 - b), where |sum| <= 127^2 K < 2^b: below 2^15 (with codes of -128 below 2^15.1,
+// in fp16 too), and the least, 2^(15 - 30), is a whole number of fp16's smallest steps.  So each keeps 11 bits whatever
+// the others are; the scales of its row and column meet it in k_combine.
+__host__ __device__ __forceinline__ int term_bits(int K) { return 32 - __builtin_clz(127u * 127u * (uint32_t)K); }
 
 // The largest of the four lanes l % 16 + 16 k.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
@@ -1015,7 +1009,7 @@ struct TileLds {
     char stage[2][kStage];  // rows, then weight rows
     union {
         uint8_t xs[2][4][kTM];  // e4m3: scale bytes of four units' rows, [wm][row % 16][i]
-        float scale[2][kTM];    // int8: scales of a tile's rows and weight rows (gate/up: 128 of each matrix)
+        float scale[2][kTM];    // int8 gate/up: scales of a tile's rows and weight rows (128 of each matrix)
     };
     uint32_t red[4][kTM];   // e4m3 gate/up: |h| maxima (their bits) of a row's four column groups
     char turn[8][16 * 144]; // a wave's results on their way from columns to rows
@@ -1160,13 +1154,13 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
     auto keep_weight_scale = [&](int par, int i, uint8_t v) {
         if (i < 2 * KB) lds.ws[par][i >= KB][i >= KB ? i - KB : i] = v;
     };
-    // int8: a scale a thread, gate/up those of the tile's rows, then of its weight rows, down of its weight rows.  (At a
-    // tile's first unit lds.token still has its own tokens.)
+    // int8 gate/up: a scale a thread, those of the tile's rows, then of its weight rows.  (At a tile's first unit lds.token
+    // still has its own tokens.)
     auto tile_scale = [&](const Place& t) {
-        const int c = tid & (kTM - 1), half = GU ? c >> 7 : 0;
-        const float *s0 = reinterpret_cast<const float*>(arg()->s0), *s1 = GU ? reinterpret_cast<const float*>(arg()->s1) : s0;
-        const float* at = (half ? s1 : s0) + ((int64_t)t.e * a.R + min(t.ct * TC + (GU ? c & 127 : c), a.R - 1));
-        if (GU && tid < kTM) at = reinterpret_cast<const float*>(arg()->xs) + lds.token[c];
+        const int c = tid & (kTM - 1);
+        const float *s0 = reinterpret_cast<const float*>(arg()->s0), *s1 = reinterpret_cast<const float*>(arg()->s1);
+        const float* at = (c >> 7 ? s1 : s0) + ((int64_t)t.e * a.R + min(t.ct * TC + (c & 127), a.R - 1));
+        if (tid < kTM) at = reinterpret_cast<const float*>(arg()->xs) + lds.token[c];
         return *at;
     };
     const int sxat = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + ((tid >> 5) & 7);
@@ -1215,7 +1209,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
         for (int i = 0; i < NB; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = Sum4<T>{0, 0, 0, 0};
-        float scale = 0.f;  // int8: one of the tile's, on its way to shared memory
+        float scale = 0.f;  // int8 gate/up: one of the tile's, on its way to shared memory
         for (int u = 0; u < U; ++u) {
             char* here = lds.stage[par];
             char* there = lds.stage[par ^ 1];
@@ -1296,13 +1290,13 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                         wsn[0] = weight_scale(pn, tid);
                         if (KB > kTileThreads / 2) wsn[1] = weight_scale(pn, tid + kTileThreads);
                     }
-                    if (I8) scale = tile_scale(p);
+                    if (I8 && GU) scale = tile_scale(p);
                 } else if (u == 1) {
                     if (FP8) {
                         keep_weight_scale(spar ^ 1, tid, wsn[0]);
                         if (KB > kTileThreads / 2) keep_weight_scale(spar ^ 1, tid + kTileThreads, wsn[1]);
                     }
-                    if (I8) lds.scale[tid / kTM][tid & (kTM - 1)] = scale;  // (read at the tile's end, long before the next's)
+                    if (I8 && GU) lds.scale[tid / kTM][tid & (kTM - 1)] = scale;  // (read at the tile's end, long before the next's)
                     if (GU) keep(slot_n);
                     if (tid == 0) lds.after = got + 2 * step;
                 } else if (ub == U) {
@@ -1454,33 +1448,18 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
             int byte[NB];
             const int cd = c0 + (el & 7) * 8;
             const uint32_t od = cd < a.R ? ((uint32_t)(wm * 16 + (el >> 3)) * a.R + cd) * 2 : kOOB;
-            f32x4 sw[4];  // int8: the columns' scales times the terms' power of two
-            int byte_i8 = 0;
-            if constexpr (I8) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sw[j] = *reinterpret_cast<const f32x4*>(&lds.scale[1][wn * 64 + j * 16 + 4 * eq]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(mag(sw[j][k])));
-                }
-                byte_i8 = term_byte_i8(quad_max(m), a.K);
-                const float inv = __uint_as_float((uint32_t)(268 - byte_i8) << 23);  // 2^(141 - byte)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sw[j] *= inv;
-            }
+            const float unit = I8 ? pow2(15 - term_bits(a.K)) : 0.f;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 auto keep16 = [&](int j, const float (&o)[4]) {
                     *reinterpret_cast<u32x2*>(turn + er * 144 + j * 32 + 8 * eq) = u32x2{f16_pair(o[0], o[1]), f16_pair(o[2], o[3])};
                 };
                 if constexpr (I8) {
-                    byte[i] = byte_i8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float o[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[k] = (float)acc[i][j][k] * sw[j][k];
+                        for (int k = 0; k < 4; ++k) o[k] = (float)acc[i][j][k] * unit;
                         keep16(j, o);
                     }
                 } else {
@@ -1516,16 +1495,18 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(Args a) {
                     __builtin_amdgcn_raw_buffer_store_b128(row, ro, od + (uint32_t)(i * 32 + k * 8) * a.R * 2, 0, 0);
                 }
             }
-            // the bytes of four row blocks at a time, a lane a row
-            const int OB = (a.R + 63) / 64, ob = p.ct * (TC / 64) + wn;
-            const auto rso = rsrc(arg()->outs + (int64_t)p.r0 * OB, (uint32_t)p.rows * OB);
-            const uint32_t oo = ob < OB ? (uint32_t)((eq * 2 + wm) * 16 + er) * OB + ob : kOOB;
+            if constexpr (!I8) {
+                // the bytes of four row blocks at a time, a lane a row
+                const int OB = (a.R + 63) / 64, ob = p.ct * (TC / 64) + wn;
+                const auto rso = rsrc(arg()->outs + (int64_t)p.r0 * OB, (uint32_t)p.rows * OB);
+                const uint32_t oo = ob < OB ? (uint32_t)((eq * 2 + wm) * 16 + er) * OB + ob : kOOB;
 #pragma unroll
-            for (int i = 0; i < NB; i += 4) {
-                int v = byte[i];
+                for (int i = 0; i < NB; i += 4) {
+                    int v = byte[i];
 #pragma unroll
-                for (int k = 1; k < 4; ++k) v = i + k < NB && eq == k ? byte[min(i + k, NB - 1)] : v;
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, rso, i + eq < NB ? oo + (uint32_t)(i * 32) * OB : kOOB, 0, 0);
+                    for (int k = 1; k < 4; ++k) v = i + k < NB && eq == k ? byte[min(i + k, NB - 1)] : v;
+                    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, rso, i + eq < NB ? oo + (uint32_t)(i * 32) * OB : kOOB, 0, 0);
+                }
             }
         }
         spar ^= 1;
@@ -1575,11 +1556,15 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 // The error of y in that bf16 down is 0.0023 (norm) with bf16 terms and 0.0017 here, that of rounding y.
 // (Long passes whose contraction is too short for square tiles pay for fp32: down of 4096 x 8 tokens of 16
 // experts, 1024 x 176 in bf16, 128 -> 136 us, 1024 x 368 in e4m3 142 -> 153.)
-// What is not finite is itself in fp16 and takes no part in a block's largest.  ROWS (int8): O still lacks its row's `scale`.
+// What is not finite is itself in fp16 and takes no part in a block's largest.
+// I8: O is whole sums times 1 / `unit` (term_bits), still without its row's scale `rs` and its expert's columns' `cs` [N][d],
+// which are read here again for every slot (from the caches: 1 MB for 128 experts of 2048) instead of a power of two for 64
+// columns: int8 down of 2777 x 6 tokens 103 us for 103, pass of 8191 x 8 494-505 for 491-497, and every term has its 11
+// bits, also beside columns of far larger scales.
 // info (may be null): U, ids status, MOE_OK.
-template <bool F32, bool ROWS = false>
+template <bool F32, bool I8 = false>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const uint8_t* __restrict__ os,
-                                                const float* __restrict__ scale,
+                                                const float* __restrict__ rs, const float* __restrict__ cs, float unit,
                                                 const int32_t* __restrict__ row_of,
                                                 const int32_t* __restrict__ ids, const float* __restrict__ w, int64_t n,
                                                 int m, int N, int d,
@@ -1596,18 +1581,21 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
         for (int k = 0; k < 8; ++k) s[k] = 0.f;
         for (int j0 = 0; j0 < m; j0 += 64) {
             // this lane's slot: its row (-1: none) and weight
-            int row = -1;
+            int row = -1, e = 0;
             float wj = 0.f, sj = 0.f;
             if (j0 + lane < m) {
                 const int64_t slot = t * m + j0 + lane;
                 const int id = ids[slot], r = min(max(row_of[slot], 0), last);
                 wj = w[slot];
                 row = id >= 0 && id < N ? r : -1;
-                if (ROWS) sj = scale[r];
+                if (I8) {
+                    e = row >= 0 ? id : 0;
+                    sj = rs[r];
+                }
             }
             uint64_t live = __ballot(row >= 0);
             while (live) {
-                u32x4 o[8][F32 ? 2 : 1];
+                u32x4 o[8][F32 ? 2 : 1], sw[8][2];
                 float wt[8], sx[8];
                 int rows8 = 0;  // of lane 8 k + b: row k of the eight
 #pragma unroll
@@ -1616,25 +1604,32 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                     live &= live - 1;
 #pragma unroll
                     for (auto& p : o[k]) p = u32x4{0u, 0u, 0u, 0u};
+                    if constexpr (I8) sw[k][0] = sw[k][1] = u32x4{0u, 0u, 0u, 0u};
                     wt[k] = sx[k] = 0.f;
                     if (l < 64) {
                         const int64_t r = __builtin_amdgcn_readlane(row, l);
                         wt[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(wj), l));
-                        if (ROWS) sx[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(sj), l));
+                        if constexpr (I8) {
+                            sx[k] = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(sj), l));
+                            const int64_t ek = __builtin_amdgcn_readlane(e, l);
+                            typedef u32x4 __attribute__((aligned(4))) u32x4_a4;  // (of floats, wherever they begin)
+                            const u32x4_a4* sc = reinterpret_cast<const u32x4_a4*>(cs + ek * d + c);
+                            if (in) sw[k][0] = sc[0], sw[k][1] = sc[1];
+                        }
                         const u32x4* at = reinterpret_cast<const u32x4*>(O + (r * d + c) * (F32 ? 4 : 2));
                         if (in) o[k][0] = at[0];
                         if constexpr (F32) {
                             if (in) o[k][1] = at[1];
-                        } else {
+                        } else if constexpr (!I8) {
                             rows8 = lane >> 3 == k ? (int)r : rows8;
                         }
                     }
                 }
                 int byte = 0;
-                if (!F32) byte = os[(int64_t)rows8 * OB + min((c0 >> 6) + (lane & 7), OB - 1)];
+                if (!F32 && !I8) byte = os[(int64_t)rows8 * OB + min((c0 >> 6) + (lane & 7), OB - 1)];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float f = F32 ? 1.f : pow2(__shfl(byte, k * 8 + (lane >> 3), 64) - 141);
+                    const float f = F32 ? 1.f : I8 ? unit : pow2(__shfl(byte, k * 8 + (lane >> 3), 64) - 141);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         if constexpr (F32) {
@@ -1642,9 +1637,12 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                             s[4 + v] += wt[k] * __uint_as_float(o[k][1][v]);
                         } else {
                             const f32x2 t2 = f16_values(o[k][0][v]);
-                            const float o0 = t2[0] * f, o1 = t2[1] * f;
-                            s[2 * v] += wt[k] * (ROWS ? o0 * sx[k] : o0);
-                            s[2 * v + 1] += wt[k] * (ROWS ? o1 * sx[k] : o1);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float o0 = t2[i] * f;
+                                if constexpr (I8) o0 = o0 * __uint_as_float(sw[k][v >> 1][(2 * v + i) & 3]) * sx[k];
+                                s[2 * v + i] += wt[k] * o0;
+                            }
                         }
                     }
                 }

@@ -353,12 +353,11 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
  * for h with 8-bit weights, the quantisation below.  The two kinds of tiles that the products
  * run on differ in their arithmetic.  Thin tiles (passes of few rows an expert) keep the terms
  * W_down h in fp32, so that y is rounded once.  Square tiles (from 8 to 16 rows an expert on average,
- * by type and size, int8 in small layers later: moe_grouped_square) hand them on in 11 bits: each term is off by up to 2^-11 |w_tj W_down h|
- * (and 2^-39 of the largest of its 64 columns; int8: of 2^b times the row's scale and their largest, 2^-126 at least, with
- * 127^2 d_ff < 2^b), whatever is left of their sum.  e4m3 products on square tiles
- * go through a matrix instruction that cuts each product to 2^-13 of the largest of its 8 neighbours along the
- * contraction (which is small beside the 2^-4 of an operand's own quantisation); thin tiles do not cut,
- * and int8 products add whole numbers.  Results are deterministic.
+ * by type and size, int8 in small layers later: moe_grouped_square) hand them on in 11 bits: each term is off by up
+ * to 2^-11 |w_tj W_down h| (bf16 and e4m3: and 2^-39 of the largest of its 64 columns), whatever is left of their sum.
+ * e4m3 products on square tiles go through a matrix instruction that cuts each product to 2^-13 of the largest of
+ * its 8 neighbours along the contraction (which is small beside the 2^-4 of an operand's own quantisation); thin tiles
+ * do not cut, and int8 products add whole numbers.  Results are deterministic.
  *
  * Limits: 1 <= m <= N <= MOE_MAX_EXPERTS, m <= MOE_MAX_SLOTS, n*m <=
  * MOE_MAX_GROUP_SLOTS, d_model and d_ff <= MOE_MAX_GROUP_WIDTH, multiples of 8 (bf16)
