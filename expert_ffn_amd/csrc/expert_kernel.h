@@ -239,8 +239,9 @@ __device__ __forceinline__ int atomic_load_agent(const int32_t* p) {
 // Args::out.  (One word: with y's type in a word of its own, which moved the arguments behind it and took two more
 // scalar registers to the stack, passes of 1..8 tokens through 48 layers of 128 experts of 2048 x 768, each length by both
 // kernels, took 32.20 ms for 31.98 without a choice of y's type; this way 32.09 for 32.06 on another box.)
-constexpr int kYAdd = 1;   // to what is there
-constexpr int kYBf16 = 2;  // rounded to bf16
+constexpr int kYAdd = 1;    // to what is there
+constexpr int kYLayer = 2;  // of a whole layer: NaN for a token whose first id is not valid (no expert was left to take)
+constexpr int kYBf16 = 4;   // (with kYLayer) rounded to bf16
 
 struct Args {
     const char* wg;      // W_gate [N][d_ff][d] (or tiled)
@@ -981,19 +982,22 @@ __device__ __forceinline__ void down_work(const Args& a, Smem<NT * RB>& sm, int&
                         for (int r = 0; r < 4; ++r) acc[r] = fmaf(wv[jj], __uint_as_float(ov[jj][r]), acc[r]);
             }
             const size_t at = (size_t)tok * a.d + i;
-            if (a.out & kYBf16) {
-                u32x2* yp = reinterpret_cast<u32x2*>(a.y + at * 2);
-                if (a.out & kYAdd) {
-                    const u32x2 v = *yp;
-                    acc += f32x4{bf16_to_f32(v.x & 0xffffu), bf16_to_f32(v.x >> 16), bf16_to_f32(v.y & 0xffffu),
-                                 bf16_to_f32(v.y >> 16)};
+            if (__builtin_expect(a.out > kYAdd, 0)) {  // (a layer's pass)
+                if (!sm.cok[tok * a.m]) acc = f32x4{NAN, NAN, NAN, NAN};
+                if (a.out & kYBf16) {
+                    u32x2* yp = reinterpret_cast<u32x2*>(a.y + at * 2);
+                    if (a.out & kYAdd) {
+                        const u32x2 v = *yp;
+                        acc += f32x4{bf16_to_f32(v.x & 0xffffu), bf16_to_f32(v.x >> 16), bf16_to_f32(v.y & 0xffffu),
+                                     bf16_to_f32(v.y >> 16)};
+                    }
+                    *yp = u32x2{bf16_rne(acc[0]) | (bf16_rne(acc[1]) << 16), bf16_rne(acc[2]) | (bf16_rne(acc[3]) << 16)};
+                    continue;
                 }
-                *yp = u32x2{bf16_rne(acc[0]) | (bf16_rne(acc[1]) << 16), bf16_rne(acc[2]) | (bf16_rne(acc[3]) << 16)};
-            } else {
-                f32x4* yp = reinterpret_cast<f32x4*>(a.y + at * 4);
-                if (a.out & kYAdd) acc += *yp;  // y is read only when the call accumulates
-                *yp = acc;
             }
+            f32x4* yp = reinterpret_cast<f32x4*>(a.y + at * 4);
+            if (a.out & kYAdd) acc += *yp;  // y is read only when the call accumulates
+            *yp = acc;
         }
     }
 }

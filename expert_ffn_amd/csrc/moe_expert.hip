@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256) void k_zero_words(int32_t* __restrict__ p, int
 template <int MODE>
 int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* x, const int32_t* ids,
                const float* w, int32_t n, void* y, int32_t* info, void* ws, size_t ws_bytes, void* stream,
-               void* const* events, int32_t n_events, bool clear_counters = false, bool y16 = false) {
+               void* const* events, int32_t n_events, bool clear_counters = false, int out = 0) {
     int rc = check_desc(d, n);
     if (rc != MOE_OK) return rc;
     if (!W || !W->w_gate || !W->w_up || !W->w_down || !x || !ids || !w || !y || !ws) return MOE_E_INVAL;
@@ -586,7 +586,7 @@ int run_expert(const moe_layer_desc* d, const moe_layer_weights* W, const void* 
     args.T1 = p.T1;
     args.T2 = p.T2;
     args.ks = p.ks;
-    args.out = ((d->flags & MOE_FLAG_ACCUMULATE) ? kYAdd : 0) | (y16 ? kYBf16 : 0);
+    args.out = ((d->flags & MOE_FLAG_ACCUMULATE) ? kYAdd : 0) | out;
     args.gl = p.gl;
     args.g1 = p.g1;
     args.S1 = p.S1;
@@ -941,10 +941,11 @@ int moe_layer_pass(const moe_layer_desc* desc, const moe_layer_weights* weights,
                                         : (bf ? k_route<true, 16> : k_route<false, 16>);
     hipLaunchKernelGGL(route, grid, dim3(kRouteThreads), 0, st, a);
     if (hipGetLastError() != hipSuccess) return MOE_E_HIP;
+    const int out = kYLayer | (bf ? kYBf16 : 0);
     return kind == MOE_KIND_DEDUP ? run_expert<kDedup>(desc, weights, x, a.ids, a.w, n, y, info, b + p.expert, expert_bytes,
-                                                       hip_stream, nullptr, 0, false, bf)
+                                                       hip_stream, nullptr, 0, false, out)
                                   : run_expert<kPerSlot>(desc, weights, x, a.ids, a.w, n, y, info, b + p.expert,
-                                                         expert_bytes, hip_stream, nullptr, 0, false, bf);
+                                                         expert_bytes, hip_stream, nullptr, 0, false, out);
 }
 
 }  // extern "C"

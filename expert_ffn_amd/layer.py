@@ -54,7 +54,8 @@ def layer_pass(layer, router, x, y=None, ids=None, w=None, info=None, ws=None, a
     """y [n][d] of the layer for x [n][d], both of the layer's type (``moe_layer_pass``): at
     most 64 tokens and 256 slots.  ``ids`` int32 [n][m] and ``w`` float32 [n][m] receive the
     routing where given, ``info`` int32 [3] U, ids status and sync status; ``ws`` comes
-    from ``pass_workspace`` (one call at a time).  Runs on ``stream`` (default: the current
+    from ``pass_workspace`` (one call at a time).  A token all of whose logits are NaN gets ids -1,
+    weights 0 and a y of NaN.  Runs on ``stream`` (default: the current
     stream of the layer's device)."""
     dev = _check_layer(layer)
     if not isinstance(router, Router):

@@ -319,8 +319,9 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  *   info     device [3] int32 or NULL, as for moe_expert_perslot
  *   ws       device workspace of at least moe_pass_workspace_bytes(desc, n), 256-byte aligned, zero-filled before
  *            first use, as for the expert calls; one sized for n serves fewer tokens too
- * Logits should be finite.  One that is NaN takes no part: its expert is never selected, and not in the softmax's sum; a slot left
- * without a candidate gets id -1 and weight 0 (info[1] is then MOE_E_IDS).
+ * Logits should be finite.  One that is NaN takes no part: its expert is never selected, and not in the softmax's sum; a
+ * slot left without a candidate gets id -1 and weight 0 (info[1] is then MOE_E_IDS).  A token all of whose logits are NaN
+ * (an x of NaN) has no expert at all: its y is NaN.
  * Returns MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE (nothing enqueued), or MOE_E_HIP.
  */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
