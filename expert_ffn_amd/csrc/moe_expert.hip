@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void k_router_topm(const float* __restric
     part_sum = __shfl(part_sum, 0, 64);  // one denominator for every lane
     for (int j = lane; j < m; j += 64) {
         ids[(size_t)t * m + j] = seli[wave][j];
-        w[(size_t)t * m + j] = expf(selv[wave][j] - top) / part_sum;
+        w[(size_t)t * m + j] = seli[wave][j] < 0 ? 0.f : expf(selv[wave][j] - top) / part_sum;
     }
 }
 
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(kThreads) void k_router_topm(const float* __restric
 // tokens loads their logits (the KS parts added in order, written out) into LDS and
 // ranks every (token, expert) by the number of experts that come before it (larger
 // logit, or equal logit and lower id): the rank is the expert's position, so the
-// ranks below m are the selection, in order.  One wave per token then takes the
+// ranks below m are the selection, in order.  (A NaN logit has no rank, and comes
+// before none; places that no expert has keep id -1.)  One wave per token then takes the
 // softmax of the selected logits.  No rounds: the cost does not grow with m.
 constexpr int kRRW = 16;                 // waves of the ranking workgroup
 constexpr int kRRMaxN = 256, kRRMaxM = 64;
@@ -186,6 +187,10 @@ __global__ __launch_bounds__(64 * kRRW) void k_router_rank(const float* __restri
     const int t0 = blockIdx.x * kTile;
     const int nt = min(kTile, n - t0);
     const auto rp = rsrc(part, (uint32_t)KS * n * N * 4);
+    for (int i = tid; i < kTile * kRRMaxM; i += 64 * kRRW) {
+        selv[i / kRRMaxM][i % kRRMaxM] = -INFINITY;
+        seli[i / kRRMaxM][i % kRRMaxM] = -1;
+    }
     for (int it = tid; it < nt * N; it += 64 * kRRW) {
         const int t = it / N, e = it - t * N;
         float pv[kRKS];  // every part's load in flight, then the sum in part order
@@ -206,7 +211,7 @@ __global__ __launch_bounds__(64 * kRRW) void k_router_rank(const float* __restri
         const float v = lgt[t][e];
         int rank = 0;
         for (int k = 0; k < N; ++k) rank += rk_before(lgt[t][k], k, v, e) ? 1 : 0;
-        if (rank < m) {
+        if (v == v && rank < m) {
             selv[t][rank] = v;
             seli[t][rank] = e;
         }
@@ -221,7 +226,7 @@ __global__ __launch_bounds__(64 * kRRW) void k_router_rank(const float* __restri
         sum = __shfl(sum, 0, 64);
         if (lane < m) {
             ids[(size_t)(t0 + t) * m + lane] = seli[t][lane];
-            w[(size_t)(t0 + t) * m + lane] = expf(selv[t][lane] - top) / sum;
+            w[(size_t)(t0 + t) * m + lane] = seli[t][lane] < 0 ? 0.f : expf(selv[t][lane] - top) / sum;
         }
     }
 }

@@ -285,8 +285,8 @@ int moe_pack_tiled(const moe_layer_desc* desc, const void* w, void* w_tiled, int
  *             4-byte aligned: partial logits of up to 16 parts of the d contraction,
  *             added in a fixed order (no zero-fill needed)
  * Logits should be finite: NaN logits are never selected, and a slot left without
- * a candidate gets id -1 (which the expert calls skip).  Two kernel launches on
- * hip_stream, deterministic.
+ * a candidate gets id -1 (which the expert calls skip) and weight 0.  Two kernel
+ * launches on hip_stream, deterministic.
  * Returns MOE_OK, MOE_E_INVAL / MOE_E_DTYPE / MOE_E_WORKSPACE for bad arguments
  * (nothing enqueued), or MOE_E_HIP.
  */
