@@ -7,14 +7,16 @@
 // One work group of 16 waves for 16 experts x 4 tokens x one of KS parts of the contraction; its waves split
 // the part, so that at d = 2048 in bf16 each has one step: one round of loads.  The parts go to memory, and the work
 // group that arrives last on a token tile adds them, in order, and selects: a wave a token, m rounds of a
-// wave-wide maximum; or, of few tokens, by rank (an expert's place is the number of those before it), all
+// wave-wide maximum; or, of many experts a token, by rank (an expert's place is the number of those before it), all
 // threads together.  How the contraction is cut depends on N, d and the type alone, so a token's routing does not
 // depend on the pass that it is in.
 //
-// Latency is the time: one token on 128 experts of d = 2048 takes 6.3 us, of which logits and arrival are 4.5 (a launch,
-// a round of loads, a store, an atomic); 32 tokens 9.0, with 16 tokens a work group, where four waves a SIMD select,
+// Latency is the time: one token on 128 experts of d = 2048 takes 6.3-7.0 us, of which logits and arrival are 4.5 (a launch,
+// a round of loads, a store, an atomic); 32 tokens 7.6-9.0, with 16 tokens a work group, where four waves a SIMD select,
 // 10.2.  The two launches of moe_router_topk are 7.3 for one token.  Half or a quarter of the parts: no difference for one
-// token, 0.9 and 2.2 us more for 32.
+// token, 0.9 and 2.2 us more for 32.  Of 1 / 5 / 32 tokens, 8 experts each: 64 experts 6.4 / 6.6 / 7.0 us, 128 7.0 / 7.4 / 7.6,
+// 256 7.6 / 8.4 / 11.8, 384 14.0 / 17.2 / 23.8, 1024 15.9 / 22.2 / 42.  Beyond 256 a lane holds 16 experts, and their parts
+// of 8 in flight do not fit 128 registers: 32 of them go to the stack.
 #pragma once
 
 #include "expert_kernel.h"
@@ -23,12 +25,25 @@ namespace moe_k {
 
 constexpr int kRouteWaves = 16, kRouteThreads = 64 * kRouteWaves;
 constexpr int kRouteParts = 8;  // most parts of the contraction
-// Selection by rank for tiles of up to so many (token, expert) pairs: its work grows with tokens N^2 and all of the work
-// group shares it.  The launch by rank and by rounds at N = 128: one token 6.9 / 7.6 us, 5 tokens 11.1 / 8.9, 16 18.2 / 11.4
-// (with rounds slower than now).
-constexpr int kRankMost = 256;
 // Tokens of a work group: a quarter of the matrix operand's columns, so that the waves that select have a SIMD each.
 constexpr int kRouteTokens = 4;
+// Selection by rank, not by rounds, of the m experts of each of nt tokens, NK places for experts a token.  A round is 0.07
+// (64 places) to 0.17 us (256); by rank m costs nothing, but nt NK^2 comparisons are shared by the work group.  The launch by rank /
+// by rounds in us, d = 2048 in bf16:
+//              nt   m = 4        8            12           16           32           64
+//     N =  64   1                6.1 / 6.5    6.3 / 6.6    6.1 / 7.0    6.1 / 8.6    6.1 / 11.8
+//               4                6.9 / 6.6    6.8 / 6.9    7.0 / 7.4    6.6 / 9.0    7.0 / 12.3
+//     N = 128   1   6.8 / 5.9    6.8 / 6.8    6.8 / 7.5    6.9 / 8.2    6.7 / 10.3   6.7 / 15.1
+//               2   7.3 / 6.2    7.5 / 7.1    7.5 / 7.7    7.5 / 8.3    7.5 / 10.6   7.3 / 15.2
+//               4   8.7 / 6.6    8.9 / 7.4    9.0 / 8.0    8.8 / 8.5    8.7 / 10.8   8.9 / 15.7
+//     N = 256   1                8.9 / 7.4    9.1 / 8.3    9.1 / 8.9    9.1 / 11.5   9.2 / 17.0
+//               2               11.5 / 8.0   11.5 / 8.6   11.6 / 9.5   11.3 / 11.7  11.2 / 17.0
+//               4               16.3 / 8.3   16.2 / 8.8   16.2 / 9.6   16.3 / 12.2  16.0 / 17.3
+// With more places by rounds alone (1024, one token, m = 8 / 64: by rank 49 / 49, by rounds 16 / 34).
+constexpr int kRankPlaces = 256;
+__device__ __forceinline__ bool by_rank(int nt, int NK, int m) {
+    return NK <= kRankPlaces && m > max(8, 4 + nt * NK * NK / 5120);
+}
 
 struct RouteArgs {
     const char* wr;     // [N][d]
@@ -111,9 +126,9 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     __shared__ int sel_e[kRouteTokens][MOE_MAX_SLOTS];
     __shared__ float sel_l[kRouteTokens][MOE_MAX_SLOTS];
     __shared__ int s_last;
-    constexpr int NK = 64 * CL;
-    __shared__ __align__(16) uint32_t s_key[kRankMost];
-    __shared__ float s_l[kRankMost];
+    constexpr int NK = 64 * CL, kPairs = NK <= kRankPlaces ? kRouteTokens * NK : 4;
+    __shared__ __align__(16) uint32_t s_key[kPairs];
+    __shared__ float s_l[kPairs];
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int lr = lane & 15, q = lane >> 4;
     const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kRouteTokens, ks = blockIdx.z, KS = a.KS;
@@ -166,7 +181,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a) {
     if (!s_last) return;
     const int t = t0 + wave;  // this wave's token
     const bool live = wave < nt;
-    const bool rank = nt * NK <= kRankMost;
+    const bool rank = by_rank(nt, NK, a.m);
     if (!rank && !live) return;  // (by rounds there is no barrier)
     int* se = sel_e[live ? wave : 0];
     float* sl = sel_l[live ? wave : 0];

@@ -33,3 +33,24 @@ def test_ids_and_weights(N, m, d, typ):
             wt = torch.full((n, m), 7.0, device="cuda")
             efa.layer_pass(layer, efa.Router(w.to(typ).cuda(), **dev), x.to(typ).cuda(), ids=ids, w=wt, ws=ws)
             check(ids, wt, l, m, **f)
+
+
+@pytest.mark.parametrize("N", [16, 63, 64, 65, 128, 129, 256])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 6])
+def test_selection_of_any_number(N, n):
+    """By rounds or by rank, as the number of experts to take, the tokens and the experts have it."""
+    zero = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")  # noqa: E731
+    W = (zero(N, 8, 1024), zero(N, 8, 1024), zero(N, 1024, 8))
+    for m in (1, 7, 8, 9, 12, 13, 16, 17, 18, 30, 31, 42, 43, 55, 56, 64, 65, 128, 256):
+        if m > N or n * m > 256:
+            continue
+        layer = efa.Layer(*W, m=m)
+        for i in (0, 2, 3):
+            say("layer selection", N, n, m, i)
+            f = form(i, N)
+            x, w, l = problem(N, 1024, n, 10 * i + n)
+            dev = dict(f, bias=f["bias"].cuda()) if "bias" in f else f
+            ids = torch.full((n, m), -7, dtype=torch.int32, device="cuda")
+            wt = torch.full((n, m), 7.0, device="cuda")
+            efa.layer_pass(layer, efa.Router(w.to(BF).cuda(), **dev), x.to(BF).cuda(), ids=ids, w=wt)
+            check(ids, wt, l, m, **f)
