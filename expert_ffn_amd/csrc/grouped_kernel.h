@@ -1559,8 +1559,8 @@ __global__ __launch_bounds__(256) void k_row_of(const int32_t* __restrict__ slot
 // What is not finite is itself in fp16 and takes no part in a block's largest.
 // I8: O is whole sums times 1 / `unit` (term_bits), still without its row's scale `rs` and its expert's columns' `cs` [N][d],
 // which are read here again for every slot (from the caches: 1 MB for 128 experts of 2048) instead of a power of two for 64
-// columns: int8 down of 2777 x 6 tokens 103 us for 103, pass of 8191 x 8 494-505 for 491-497, and every term has its 11
-// bits, also beside columns of far larger scales.
+// columns.  This launch takes more (8191 x 8 tokens 76 us for 53, 2777 x 6 16 for 15) and the tiles before it, which need no
+// scales, less (169 for 185, 77 for 83); and every term has its 11 bits, also beside columns of far larger scales.
 // info (may be null): U, ids status, MOE_OK.
 template <bool F32, bool I8 = false>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, const uint8_t* __restrict__ os,
@@ -1570,6 +1570,8 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                                                 int m, int N, int d,
                                                 int accumulate, char* __restrict__ y, const int32_t* __restrict__ u_err,
                                                 int32_t* __restrict__ info) {
+    // slots whose loads are in flight together (int8 with 8: wide pass 21 us for 15, 2777 x 6 18 for 16, 8191 x 8 equal)
+    constexpr int B = I8 ? 4 : 8;
     const int lane = threadIdx.x & 63, CW = (d + 511) / 512, OB = (d + 63) / 64, last = (int)(n * m) - 1;
     if (info && blockIdx.x == 0 && threadIdx.x < 3) info[threadIdx.x] = threadIdx.x < 2 ? u_err[threadIdx.x] : MOE_OK;
     for (int64_t i = (int64_t)blockIdx.x * 4 + uni(threadIdx.x >> 6); i < n * CW; i += (int64_t)gridDim.x * 4) {
@@ -1595,11 +1597,11 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
             }
             uint64_t live = __ballot(row >= 0);
             while (live) {
-                u32x4 o[8][F32 ? 2 : 1], sw[8][2];
-                float wt[8], sx[8];
+                u32x4 o[B][F32 ? 2 : 1], sw[B][2];
+                float wt[B], sx[B];
                 int rows8 = 0;  // of lane 8 k + b: row k of the eight
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < B; ++k) {
                     const int l = live ? __ffsll((unsigned long long)live) - 1 : 64;
                     live &= live - 1;
 #pragma unroll
@@ -1628,7 +1630,7 @@ __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ O, con
                 int byte = 0;
                 if (!F32 && !I8) byte = os[(int64_t)rows8 * OB + min((c0 >> 6) + (lane & 7), OB - 1)];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < B; ++k) {
                     const float f = F32 ? 1.f : I8 ? unit : pow2(__shfl(byte, k * 8 + (lane >> 3), 64) - 141);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {

@@ -4,7 +4,7 @@
 // latency of 2.5 us and more: one token on 8 of 128 experts of 2048 x 768 takes 24 us, of which the 38 MB of its
 // codes are 8.  Here every work group groups the slots itself (a lane a slot, ten ballots) and quantises the rows
 // that it needs, while its first weights are on their way; the tokens' sums are formed where the down products are:
-// 14.4 us, 8.6 and 5.8, of which 5 are two launches.  The arithmetic is that of the grouped calls, bit for bit: sums of
+// 14.7 us, 8.1-8.8 and 6.0-6.4, of which 5 are two launches.  The arithmetic is that of the grouped calls, bit for bit: sums of
 // codes are whole numbers, so a contraction may be cut anywhere, and the rest is done in the same order.
 #pragma once
 
