@@ -310,7 +310,7 @@ size_t moe_router_workspace_bytes(const moe_layer_desc* desc, int32_t n);
  *   y_t  = sum_j w_tj FFN_tj(x_t) + sum over the shared experts of FFN(x_t)
  * with the expert calls' FFN and order of the sums: y is what moe_expert_dedup (or, for one token without
  * shared experts, moe_expert_perslot) gives for the ids and weights that the call hands back, rounded once more where
- * the layer is bf16.  A token's ids and weights do not depend on the other tokens of the pass.  (moe_router_topk sums
+ * the layer is bf16 (a token without any expert aside, see below).  A token's ids and weights do not depend on the other tokens of the pass.  (moe_router_topk sums
  * its logits in another order: two experts within its fp32 error of each other may change places.)
  *   desc     as for the expert calls (fp32 or bf16; every weight layout; n_shared; accumulate: y = round(y + result));
  *            N * d_model * element size < 2^31
